@@ -370,6 +370,99 @@ moe_status moe_forward_marked(const moe_desc* desc, const void* x,
                               void* ws, size_t ws_bytes, hipEvent_t* marks,
                               hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit integer products with one scale per token and per output channel
+ * ("Under The Hood: Inkling", quantization: the experts' matrices in few bits;
+ * here int8 for weights and activations, beside MXFP4's weights only).
+ *
+ * Codes: a row of K values becomes q_k = round(127 x_k / max|x|), ties to
+ * even, of exact arithmetic, and the scale s = max|x| / 127 (fp32), so that
+ * x_k ~ s q_k.  Activations are quantised per token (row of x), weights per
+ * output channel (row of an [out, in] matrix).  A row of codes is padded with
+ * zeros to Kp = K rounded up to 128.  A row of zeros has scale 0; a row that
+ * holds a NaN or an infinity has codes 0 and scale NaN (the products of that
+ * row are NaN, no others are).
+ *
+ * moe_quantize_int8: x [rows, K] (MOE_F32 or MOE_BF16, dense, aligned to its
+ * element) -> codes [rows, Kp] (16-byte aligned), scales [rows].  rows >= 0,
+ * 1 <= K <= 131072; rows up to 2^31 - 1.  No workspace. */
+moe_status moe_quantize_int8(int64_t rows, int32_t K, moe_dtype dtype, const void* x,
+                             int8_t* codes, float* scales, hipStream_t stream);
+
+/* Grouped product: y[m, n] = a_scale[m] w_scale[e, n] sum_k a[m, k] w[e, n, k]
+ * for the rows m of group e, offsets[e] <= m < offsets[e+1]; the sum is exact
+ * (int32), scaled in fp32 and rounded once to `out` (MOE_F32 or MOE_BF16).
+ *   a [M, Kp], a_scale [M], w [E, N, Kp], w_scale [E, N], y [M, N];
+ *   offsets int32 [E+1], non-decreasing; NULL with E = 1: group 0 has all M rows.
+ * Rows outside every group keep what y held.  Offsets outside [0, M] or
+ * decreasing are clamped, never followed out of bounds.
+ * M, N >= 0, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and M * max(N, Kp)
+ * < 2^40, a and w 16-byte aligned. */
+typedef struct {
+  int32_t M, N, K, E;
+  moe_dtype out;
+} moe_gemm_int8_desc;
+
+moe_status moe_gemm_int8_workspace_size(const moe_gemm_int8_desc* desc, size_t* bytes);
+moe_status moe_gemm_int8(const moe_gemm_int8_desc* desc, const int8_t* a, const float* a_scale,
+                         const int8_t* w, const float* w_scale, const int32_t* offsets_or_null,
+                         void* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* A layer's weights in 8 bits: the expert matrices of moe_weights as codes
+ * (d and F are multiples of 128, so rows have no padding) with a scale per
+ * row: t_gate, t_up [E, F], t_down [E, d], ts_* [S, ...] likewise.  w_router
+ * (fp32) is read by moe_forward_few_int8 only.  With S = 0 the shared experts'
+ * pointers may be NULL. */
+typedef struct {
+  const float* w_router;
+  const int8_t* w_gate;
+  const float* t_gate;
+  const int8_t* w_up;
+  const float* t_up;
+  const int8_t* w_down;
+  const float* t_down;
+  const int8_t* ws_gate;
+  const float* ts_gate;
+  const int8_t* ws_up;
+  const float* ts_up;
+  const int8_t* ws_down;
+  const float* ts_down;
+} moe_weights_int8;
+
+/* Every expert's whole FFN with 8-bit weights: moe_expert_ffn's inputs and
+ * outputs.  x is quantised per token, h = silu(gate) * up is taken in fp32 and
+ * quantised per row, y_routed and y_shared are rounded once to act.  The
+ * descriptor is that of the layer without 8-bit weights (act == weight), the
+ * same that moe_router, moe_dispatch and moe_combine take around this call.
+ * Rows of y_routed from offsets[E] on keep what they held. */
+moe_status moe_expert_ffn_int8_workspace_size(const moe_desc* desc, size_t* bytes);
+moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_weights_int8* w,
+                               const int32_t* offsets, const int32_t* sorted_pair,
+                               void* y_routed, void* y_shared, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
+/* The whole layer for few tokens (0 <= T <= 16), for decoding ("Inkling,
+ * Dissected", 02b: router, top-6, joint gates, weighted sum of the 8 experts'
+ * outputs), in two kernels.  moe_forward's arithmetic with one rounding: h and
+ * the experts' outputs are not rounded to act, only y is.  The bias is read,
+ * not updated; capacity_factor must be 0 (MOE_ERR_UNSUPPORTED otherwise, as
+ * are T > 16, weight == MOE_MXFP4, d or F > 65536 and the shapes
+ * moe_forward does not take).  topk_idx [T, 6] and gates [T, 6+S] are written
+ * where given.  A token whose x holds a NaN or an infinity gets NaN gates or
+ * outputs, its choice of experts is unspecified but valid; other tokens are
+ * not touched by it.
+ * moe_forward_few_int8 takes 8-bit weights: x is quantised per token, h per row
+ * (from fp32).  Both calls take the workspace of
+ * moe_forward_few_workspace_size; calls that overlap need one each. */
+moe_status moe_forward_few_workspace_size(const moe_desc* desc, size_t* bytes);
+moe_status moe_forward_few(const moe_desc* desc, const void* x, const moe_weights* w,
+                           const float* bias, void* y, int32_t* topk_idx_or_null,
+                           float* gates_or_null, void* ws, size_t ws_bytes, hipStream_t stream);
+moe_status moe_forward_few_int8(const moe_desc* desc, const void* x, const moe_weights_int8* w,
+                                const float* bias, void* y, int32_t* topk_idx_or_null,
+                                float* gates_or_null, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,7 +28,10 @@ SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_workspace_size", "moe_ro
            "moe_dispatch", "moe_expert_gate_up", "moe_expert_down", "moe_expert_ffn",
            "moe_combine", "moe_bias_update", "moe_forward", "moe_expert_gate_up_marked",
            "moe_expert_down_marked", "moe_quantize_mxfp4", "moe_forward_marked",
-           "moe_dispatch_noalloc", "moe_router_planes_size", "moe_router_prepare")
+           "moe_dispatch_noalloc", "moe_router_planes_size", "moe_router_prepare",
+           "moe_quantize_int8", "moe_gemm_int8_workspace_size", "moe_gemm_int8",
+           "moe_expert_ffn_int8_workspace_size", "moe_expert_ffn_int8",
+           "moe_forward_few_workspace_size", "moe_forward_few", "moe_forward_few_int8")
 
 
 class MoEError(RuntimeError):
@@ -49,6 +52,17 @@ class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("w_router", "w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down",
                  "sc_gate", "sc_up", "sc_down", "w_router_planes")]
+
+
+class GemmInt8Desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("out", ctypes.c_int)]
+
+
+class WeightsInt8(ctypes.Structure):
+    _fields_ = [("w_router", ctypes.c_void_p)] + [
+        (f"{a}{g}{p}", ctypes.c_void_p)
+        for g in ("", "s") for p in ("_gate", "_up", "_down") for a in ("w", "t")]
 
 
 class Routing(ctypes.Structure):
@@ -85,6 +99,14 @@ def _load(path=LIB_PATH):
         "moe_quantize_mxfp4": (I, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P, P, P]),
         "moe_router_planes_size": (I, [D, ctypes.POINTER(Z)]),
         "moe_router_prepare": (I, [D, P, P, P]),
+        "moe_quantize_int8": (I, [ctypes.c_int64, ctypes.c_int32, I, P, P, P, P]),
+        "moe_gemm_int8_workspace_size": (I, [ctypes.POINTER(GemmInt8Desc), ctypes.POINTER(Z)]),
+        "moe_gemm_int8": (I, [ctypes.POINTER(GemmInt8Desc), P, P, P, P, P, P, P, Z, P]),
+        "moe_expert_ffn_int8_workspace_size": (I, [D, ctypes.POINTER(Z)]),
+        "moe_expert_ffn_int8": (I, [D, P, ctypes.POINTER(WeightsInt8), P, P, P, P, P, Z, P]),
+        "moe_forward_few_workspace_size": (I, [D, ctypes.POINTER(Z)]),
+        "moe_forward_few": (I, [D, P, W, P, P, P, P, P, Z, P]),
+        "moe_forward_few_int8": (I, [D, P, ctypes.POINTER(WeightsInt8), P, P, P, P, P, Z, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -192,6 +214,7 @@ def make_weights(w_router, w_gate, w_up, w_down, ws_gate, ws_up, ws_down):
     dt = w_gate.dtype
     E, F, d = w_gate.shape
     S = ws_gate.shape[0]
+    wt.made_of = (E, F, d, S, dt, w_gate.device)
     wt.w_router = _ptr(w_router, torch.float32, (E + S, d), "w_router") if w_router is not None else None
     wt.w_gate = _ptr(w_gate, dt, (E, F, d), "w_gate")
     wt.w_up = _ptr(w_up, dt, (E, F, d), "w_up")
@@ -404,3 +427,208 @@ def forward(desc, x, weights, bias, gamma, y, routing=None, ws=None, events=None
     else:
         st = lib.moe_forward_marked(*args, _marks(events, 7), _stream(bias.device))
         _check("moe_forward_marked", st)
+
+
+# ------------------------------------------------- 8-bit products, few tokens
+
+def code_row(K):
+    """Length of a row of int8 codes: K rounded up to 128."""
+    return (K + 127) // 128 * 128
+
+
+def _at(t, dev, dtype, shape, name):
+    """Address of a tensor that must be on `dev`, dense, of this dtype and shape."""
+    if (isinstance(t, torch.Tensor) and t.device == dev and t.dtype is dtype
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    _ptr(t, dtype, shape, name)
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _on_gpu(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    return t.device
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _workspace(ws, need, dev, name):
+    if ws is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if ws.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {ws.device}")
+    return ws
+
+
+def quantize_int8(x, codes=None, scales=None):
+    """moe_quantize_int8 of the rows of x [..., K] (fp32 or bf16): codes int8
+    [..., Kp], Kp = K rounded up to 128, and scales fp32 [...].  Allocates the
+    outputs that are not given."""
+    dev = _on_gpu(x, "x")
+    code = act_code(x.dtype)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x needs a last dimension of at least one value")
+    K = x.shape[-1]
+    lead = x.shape[:-1]
+    if codes is None:
+        codes = torch.empty((*lead, code_row(K)), dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(lead, dtype=torch.float32, device=dev)
+    rows = lead.numel()
+    _check("moe_quantize_int8", _call(
+        dev, lib.moe_quantize_int8, rows, K, code, _at(x, dev, x.dtype, x.shape, "x"),
+        _at(codes, dev, torch.int8, (*lead, code_row(K)), "codes"),
+        _at(scales, dev, torch.float32, lead, "scales")))
+    return codes, scales
+
+
+def gemm_int8_workspace(M, N, K, E=1, device="cuda"):
+    """A workspace for gemm_int8 of these sizes (reusable by calls in turn)."""
+    n = ctypes.c_size_t(0)
+    _check("moe_gemm_int8_workspace_size",
+           lib.moe_gemm_int8_workspace_size(ctypes.byref(GemmInt8Desc(M, N, K, E, F32)),
+                                            ctypes.byref(n)))
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
+
+
+def gemm_int8(a, a_scale, w, w_scale, y, offsets=None, ws=None):
+    """moe_gemm_int8: y [M, N] (fp32 or bf16) = a [M, Kp] int8 times w [E, N, Kp]
+    int8, scaled by a_scale [M] and w_scale [E, N].  ``offsets`` int32 [E+1]
+    gives each group's rows; without it E must be 1.  Rows outside the groups
+    keep what y held."""
+    dev = _on_gpu(a, "a")
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("gemm_int8 takes a [M, Kp] and w [E, N, Kp]")
+    M, Kp = a.shape
+    E, N, _ = w.shape
+    if Kp == 0 or Kp % 128:
+        raise ValueError(f"gemm_int8: rows of codes are padded to a multiple of 128, got {Kp}")
+    desc = GemmInt8Desc(M, N, Kp, E, act_code(y.dtype))
+    if ws is None:
+        ws = gemm_int8_workspace(M, N, Kp, E, dev)
+    ws = _workspace(ws, 0, dev, "ws")
+    _check("moe_gemm_int8", _call(
+        dev, lib.moe_gemm_int8, ctypes.byref(desc), _at(a, dev, torch.int8, (M, Kp), "a"),
+        _at(a_scale, dev, torch.float32, (M,), "a_scale"),
+        _at(w, dev, torch.int8, (E, N, Kp), "w"),
+        _at(w_scale, dev, torch.float32, (E, N), "w_scale"),
+        None if offsets is None else _at(offsets, dev, torch.int32, (E + 1,), "offsets"),
+        _at(y, dev, y.dtype, (M, N), "y"), _ptr(ws, torch.uint8, None, "ws"), ws.numel()))
+
+
+def make_weights_int8(w_router, w_gate, t_gate, w_up, t_up, w_down, t_down,
+                      ws_gate, ts_gate, ws_up, ts_up, ws_down, ts_down):
+    """WeightsInt8 from the codes [E or S, out, in] and scales [E or S, out] of
+    each matrix (quantize_int8 of the stacks); w_router may be None where the
+    router is called on its own.  The tensors must stay alive while the
+    WeightsInt8 is used."""
+    dev = _on_gpu(w_gate, "w_gate")
+    E, F, d = w_gate.shape
+    S = ws_gate.shape[0]
+    wt = WeightsInt8()
+    wt.made_of = (E, F, d, S, torch.int8, dev)
+    wt.w_router = (None if w_router is None else
+                   _at(w_router, dev, torch.float32, (E + S, d), "w_router"))
+    for n, prefix, parts in ((E, "", ((w_gate, t_gate), (w_up, t_up), (w_down, t_down))),
+                             (S, "s", ((ws_gate, ts_gate), (ws_up, ts_up), (ws_down, ts_down)))):
+        for part, (w, t) in zip(("gate", "up", "down"), parts):
+            out, inner = (d, F) if part == "down" else (F, d)
+            setattr(wt, f"w{prefix}_{part}",
+                    _at(w, dev, torch.int8, (n, out, inner), f"w{prefix}_{part}"))
+            setattr(wt, f"t{prefix}_{part}",
+                    _at(t, dev, torch.float32, (n, out), f"t{prefix}_{part}"))
+    return wt
+
+
+def int8_weights(inp):
+    """WeightsInt8 of a layer's fp32 or bf16 weights, each expert matrix
+    quantized per output channel (its last dimension a multiple of 128).
+    Returns (WeightsInt8, dict of the new tensors, which must stay alive with
+    inp["w_router"] while the WeightsInt8 is used)."""
+    q = {}
+    for n in ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down"):
+        if inp[n].shape[-1] % 128:
+            raise ValueError(f"int8_weights: rows of {n} are not a multiple of 128 values")
+        q[n], q["t" + n[1:]] = quantize_int8(inp[n])
+    return make_weights_int8(inp["w_router"], *(q[a + p] for s in ("", "s")
+                                                for p in ("_gate", "_up", "_down")
+                                                for a in ("w" + s, "t" + s))), q
+
+
+def _weights_for(desc, weights, dev, kinds, fn):
+    """Checks that `weights` was made for the descriptor's layer and device."""
+    if not isinstance(weights, kinds):
+        raise TypeError(f"{fn}: weights must be {' or '.join(k.__name__ for k in kinds)}")
+    made = getattr(weights, "made_of", None)
+    if made is not None:
+        want = (desc.E, desc.F, desc.d, desc.S)
+        if made[:4] != want:
+            raise ValueError(f"{fn}: weights are of a layer (E, F, d, S) = {made[:4]}, the "
+                             f"descriptor's is {want}")
+        if made[4] not in (torch.int8, _act(desc)):
+            raise TypeError(f"{fn}: weights are {made[4]}, the descriptor's dtype is {_act(desc)}")
+        if made[5] != dev:
+            raise ValueError(f"{fn}: weights are on {made[5]}, x on {dev}")
+
+
+def _sized(fn, name, desc, dev):
+    n = ctypes.c_size_t(0)
+    _check(name, fn(ctypes.byref(desc), ctypes.byref(n)))
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=dev)
+
+
+def expert_ffn_int8_workspace(desc, device):
+    return _sized(lib.moe_expert_ffn_int8_workspace_size, "moe_expert_ffn_int8_workspace_size",
+                  desc, device)
+
+
+def expert_ffn_int8(desc, x, weights, offsets, sorted_pair, y_routed, y_shared, ws=None):
+    """moe_expert_ffn_int8: expert_ffn with 8-bit weights (WeightsInt8); desc is
+    the layer's ordinary descriptor."""
+    dev = _on_gpu(x, "x")
+    _weights_for(desc, weights, dev, (WeightsInt8,), "expert_ffn_int8")
+    ws = expert_ffn_int8_workspace(desc, dev) if ws is None else _workspace(ws, 0, dev, "ws")
+    T, d, k, S, E = desc.T, desc.d, desc.k, desc.S, desc.E
+    act, i32 = _act(desc), torch.int32
+    _check("moe_expert_ffn_int8", _call(
+        dev, lib.moe_expert_ffn_int8, ctypes.byref(desc), _at(x, dev, act, (T, d), "x"),
+        ctypes.byref(weights), _at(offsets, dev, i32, (E + 1,), "offsets"),
+        _at(sorted_pair, dev, i32, (T * k,), "sorted_pair"),
+        _at(y_routed, dev, act, (T * k, d), "y_routed"),
+        None if y_shared is None else _at(y_shared, dev, act, (S, T, d), "y_shared"),
+        _ptr(ws, torch.uint8, None, "ws"), ws.numel()))
+
+
+def forward_few_workspace(desc, device):
+    return _sized(lib.moe_forward_few_workspace_size, "moe_forward_few_workspace_size", desc,
+                  device)
+
+
+def forward_few(desc, x, weights, bias, y, topk_idx=None, gates=None, ws=None):
+    """The whole layer for 1 to 16 tokens in two kernels: moe_forward_few with
+    Weights of desc's dtype, moe_forward_few_int8 with WeightsInt8.  The bias is
+    read, not updated.  Calls that overlap need a workspace each."""
+    dev = _on_gpu(x, "x")
+    _weights_for(desc, weights, dev, (Weights, WeightsInt8), "forward_few")
+    ws = forward_few_workspace(desc, dev) if ws is None else _workspace(ws, 0, dev, "ws")
+    T, d, k, S, E = desc.T, desc.d, desc.k, desc.S, desc.E
+    act = _act(desc)
+    int8 = type(weights) is WeightsInt8
+    _check("moe_forward_few_int8" if int8 else "moe_forward_few", _call(
+        dev, lib.moe_forward_few_int8 if int8 else lib.moe_forward_few, ctypes.byref(desc),
+        _at(x, dev, act, (T, d), "x"), ctypes.byref(weights),
+        _at(bias, dev, torch.float32, (E,), "bias"), _at(y, dev, act, (T, d), "y"),
+        None if topk_idx is None else _at(topk_idx, dev, torch.int32, (T, k), "topk_idx"),
+        None if gates is None else _at(gates, dev, torch.float32, (T, k + S), "gates"),
+        _ptr(ws, torch.uint8, None, "ws"), ws.numel()))

@@ -1,0 +1,166 @@
+"""Refusals of the 8-bit products and of the few-token layer (no GPU: every
+call here fails validation, or has nothing to do, before any launch)."""
+import ctypes
+
+import pytest
+import torch
+
+L = pytest.importorskip("sparse_mixture_experts_04_amd._lib")
+lib = L.lib
+P = ctypes.c_void_p(0x1000)      # never dereferenced
+ODD = ctypes.c_void_p(0x1004)    # not 16-byte aligned
+
+
+def ref(s):
+    return ctypes.byref(s)
+
+
+def size_of(fn, d):
+    n = ctypes.c_size_t(0)
+    return fn(ref(d) if d is not None else None, ref(n)), n.value
+
+
+def desc(**kw):
+    base = dict(T=8, d=512, F=128, E=256, S=2, k=6, act=L.BF16, weight=L.BF16,
+                gate_norm=L.GATE_RATIO, gate_scale=1.0, capacity_factor=0.0)
+    base.update(kw)
+    return L.Desc(**base)
+
+
+def w8(**kw):
+    w = L.WeightsInt8(*([0x1000] * 13))
+    for k, v in kw.items():
+        setattr(w, k, v)
+    return w
+
+
+def test_quantize_checks():
+    q = lib.moe_quantize_int8
+    assert q(-1, 64, L.F32, P, P, P, None) == 2
+    assert q(4, 0, L.F32, P, P, P, None) == 2
+    assert q(4, 64, L.MXFP4, P, P, P, None) == 3
+    assert q(4, 131073, L.F32, P, P, P, None) == 5
+    assert q(1 << 31, 64, L.F32, P, P, P, None) == 5
+    assert q(4, 64, L.F32, None, P, P, None) == 1
+    assert q(4, 64, L.F32, P, None, P, None) == 1
+    assert q(4, 64, L.F32, P, P, None, None) == 1
+    assert q(4, 64, L.BF16, P, ODD, P, None) == 5
+    assert q(0, 64, L.BF16, None, None, None, None) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), 2), (dict(N=-1), 2), (dict(K=0), 2), (dict(E=0), 2), (dict(out=2), 3),
+    (dict(K=131073), 5), (dict(E=257), 5), (dict(E=256, N=1 << 24, K=1 << 14), 5),
+    (dict(M=1 << 30, K=1 << 11), 5), (dict(), 0), (dict(M=0), 0), (dict(K=131072), 0),
+])
+def test_gemm_desc(kw, code):
+    d = L.GemmInt8Desc(**{**dict(M=4, N=8, K=100, E=1, out=L.BF16), **kw})
+    st, n = size_of(lib.moe_gemm_int8_workspace_size, d)
+    assert st == code and (code != 0 or n > 0)
+
+
+def test_gemm_checks():
+    g = lib.moe_gemm_int8
+    d = L.GemmInt8Desc(4, 8, 100, 1, L.BF16)
+    need = size_of(lib.moe_gemm_int8_workspace_size, d)[1]
+    assert g(None, P, P, P, P, None, P, P, need, None) == 1
+    for hole in range(4):
+        a = [P, P, P, P]
+        a[hole] = None
+        assert g(ref(d), *a, None, P, P, need, None) == 1
+    assert g(ref(d), P, P, P, P, None, None, P, need, None) == 1
+    assert g(ref(d), ODD, P, P, P, None, P, P, need, None) == 5
+    assert g(ref(d), P, P, ODD, P, None, P, P, need, None) == 5
+    assert g(ref(d), P, P, P, P, None, ODD, P, need, None) == 5
+    assert g(ref(d), P, P, P, P, None, P, P, need - 1, None) == 4
+    assert g(ref(d), P, P, P, P, None, P, None, need, None) == 4
+    grouped = L.GemmInt8Desc(4, 8, 100, 2, L.BF16)
+    assert g(ref(grouped), P, P, P, P, None, P, P, 1 << 20, None) == 1    # offsets missing
+    assert lib.moe_gemm_int8_workspace_size(ref(d), None) == 1
+    # nothing to do
+    for shape in ((0, 8), (4, 0)):
+        assert g(ref(L.GemmInt8Desc(*shape, 100, 1, L.F32)), None, None, None, None, None, None,
+                 None, 0, None) == 0
+
+
+def test_expert_ffn_int8_checks():
+    f = lib.moe_expert_ffn_int8
+    d = desc()
+    need = size_of(lib.moe_expert_ffn_int8_workspace_size, d)[1]
+    assert size_of(lib.moe_expert_ffn_int8_workspace_size, None)[0] == 1
+    assert size_of(lib.moe_expert_ffn_int8_workspace_size, desc(weight=L.MXFP4))[0] == 3
+    assert size_of(lib.moe_expert_ffn_int8_workspace_size, desc(d=384))[0] == 5
+    w = w8()
+    assert f(ref(d), P, ref(w), P, P, P, P, P, need - 1, None) == 4
+    assert f(ref(d), P, None, P, P, P, P, P, need, None) == 1
+    assert f(ref(d), None, ref(w), P, P, P, P, P, need, None) == 1
+    assert f(ref(d), P, ref(w), None, P, P, P, P, need, None) == 1
+    assert f(ref(d), P, ref(w), P, None, P, P, P, need, None) == 1
+    assert f(ref(d), P, ref(w), P, P, None, P, P, need, None) == 1
+    assert f(ref(d), P, ref(w), P, P, P, None, P, need, None) == 1
+    assert f(ref(d), ODD, ref(w), P, P, P, P, P, need, None) == 5
+    for name, _ in L.WeightsInt8._fields_[1:]:
+        assert f(ref(d), P, ref(w8(**{name: None})), P, P, P, P, P, need, None) == 1, name
+    assert f(ref(d), P, ref(w8(ws_up=0x1008)), P, P, P, P, P, need, None) == 5
+    assert f(ref(desc(T=0)), None, ref(w), P, None, None, None, P, 1 << 20, None) == 0
+
+
+def test_forward_few_checks():
+    few, few8 = lib.moe_forward_few, lib.moe_forward_few_int8
+    size = lib.moe_forward_few_workspace_size
+    d = desc()
+    need = size_of(size, d)[1]
+    assert need > 0 and size(ref(d), None) == 1
+    for kw, code in ((dict(T=17), 5), (dict(capacity_factor=1.25), 5), (dict(weight=L.MXFP4), 5),
+                     (dict(d=384), 5), (dict(F=64), 5), (dict(d=65536 + 256), 5),
+                     (dict(k=8), 5), (dict(T=-1), 2), (dict(act=L.F32), 3),
+                     (dict(gate_scale=0.0), 2), (dict(T=16), 0), (dict(S=0), 0), (dict(T=0), 0)):
+        assert size_of(size, desc(**kw))[0] == code, kw
+    w = L.Weights(*([0x1000] * 7))
+    assert few(ref(d), P, ref(w), P, P, None, None, P, need - 1, None) == 4
+    assert few(ref(d), P, None, P, P, None, None, P, need, None) == 1
+    assert few(ref(d), None, ref(w), P, P, None, None, P, need, None) == 1
+    assert few(ref(d), P, ref(w), None, P, None, None, P, need, None) == 1
+    assert few(ref(d), P, ref(w), P, None, None, None, P, need, None) == 1
+    assert few(ref(d), ODD, ref(w), P, P, None, None, P, need, None) == 5
+    assert few(ref(d), P, ref(L.Weights(0x1000, 0x1004, *([0x1000] * 5))), P, P, None, None, P,
+               need, None) == 5
+    # MXFP4 matrices are a quarter of what this call reads
+    fp4 = L.Weights(*([0x1000] * 10))
+    assert few(ref(d), P, ref(fp4), P, P, None, None, P, need, None) == 3
+    assert few8(ref(d), P, ref(w8(w_router=None)), P, P, None, None, P, need, None) == 1
+    assert few8(ref(d), P, ref(w8(t_down=None)), P, P, None, None, P, need, None) == 1
+    assert few8(ref(d), P, ref(w8(w_down=0x1008)), P, P, None, None, P, need, None) == 5
+    assert few8(ref(d), P, ref(w8()), P, P, None, None, None, need, None) == 4
+    assert few(ref(desc(T=0)), None, ref(w), P, None, None, None, P, need, None) == 0
+
+
+def test_binding_refuses_host_tensors_and_other_layers():
+    x = torch.zeros(2, 128)
+    with pytest.raises(ValueError, match="GPU"):
+        L.quantize_int8(x)
+    with pytest.raises(TypeError):
+        L.quantize_int8([1.0])
+    with pytest.raises(ValueError, match="GPU"):
+        L.gemm_int8(torch.zeros(2, 128, dtype=torch.int8), x, x, x, x)
+    with pytest.raises(ValueError, match="GPU"):
+        L.forward_few(L.make_desc(2, 512, 128, torch.float32), x, L.Weights(), x, x)
+    # weights remember the layer they were made for
+    dev = torch.device("cuda:0")
+    d = L.make_desc(2, 512, 128, torch.bfloat16)
+    w = L.WeightsInt8()
+    w.made_of = (256, 256, 512, 2, torch.int8, dev)
+    with pytest.raises(ValueError, match="layer"):
+        L._weights_for(d, w, dev, (L.WeightsInt8,), "f")
+    w.made_of = (256, 128, 512, 2, torch.int8, torch.device("cuda:1"))
+    with pytest.raises(ValueError, match="cuda:1"):
+        L._weights_for(d, w, dev, (L.WeightsInt8,), "f")
+    with pytest.raises(TypeError):
+        L._weights_for(d, w, dev, (L.Weights,), "f")
+    wf = L.Weights()
+    wf.made_of = (256, 128, 512, 2, torch.float32, dev)
+    with pytest.raises(TypeError, match="float32"):
+        L._weights_for(d, wf, dev, (L.Weights, L.WeightsInt8), "f")
+    with pytest.raises(ValueError, match="128"):
+        L.int8_weights({n: torch.zeros(1, 8, 100) for n in
+                        ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")})
