@@ -446,7 +446,7 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
  * outputs), in two kernels.  moe_forward's arithmetic with one rounding: h and
  * the experts' outputs are not rounded to act, only y is.  The bias is read,
  * not updated; capacity_factor must be 0 (MOE_ERR_UNSUPPORTED otherwise, as
- * are T > 16, weight == MOE_MXFP4, d or F > 65536 and the shapes
+ * are T > 16, weight == MOE_MXFP4, d or F > 16384 and the shapes
  * moe_forward does not take).  topk_idx [T, 6] and gates [T, 6+S] are written
  * where given.  A token whose x holds a NaN or an infinity gets NaN gates or
  * outputs, its choice of experts is unspecified but valid; other tokens are

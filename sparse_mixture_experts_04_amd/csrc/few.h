@@ -11,14 +11,14 @@ constexpr int kFewTopK = 6;
 // Weight element type of the few-token layer.
 enum class FewWeight { kBf16, kF32, kInt8 };
 
-// Workgroups of the experts' kernel: two per compute unit.
-constexpr int kFewGrid = 512;
-// Largest number of parts that a block of output columns is summed in.
-constexpr int kFewMaxParts = 4;
+// Workgroups of the experts' kernel: one per compute unit.
+constexpr int kFewGrid = 256;
+// Largest d and F.
+constexpr int kFewMaxWidth = 16384;
 // int32 words of the control block: a flag per workgroup, per token and per
-// row of h, a counter per block of 16 output columns.
+// row of h.
 inline size_t few_ctrl_ints(const Shape& s) {
-  return kFewGrid + kFewMaxTokens + static_cast<size_t>(kFewTopK + s.S) * s.T + s.d / 16;
+  return kFewGrid + kFewMaxTokens + static_cast<size_t>(kFewTopK + s.S) * s.T;
 }
 
 struct FewArgs {
@@ -33,18 +33,16 @@ struct FewArgs {
   int32_t* topk_out;       // [T, 6] or null
   float* gates_out;        // [T, 6 + S] or null
   // workspace; rows of h are the 6 T pairs, then shared expert s's T rows
-  double* z;               // [T, E+S] logits
+  double2* zs;             // [T, E+S] logits and their sigmoids
   int32_t* topk;           // [T, 6]
   float* gates;            // [T, 6 + S]
   int32_t* ctrl;           // few_ctrl_ints
   int8_t* xq;              // [T, d] codes (int8)
   float* xs;               // [T]
-  void* h;                 // [rows, F] fp32, or two bf16 planes [2, rows, F]
+  float* h;                // [rows, F]
   int8_t* hq;              // [rows, F] codes (int8)
   float* hs;               // [rows]
-  float* ypart;            // [kFewMaxParts, T, d] fp32
   int T, d, F, E, S;
-  int parts;               // parts each block of output columns is summed in
   bool logsumexp;
   double gate_scale;
 };

@@ -33,10 +33,12 @@
 // With bf16 weights h enters the down product as two bf16 terms (h = hi + lo
 // to 2^-17): the second product costs no memory traffic.  With 8-bit weights x
 // is quantised per token and h per row.
+#include <type_traits>
+
 #include "few.h"
 #include "int8_quant.h"
 #include "select.h"
-#include "stream.h"
+#include "rowstream.h"
 
 namespace moe {
 
@@ -56,7 +58,7 @@ __device__ __forceinline__ void load4(const bf16_t* p, double (&v)[4]) {
 }
 
 // Block b < E + S: the logits of router row b for all tokens (products exact
-// in fp64, sums in a fixed order).  Block E + S clears the control block of
+// in fp64, sums in a fixed order) and their sigmoids.  Block E + S clears the control block of
 // few_ffn_kernel.  INT8: block E + S + 1 + t quantises token t.  TM: tokens
 // rounded up to a power of two.
 template <typename X, int TM, bool INT8>
@@ -99,53 +101,78 @@ __global__ __launch_bounds__(256) void few_route_kernel(FewArgs p, int ctrl_ints
     if (lane == 0) sum[wave][t] = v;
   }
   __syncthreads();
-  if (tid < p.T)
-    p.z[static_cast<size_t>(tid) * rows + b] =
-        ((sum[0][tid] + sum[1][tid]) + sum[2][tid]) + sum[3][tid];
+  if (tid < p.T) {
+    const double z = ((sum[0][tid] + sum[1][tid]) + sum[2][tid]) + sum[3][tid];
+    p.zs[static_cast<size_t>(tid) * rows + b] = double2{z, sigmoid64(z)};
+  }
 }
 
 // --------------------------------------------------------------- the experts
 
-// Top-6, gates of token t by one wave.  A NaN key ranks last (the gates of
-// such a token are NaN, and so is its output).
+// Top-6 and gates of token t by one wave, in little code: a workgroup that runs
+// this waits for every line of it to come from memory (the weights have
+// streamed it out of the caches since the last call), so the rounds are a loop
+// and the gates are taken a lane each.  A NaN key ranks last (the gates of such
+// a token are NaN, and so is its output).
 template <int S>
 __device__ __forceinline__ void few_select(const FewArgs& p, int t, int lane) {
-  __shared__ int32_t s_topk[kFewTopK];
-  __shared__ float s_gates[kFewTopK + S];
   constexpr int EPL = 4;  // experts per lane; those past E are no candidates
-  const double* z = p.z + static_cast<size_t>(t) * (p.E + S);
-  double zv[EPL], sv[EPL], key[EPL];
-  bool valid[EPL];
+  const double2* zs = p.zs + static_cast<size_t>(t) * (p.E + S);
+  double key[EPL];
+  int open = 0;  // bit q: expert lane + 64 q is a candidate
 #pragma unroll
   for (int q = 0; q < EPL; ++q) {
     const int e = lane + 64 * q;
-    valid[q] = e < p.E;
-    zv[q] = valid[q] ? z[e] : 0.0;
-    sv[q] = sigmoid64(zv[q]);
-    const double k = valid[q] ? sv[q] + static_cast<double>(p.bias[e]) : 0.0;
-    key[q] = k == k ? k : -INFINITY;
+    key[q] = -INFINITY;
+    if (e < p.E) {
+      const double k = zs[e].y + static_cast<double>(p.bias[e]);
+      key[q] = k == k ? k : -INFINITY;
+      open |= 1 << q;
+    }
   }
-  const double z_sh = lane < S ? z[p.E + lane] : 0.0;
-  int i_sel[kFewTopK];
-  double s_pick[kFewTopK], z_pick[kFewTopK], k_sel[kFewTopK + 1];
-  rank_rounds<kFewTopK, EPL>(lane, valid, key, sv, zv, i_sel, s_pick, z_pick, k_sel);
-  write_token<kFewTopK, S>(0, lane, i_sel, s_pick, z_pick, sigmoid64(z_sh), z_sh, k_sel, s_topk,
-                           s_gates, nullptr, p.logsumexp, p.gate_scale);
-  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // LDS of one wave, in order
+  int id = p.E + (lane - kFewTopK < S ? lane - kFewTopK : 0);  // this lane's contributor
+#pragma unroll 1
+  for (int r = 0; r < kFewTopK; ++r) {
+    double bk = -INFINITY;
+    int bj = 0x7fffffff;
+#pragma unroll
+    for (int q = 0; q < EPL; ++q) {
+      if (((open >> q) & 1) && better(key[q], lane + 64 * q, bk, bj)) {
+        bk = key[q];
+        bj = lane + 64 * q;
+      }
+    }
+    wave_argmax(bk, bj, lane);
+    if ((bj & 63) == lane) open &= ~(1 << (bj >> 6));
+    if (lane == r) id = bj;
+  }
+  // lane j < 6 + S: contributor j
+  const bool mine = lane < kFewTopK + S;
+  const double2 v = mine ? zs[id] : double2{0.0, 0.0};
+  double g;
+  if (p.logsumexp) {  // exp(l - logsumexp l), l = logsigmoid(z)
+    const double l = fmin(v.x, 0.0) - log1p(exp(-fabs(v.x)));
+    double m = mine ? l : -INFINITY;
+    int who = lane;
+    wave_argmax(m, who, lane);
+    g = exp(l - (m + log(wave_sum(mine ? exp(l - m) : 0.0, lane)))) * p.gate_scale;
+  } else {
+    g = v.y / (wave_sum(v.y, lane) / p.gate_scale);
+  }
+  if (!mine) return;
+  const int at = t * (kFewTopK + S) + lane;
+  agent_store(p.gates + at, static_cast<float>(g));
+  if (p.gates_out) p.gates_out[at] = static_cast<float>(g);
   if (lane < kFewTopK) {
-    agent_store(p.topk + t * kFewTopK + lane, s_topk[lane]);
-    if (p.topk_out) p.topk_out[t * kFewTopK + lane] = s_topk[lane];
-  }
-  if (lane < kFewTopK + S) {
-    agent_store(p.gates + t * (kFewTopK + S) + lane, s_gates[lane]);
-    if (p.gates_out) p.gates_out[t * (kFewTopK + S) + lane] = s_gates[lane];
+    agent_store(p.topk + t * kFewTopK + lane, id);
+    if (p.topk_out) p.topk_out[t * kFewTopK + lane] = id;
   }
 }
 
 // States of a flag.
 enum { kIdle = 0, kStarted = 1, kDone = 2 };
 
-constexpr int kFewThreads = 512;
+constexpr int kFewThreads = 1024;
 constexpr int kFewWaves = kFewThreads / 64;
 constexpr int kPatience = 64;  // polls before a waiter looks for work not started
 
@@ -193,173 +220,296 @@ __device__ __forceinline__ int wait_all(const int32_t* flags, int n, int from, i
   return -1;
 }
 
+// The rows of all contributors as one list: the shared experts' tokens, then the
+// pairs of the routed experts in ascending expert (and pair) order; entries are
+// runs of up to kUnitRows rows of one expert.
+constexpr int kFewRows = kFewMaxTokens * (kFewTopK + 2);
+constexpr int kFewEntries = kFewMaxTokens * kFewTopK + 2 * ((kFewMaxTokens + kUnitRows - 1) / kUnitRows);
 struct FewPlan {
-  int topk[kFewMaxTokens * kFewTopK];
-  int pair[kFewMaxTokens * kFewTopK];     // pairs grouped by expert, ascending
-  int expert[kFewMaxTokens * kFewTopK];   // active experts, ascending
-  int start[kFewMaxTokens * kFewTopK + 1];  // first entry of pair[] per active expert
-  int active;
+  int tok[kFewRows + kUnitRows];    // token of a list row
+  int hrow[kFewRows + kUnitRows];   // its row of h
+  float gate[kFewRows + kUnitRows]; // its gate (times its scale of h, 8-bit weights)
+  int first[kFewEntries + 1];       // first list row of an entry
+  int expert[kFewEntries + 1];      // its row of the weight stack
+  int shared_entries, entries;
 };
 
-// Groups the 6 T pairs by expert (the first 256 threads stand for an expert
-// each).
-__device__ __forceinline__ void few_plan(const FewArgs& p, FewPlan& s) {
-  __shared__ int wact[kFewWaves], wrow[kFewWaves];
+// Entries of the shared experts (all threads, a barrier after it).
+template <int S>
+__device__ __forceinline__ void plan_shared(const FewArgs& p, FewPlan& s) {
+  const int per = (p.T + kUnitRows - 1) / kUnitRows;
+  const int tid = threadIdx.x;
+  if (tid < S * p.T) {
+    s.tok[tid] = tid % p.T;
+    s.hrow[tid] = p.T * kFewTopK + tid;
+  }
+  if (tid < S * per) {
+    s.first[tid] = tid / per * p.T + tid % per * kUnitRows;
+    s.expert[tid] = tid / per;
+  }
+  if (tid == 0) {
+    s.shared_entries = S * per;
+    s.first[S * per] = S * p.T;
+  }
+}
+
+// Entries of the routed experts: thread e stands for expert e and finds its
+// pairs in a bit mask of the 6 T pairs.
+template <int S>
+__device__ __forceinline__ void plan_routed(const FewArgs& p, FewPlan& s) {
+  constexpr int MW = (kFewMaxTokens * kFewTopK + 31) / 32;
+  __shared__ uint32_t mask[256][MW];
+  __shared__ int wrow[4], went[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = p.T * kFewTopK;
+  for (int i = tid; i < 256 * MW; i += kFewThreads) (&mask[0][0])[i] = 0;
+  __syncthreads();
   if (tid < n) {
     const int e = agent_load(p.topk + tid);
-    s.topk[tid] = e < 0 ? 0 : e >= p.E ? p.E - 1 : e;
+    atomicOr(&mask[e < 0 ? 0 : e >= p.E ? p.E - 1 : e][tid / 32], 1u << (tid % 32));
   }
   __syncthreads();
-  int cnt = 0;  // pairs of expert tid
-  for (int i = 0; i < n; ++i) cnt += s.topk[i] == tid ? 1 : 0;
-  int rows = cnt, act = cnt > 0 ? 1 : 0;
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(rows, o), v = __shfl_up(act, o);
-    if (lane >= o) {
-      rows += u;
-      act += v;
+  int cnt = 0, rows = 0, ent = 0;
+  if (tid < 256) {
+    for (int i = 0; i < MW; ++i) cnt += __popc(mask[tid][i]);
+    rows = cnt;
+    ent = (cnt + kUnitRows - 1) / kUnitRows;
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(rows, o), v = __shfl_up(ent, o);
+      if (lane >= o) {
+        rows += u;
+        ent += v;
+      }
+    }
+    if (lane == 63) {
+      wrow[wave] = rows;
+      went[wave] = ent;
     }
   }
-  if (lane == 63) {
-    wrow[wave] = rows;
-    wact[wave] = act;
-  }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) {
-    rows += wrow[w];
-    act += wact[w];
-  }
-  if (cnt > 0) {
-    s.expert[act - 1] = tid;
-    int at = rows - cnt;
-    s.start[act - 1] = at;
-    for (int i = 0; i < n; ++i)
-      if (s.topk[i] == tid) s.pair[at++] = i;
-  }
-  if (tid == kFewThreads - 1) {
-    s.active = act;
-    s.start[act] = rows;
+  if (tid < 256) {
+    for (int w = 0; w < wave; ++w) {
+      rows += wrow[w];
+      ent += went[w];
+    }
+    int at = S * p.T + rows - cnt;
+    const int e0 = s.shared_entries + ent - (cnt + kUnitRows - 1) / kUnitRows;
+    for (int i = 0; i * kUnitRows < cnt; ++i) {
+      s.first[e0 + i] = at + i * kUnitRows;
+      s.expert[e0 + i] = tid;
+    }
+    for (int i = 0; i < MW; ++i)
+      for (uint32_t m = mask[tid][i]; m; m &= m - 1) {
+        const int pair = i * 32 + __ffs(m) - 1;
+        s.tok[at] = pair / kFewTopK;
+        s.hrow[at++] = pair;
+      }
+    if (tid == 255) {
+      s.entries = s.shared_entries + ent;
+      s.first[s.shared_entries + ent] = S * p.T + rows;
+    }
   }
   __syncthreads();
 }
 
-template <class Op> struct FewTraits;
-template <> struct FewTraits<OpBf16> { static constexpr int ESZ = 2, PLANES = 2; };
-template <> struct FewTraits<OpF32> { static constexpr int ESZ = 4, PLANES = 1; };
-template <> struct FewTraits<OpI8> { static constexpr int ESZ = 1, PLANES = 1; };
+// LDS of a workgroup: sums (gate and up of kPartCols columns, or each wave's
+// share of its y), then activation rows.
+constexpr int kPool = 144 * 1024;
+constexpr int kPartCols = 512;     // gate/up columns between two epilogues
+constexpr int kPartBytes = kPartCols * 2 * kUnitRows * 4;
+static_assert(kFewWaves * (kFewMaxWidth / kFewGrid) * kFewMaxTokens * 4 + 8 * kUnitRows * kChunk <=
+                  kPool, "8 chunks of 8 rows beside the widest y");
 
-// Shared memory of few_ffn_kernel outside the plan.
-template <class Op>
-union FewLds {
-  typename Op::Acc red[2][kFewWaves][4][64];              // gate/up: partial tiles
-  float ysum[kFewWaves][kFewMaxTokens][16];               // down: each wave's share of y
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Gate/up columns c0..c1-1 of the list (entry ent0 + c / F, column c % F), two
+// units each; sums go to part[c - cbase].
+template <class Acc>
+struct GateWalk {
+  const FewPlan& plan;
+  Acc (*part)[2][kUnitRows];
+  const char *wg, *wu;
+  size_t kfull;       // bytes of a weight row
+  int F, c0, n, cbase, ent0, xstride, lane;
+  bool more;          // not the first pass over K: add
+  // load side: the next unit
+  const char *lg, *lu2;
+  int lf, lent;
+  // multiply side
+  int f, ent;
+
+  __device__ __forceinline__ GateWalk(const FewPlan& pl, Acc (*pt)[2][kUnitRows], const void* g, const void* u,
+                      size_t kf, size_t koff, int F_, int c0_, int c1_, int cb, int e0, int xs,
+                      bool m)
+      : plan(pl), part(pt), wg(static_cast<const char*>(g) + koff),
+        wu(static_cast<const char*>(u) + koff), kfull(kf), F(F_), c0(c0_), n(c1_ - c0_), cbase(cb),
+        ent0(e0), xstride(xs), lane(threadIdx.x & 63), more(m) {
+    lent = ent = ent0 + c0 / F;
+    lf = f = c0 % F;
+    --f;
+    place();
+  }
+  __device__ __forceinline__ void place() {
+    const size_t o = (static_cast<size_t>(uniform(plan.expert[lent])) * F + lf) * kfull;
+    lg = wg + o;
+    lu2 = wu + o;
+  }
+  __device__ __forceinline__ int units() const { return 2 * n; }
+  __device__ __forceinline__ const char* row(int u) {
+    if (u & 1) return lu2;
+    if (u > 0) {
+      lg += kfull;
+      lu2 += kfull;
+      if (++lf == F) {
+        lf = 0;
+        ++lent;
+        place();
+      }
+    }
+    return lg;
+  }
+  __device__ __forceinline__ int enter(int u, int (&off)[kUnitRows]) {
+    if (!(u & 1) && (++f == F || u == 0)) {
+      if (f == F) {
+        f = 0;
+        ++ent;
+      }
+      const int r0 = plan.first[ent];
+      rows = uniform(plan.first[ent + 1] - r0);
+#pragma unroll
+      for (int r = 0; r < kUnitRows; ++r)
+        off[r] = plan.tok[r0 + (r < rows ? r : 0)] * xstride + lane * 16;
+    }
+    return rows;
+  }
+  __device__ __forceinline__ void leave(int u, int nr, const Acc (&acc)[kUnitRows]) {
+    Acc* out = part[c0 - cbase + (u >> 1)][u & 1];
+#pragma unroll
+    for (int r = 0; r < kUnitRows; ++r) {
+      if (r >= nr) break;
+      const Acc s = wave_total(acc[r]);
+      if (lane == 0) out[r] = more ? out[r] + s : s;
+    }
+  }
+  int rows = 0;
 };
 
-// Group of CT tiles of expert e: tile c is 8 columns from f0 + 8 c on, its 16
-// weight rows the 8 W_gate rows of these columns, then the 8 W_up rows.  The
-// waves split K.  wave c then finishes tile c: h = silu(gate) * up of the R
-// rows of the group.
-template <class Op, int CT>
-__device__ __forceinline__ void few_gate_up(const FewArgs& p, const void* wg, const void* wu,
-                                            const float* tg, const float* tu, int e, int f0,
-                                            int R, int tok, int row, int rows,
-                                            typename Op::Acc (&red)[kFewWaves][4][64]) {
-  using Acc = typename Op::Acc;
-  constexpr int ESZ = FewTraits<Op>::ESZ, PL = FewTraits<Op>::PLANES;
-  constexpr bool I8 = ESZ == 1;
-  constexpr int U = CT == 1 ? 4 : CT == 2 ? 2 : 1;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, quad = lane >> 4;
-  const size_t kbytes = static_cast<size_t>(p.d) * ESZ;
-  const int steps = static_cast<int>(kbytes / kStepBytes);
-  const int s0 = wave * steps / kFewWaves, s1 = (wave + 1) * steps / kFewWaves;
-  const size_t at = static_cast<size_t>(s0) * kStepBytes + quad * 16;
-  const char* w0 = static_cast<const char*>(r16 < 8 ? wg : wu) +
-                   (static_cast<size_t>(e) * p.F + f0 + (r16 & 7)) * kbytes + at;
-  const char* wp[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) wp[c] = w0 + 8 * c * kbytes;
-  const char* a = I8 ? reinterpret_cast<const char*>(p.xq) : static_cast<const char*>(p.x);
-  const char* ap[1] = {a + tok * kbytes + at};
-  Acc acc[CT][1];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) acc[c][0] = Acc{0, 0, 0, 0};
-  stream_dot<Op, CT, 1, U>(wp, ap, s1 - s0, acc);
-#pragma unroll
-  for (int c = 0; c < CT; ++c) red[wave][c][lane] = acc[c][0];
-  __syncthreads();
-  if (wave >= CT) return;
-  Acc v{0, 0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < kFewWaves; ++w) v += red[w][wave][lane];
-  const int f = f0 + 8 * wave + 4 * (quad & 1);
-  float hv[4];
-  float sx = 1.0f;
-  if (I8) sx = p.xs[tok];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float gt = static_cast<float>(v[i]);
-    if (I8) gt *= sx * (quad < 2 ? tg : tu)[static_cast<size_t>(e) * p.F + f + i];
-    const float up = __shfl_xor(gt, 32);  // lanes 0-31 hold gate, 32-63 up
-    hv[i] = gt / (1.0f + expf(-gt)) * up;
-  }
-  if (quad >= 2 || r16 >= R) return;
-  if (PL == 2) {  // h = hi + lo in bf16
-    bf16_t* hh = static_cast<bf16_t*>(p.h) + static_cast<size_t>(row) * p.F + f;
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bf16_t h0 = f32_to_bf16(hv[2 * i]), h1 = f32_to_bf16(hv[2 * i + 1]);
-      hi[i] = h0 | (static_cast<uint32_t>(h1) << 16);
-      lo[i] = f32_to_bf16(hv[2 * i] - bf16_to_f32(h0)) |
-              (static_cast<uint32_t>(f32_to_bf16(hv[2 * i + 1] - bf16_to_f32(h1))) << 16);
-    }
-    agent_store(reinterpret_cast<uint64_t*>(hh), hi[0] | (static_cast<uint64_t>(hi[1]) << 32));
-    agent_store(reinterpret_cast<uint64_t*>(hh + static_cast<size_t>(rows) * p.F),
-                lo[0] | (static_cast<uint64_t>(lo[1]) << 32));
-  } else {
-    uint64_t* hh = reinterpret_cast<uint64_t*>(static_cast<float*>(p.h) +
-                                               static_cast<size_t>(row) * p.F + f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      agent_store(hh + i, __float_as_uint(hv[2 * i]) |
-                              (static_cast<uint64_t>(__float_as_uint(hv[2 * i + 1])) << 32));
-  }
-}
+// Down units u0..u1-1 of a pass over entries e0..e0+ne-1: column u / ne of the
+// workgroup's columns, entry e0 + u % ne.
+template <class Acc, bool I8>
+struct DownWalk {
+  const FewPlan& plan;
+  float* ysum;             // [columns, T]
+  int T;
+  const char *w, *ws;      // routed and shared W_down at the pass's K offset
+  const float *t, *ts;     // 8-bit scales [E or S, d]
+  size_t kfull;
+  int d, n0, e0, ne, u0, n, stride, lane, se, base;
+  int lcol, lent, col, ent;
+  float gate = 0.0f, scale = 0.0f;
+  int tok = 0;
 
-template <class Op, typename Y, int S>
+  __device__ __forceinline__ DownWalk(const FewPlan& pl, float* ys, const FewArgs& p,
+                      size_t kf, size_t koff, int n0_, int e0_, int ne_, int u0_, int u1_, int st)
+      : plan(pl), ysum(ys), T(p.T), w(static_cast<const char*>(p.w_down) + koff),
+        ws(static_cast<const char*>(p.ws_down) + koff), t(p.t_down), ts(p.ts_down), kfull(kf),
+        d(p.d), n0(n0_), e0(e0_), ne(ne_), u0(u0_), n(u1_ - u0_), stride(st),
+        lane(threadIdx.x & 63), se(uniform(pl.shared_entries)), base(pl.first[e0_]) {
+    lcol = col = n > 0 ? u0 / ne : 0;
+    lent = ent = n > 0 ? u0 % ne : 0;
+  }
+  __device__ __forceinline__ int units() const { return n; }
+  __device__ __forceinline__ const char* row(int u) {
+    if (u > 0 && ++lent == ne) {
+      lent = 0;
+      ++lcol;
+    }
+    const int i = e0 + lent;
+    return (i < se ? ws : w) +
+           (static_cast<size_t>(uniform(plan.expert[i])) * d + n0 + lcol) * kfull;
+  }
+  __device__ __forceinline__ int enter(int u, int (&off)[kUnitRows]) {
+    if (u > 0 && ++ent == ne) {
+      ent = 0;
+      ++col;
+    }
+    const int i = e0 + ent, r0 = plan.first[i];
+    const int rows = uniform(plan.first[i + 1] - r0);
+#pragma unroll
+    for (int r = 0; r < kUnitRows; ++r)
+      off[r] = (r0 - base + (r < rows ? r : 0)) * stride + lane * 16;
+    const int mine = r0 + (lane < rows ? lane : 0);
+    gate = plan.gate[mine];
+    tok = plan.tok[mine];
+    if (I8) {
+      const int32_t* tp = reinterpret_cast<const int32_t*>(i < se ? ts : t) +
+                          static_cast<size_t>(uniform(plan.expert[i])) * d;
+      scale = __int_as_float(((const_words)tp)[n0 + col]);
+    }
+    return rows;
+  }
+  __device__ __forceinline__ void leave(int u, int nr, const Acc (&acc)[kUnitRows]) {
+    Acc mine{0};
+#pragma unroll
+    for (int r = 0; r < kUnitRows; ++r) {
+      if (r >= nr) break;
+      const Acc s = wave_total(acc[r]);
+      mine = lane == r ? s : mine;
+    }
+    if (lane < nr) {
+      float v = static_cast<float>(mine);
+      if (I8) v *= scale;
+      float* y = ysum + col * T + tok;
+      *y = fmaf(gate, v, *y);
+    }
+  }
+  // reads through the scalar cache do not count as vector loads
+  typedef const int32_t __attribute__((address_space(4)))* const_words;
+};
+
+// Work of one expert weight type.
+template <class Dot> struct FewTraits;
+template <> struct FewTraits<DotBf16> { static constexpr int ESZ = 2, PLANES = 2; };
+template <> struct FewTraits<DotF32> { static constexpr int ESZ = 4, PLANES = 1; };
+template <> struct FewTraits<DotI8> { static constexpr int ESZ = 1, PLANES = 1; };
+
+template <class Dot, typename Y, int S>
 __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
-  using Acc = typename Op::Acc;
-  constexpr int ESZ = FewTraits<Op>::ESZ, PL = FewTraits<Op>::PLANES;
+  using Acc = typename Dot::Acc;
+  constexpr int ESZ = FewTraits<Dot>::ESZ, PL = FewTraits<Dot>::PLANES;
   constexpr bool I8 = ESZ == 1;
+  __shared__ __attribute__((aligned(1024))) char pool[kPool];
   __shared__ FewPlan plan;
-  __shared__ FewLds<Op> lds;
   __shared__ int s_word;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r16 = lane & 15, quad = lane >> 4;
+  const int wave = uniform(tid >> 6);
   const int grid = gridDim.x;
-  const int T = p.T, tiles = p.F / 8;  // gate/up tiles per expert
+  const int T = p.T, F = p.F;
   const int pairs = T * kFewTopK, rows = pairs + S * T;
-  int32_t* chunk_flag = p.ctrl;                 // [grid]
-  int32_t* token_flag = p.ctrl + kFewGrid;      // [T]
+  int32_t* chunk_flag = p.ctrl;                    // [grid]
+  int32_t* token_flag = p.ctrl + kFewGrid;         // [T]
   int32_t* row_flag = token_flag + kFewMaxTokens;  // [rows] (8-bit weights)
-  int32_t* col_count = row_flag + rows;         // [d / 16]
   bool planned = false;
 
   if (tid == 0 && agent_load(chunk_flag + blockIdx.x) == kIdle) {
     if (blockIdx.x < T) agent_store(token_flag + blockIdx.x, kStarted);
     agent_store(chunk_flag + blockIdx.x, kStarted);
   }
-  // ---- gate/up: this workgroup's chunk, then any that nobody has started
-  int buf = 0;
+  plan_shared<S>(p, plan);
+  __syncthreads();
+
+  // ---- gate/up: this workgroup's chunk, then any that nobody has started.
+  // Passes over K of as many chunks of every token as `oper` holds.
+  const size_t kfull = static_cast<size_t>(p.d) * ESZ;
+  const int kall = static_cast<int>((kfull + kChunk - 1) / kChunk);
+  auto part_sums = reinterpret_cast<Acc(*)[2][kUnitRows]>(pool);
+  char* oper = pool + kPartBytes;
+  const int kpass = min((kall + 1) / 2 * 2, (kPool - kPartBytes) / kChunk / T / 2 * 2);
+  int staged = -1;  // first K chunk of the pass that oper holds
   int token = blockIdx.x < T ? static_cast<int>(blockIdx.x) : -1;  // to be selected here
   for (int chunk = blockIdx.x; chunk >= 0;
        chunk = wait_all(chunk_flag, grid, blockIdx.x, &s_word)) {
-    for (int part = S > 0 ? 0 : 1; part < 2;) {  // shared, then routed experts
+    for (int part = 0; part < 2;) {  // shared, then routed experts
       if (token >= 0) {
         if (wave == 0) few_select<S>(p, token, lane);
         mark_done(token_flag, token);
@@ -368,34 +518,62 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
       if (part == 1 && !planned) {
         token = wait_all(token_flag, T, 0, &s_word);
         if (token >= 0) continue;
-        few_plan(p, plan);
+        plan_routed<S>(p, plan);
         planned = true;
       }
-      const long long n = static_cast<long long>(part == 0 ? S : plan.active) * tiles;
-      const int t1 = static_cast<int>(n * (chunk + 1) / grid);
-      for (int t = static_cast<int>(n * chunk / grid); t < t1;) {
-        const int g = t / tiles, left = min(t1, (g + 1) * tiles) - t;
-        const int ct = left < 4 ? left : 4;
-        const bool shared = part == 0;
-        const int e = shared ? g : plan.expert[g];
-        const int R = shared ? T : plan.start[g + 1] - plan.start[g];
-        const int rr = r16 < R ? r16 : 0;  // spare columns repeat row 0
-        const int pair = shared ? 0 : plan.pair[plan.start[g] + rr];
-        const int row = shared ? pairs + g * T + rr : pair;
-        const int tok = shared ? rr : pair / kFewTopK;
-        const int f0 = (t - g * tiles) * 8;
-        const void* wg = shared ? p.ws_gate : p.w_gate;
-        const void* wu = shared ? p.ws_up : p.w_up;
-        const float* tg = shared ? p.ts_gate : p.t_gate;
-        const float* tu = shared ? p.ts_up : p.t_up;
-        // two sets of partial tiles in turn: one barrier per group
-        auto& red = lds.red[buf];
-        buf ^= 1;
-        if (ct == 4) few_gate_up<Op, 4>(p, wg, wu, tg, tu, e, f0, R, tok, row, rows, red);
-        else if (ct == 3) few_gate_up<Op, 3>(p, wg, wu, tg, tu, e, f0, R, tok, row, rows, red);
-        else if (ct == 2) few_gate_up<Op, 2>(p, wg, wu, tg, tu, e, f0, R, tok, row, rows, red);
-        else few_gate_up<Op, 1>(p, wg, wu, tg, tu, e, f0, R, tok, row, rows, red);
-        t += ct;
+      // columns of this chunk: the workgroups that select tokens have no share of
+      // the shared experts
+      const int ent0 = part == 0 ? 0 : plan.shared_entries;
+      const long long n = static_cast<long long>(part == 0 ? plan.shared_entries
+                                                           : plan.entries - ent0) * F;
+      const int share = part == 0 ? chunk - T : chunk, of = part == 0 ? grid - T : grid;
+      int c = share < 0 ? 0 : static_cast<int>(n * share / of);
+      const int cend = share < 0 ? 0 : static_cast<int>(n * (share + 1) / of);
+      for (; c < cend; c += kPartCols) {
+        const int c1 = min(c + kPartCols, cend);
+        for (int k0 = 0; k0 < kall; k0 += kpass) {
+          const int kbytes = static_cast<int>(min(kfull - static_cast<size_t>(k0) * kChunk,
+                                                  static_cast<size_t>(kpass) * kChunk));
+          if (staged != k0) {  // x of every token, zeros behind its last value
+            __syncthreads();
+            const char* x = I8 ? reinterpret_cast<const char*>(p.xq) : static_cast<const char*>(p.x);
+            const int pieces = kpass * (kChunk / 16);
+            for (int i = tid; i < T * pieces; i += kFewThreads) {
+              const int t = i / pieces, o = (i - t * pieces) * 16;
+              u32x4_t v{0, 0, 0, 0};
+              if (o < kbytes)
+                v = *reinterpret_cast<const u32x4_t*>(x + t * kfull +
+                                                      static_cast<size_t>(k0) * kChunk + o);
+              *reinterpret_cast<u32x4_t*>(oper + t * kpass * kChunk + o) = v;
+            }
+            staged = k0;
+          }
+          __syncthreads();
+          const int span = c1 - c;
+          GateWalk<Acc> walk(plan, part_sums, part == 0 ? p.ws_gate : p.w_gate,
+                             part == 0 ? p.ws_up : p.w_up, kfull,
+                             static_cast<size_t>(k0) * kChunk, F, c + span * wave / kFewWaves,
+                             c + span * (wave + 1) / kFewWaves, c, ent0, kpass * kChunk, k0 > 0);
+          stream_rows<Dot, 1>(walk, kbytes, oper, 0);
+        }
+        __syncthreads();
+        // h = silu(gate) * up
+        for (int i = tid; i < (c1 - c) * kUnitRows; i += kFewThreads) {
+          const int r = i / (c1 - c), j = i - r * (c1 - c);
+          const int ent = ent0 + (c + j) / F, f = (c + j) % F;
+          const int lr = plan.first[ent] + r;
+          if (lr >= plan.first[ent + 1]) continue;
+          float gt = static_cast<float>(part_sums[j][0][r]);
+          float up = static_cast<float>(part_sums[j][1][r]);
+          if (I8) {
+            const float sx = p.xs[plan.tok[lr]];
+            const size_t at = static_cast<size_t>(plan.expert[ent]) * F + f;
+            gt *= sx * (part == 0 ? p.ts_gate : p.t_gate)[at];
+            up *= sx * (part == 0 ? p.ts_up : p.t_up)[at];
+          }
+          agent_store(p.h + static_cast<size_t>(plan.hrow[lr]) * F + f,
+                      gt / (1.0f + expf(-gt)) * up);
+        }
       }
       ++part;
     }
@@ -410,11 +588,10 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     for (int r = static_cast<int>(blockIdx.x) < rows ? static_cast<int>(blockIdx.x) : -2;
          r != -1; r = wait_all(row_flag, rows, blockIdx.x % rows, &s_word)) {
       if (r < 0) continue;
-      const uint64_t* hr = reinterpret_cast<const uint64_t*>(static_cast<const float*>(p.h) +
-                                                             static_cast<size_t>(r) * p.F);
-      uint64_t* qr = reinterpret_cast<uint64_t*>(p.hq + static_cast<size_t>(r) * p.F);
+      const uint64_t* hr = reinterpret_cast<const uint64_t*>(p.h + static_cast<size_t>(r) * F);
+      uint64_t* qr = reinterpret_cast<uint64_t*>(p.hq + static_cast<size_t>(r) * F);
       const float s = quantize_row<kFewThreads>(
-          p.F, p.F,
+          F, F,
           [&](int c, int, float (&v)[8]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -429,92 +606,90 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     }
   }
 
-  // ---- down: unit u is block u / parts of 16 output columns, part u % parts.
-  // The steps of all contributors (shared experts, then the active ones in
-  // ascending order) form one list; part and wave take an equal share of it.
-  const int contributors = S + plan.active;
-  const size_t kbytes = static_cast<size_t>(p.F) * ESZ;
-  const int steps = static_cast<int>(kbytes / kStepBytes);
-  const long long list = static_cast<long long>(contributors) * steps;
-  const int slices = p.parts * kFewWaves;
-  for (int u = blockIdx.x; u < p.d / 16 * p.parts; u += grid) {
-    const int blk = u / p.parts, part = u % p.parts;
-    for (int i = tid; i < kFewWaves * kFewMaxTokens * 16; i += kFewThreads)
-      (&lds.ysum[0][0][0])[i] = 0.0f;
-    __syncthreads();
-    const int slice = part * kFewWaves + wave;
-    const long long l1 = list * (slice + 1) / slices;
-    for (long long l = list * slice / slices; l < l1;) {
-      const int ci = static_cast<int>(l / steps);
-      const int s0 = static_cast<int>(l - static_cast<long long>(ci) * steps);
-      const int n = static_cast<int>(min(static_cast<long long>(steps - s0), l1 - l));
-      const bool shared = ci < S;
-      const int g = ci - S;
-      const int e = shared ? ci : plan.expert[g];
-      const int R = shared ? T : plan.start[g + 1] - plan.start[g];
-      const int rr = r16 < R ? r16 : 0;
-      const int pair = shared ? 0 : plan.pair[plan.start[g] + rr];
-      const int row = shared ? pairs + ci * T + rr : pair;
-      const size_t at = static_cast<size_t>(s0) * kStepBytes + quad * 16;
-      const char* wp[1] = {static_cast<const char*>(shared ? p.ws_down : p.w_down) +
-                           (static_cast<size_t>(e) * p.d + blk * 16 + r16) * kbytes + at};
-      const char* hb = I8 ? reinterpret_cast<const char*>(p.hq) : static_cast<const char*>(p.h);
-      const char* ap[PL];
+  // ---- down: this workgroup's output columns, in passes over the contributors
+  // (and over K, for wide experts) of as many rows of h as `oper` holds.
+  const int n0 = static_cast<int>(static_cast<long long>(p.d) * blockIdx.x / grid);
+  const int cols = static_cast<int>(static_cast<long long>(p.d) * (blockIdx.x + 1) / grid) - n0;
+  const size_t ffull = static_cast<size_t>(F) * ESZ;
+  const int fall = static_cast<int>((ffull + kChunk - 1) / kChunk);
+  const int ywave = cols * T;  // floats of a wave's share of y
+  float* ysum = reinterpret_cast<float*>(pool);
+  const int ybytes = (kFewWaves * ywave * 4 + kChunk - 1) / kChunk * kChunk;
+  oper = pool + ybytes;
+  // every entry fits a pass: 8 rows of fpass chunks
+  const int fpass = min((fall + 1) / 2 * 2, (kPool - ybytes) / kChunk / PL / kUnitRows / 2 * 2);
+  const int stride = fpass * kChunk * PL;  // of a row of h in oper
+  const int capacity = (kPool - ybytes) / stride;
+  for (int i = tid; i < kFewWaves * ywave; i += kFewThreads) ysum[i] = 0.0f;
+  for (int i = tid; i < rows; i += kFewThreads) {
+    const int hr = plan.hrow[i], t = plan.tok[i];
+    const int slot = hr < pairs ? hr % kFewTopK : kFewTopK + (hr - pairs) / T;
+    float g = agent_load(p.gates + t * (kFewTopK + S) + slot);
+    if (I8) g *= agent_load(p.hs + hr);
+    plan.gate[i] = g;
+  }
+  for (int k0 = 0; k0 < fall; k0 += fpass) {
+    const int kbytes = static_cast<int>(min(ffull - static_cast<size_t>(k0) * kChunk,
+                                            static_cast<size_t>(fpass) * kChunk));
+    for (int e0 = 0; e0 < plan.entries;) {
+      const int first = plan.first[e0];
+      int e1 = e0 + 1;
+      while (e1 < plan.entries && plan.first[e1 + 1] - first <= capacity) ++e1;
+      const int n = plan.first[e1] - first;
+      __syncthreads();  // the pass before is done with oper
+      // 8 values of K at a time, zeros behind the last
+      const int pieces = fpass * kChunk / (8 * ESZ);
+      for (int i = tid; i < n * pieces; i += kFewThreads) {
+        const int r = i / pieces, k = (i - r * pieces) * 8;
+        char* at = oper + r * stride + k * ESZ;
+        const size_t src = static_cast<size_t>(plan.hrow[first + r]) * F +
+                           static_cast<size_t>(k0) * kChunk / ESZ + k;
+        const bool in = k * ESZ < kbytes;
+        if (I8) {
+          *reinterpret_cast<uint64_t*>(at) =
+              in ? agent_load(reinterpret_cast<const uint64_t*>(p.hq + src)) : 0;
+        } else {
+          uint64_t v[4] = {0, 0, 0, 0};
+          if (in) {
 #pragma unroll
-      for (int t = 0; t < PL; ++t)
-        ap[t] = hb + (static_cast<size_t>(t) * rows + row) * kbytes + at;
-      Acc acc[1][PL];
+            for (int q = 0; q < 4; ++q)
+              v[q] = agent_load(reinterpret_cast<const uint64_t*>(p.h + src) + q);
+          }
+          if constexpr (PL == 2) {  // h = hi + lo in bf16
+            u32x4_t hi, lo;
 #pragma unroll
-      for (int t = 0; t < PL; ++t) acc[0][t] = Acc{0, 0, 0, 0};
-      stream_dot<Op, 1, PL, PL == 2 ? 3 : 4, true>(wp, ap, n, acc);
-      if (r16 < R) {
-        const int tok = shared ? rr : pair / kFewTopK;
-        const int slot = shared ? kFewTopK + ci : pair % kFewTopK;
-        float gate = agent_load(p.gates + tok * (kFewTopK + S) + slot);
-        if (I8) gate *= agent_load(p.hs + row);
-        float4* ys = reinterpret_cast<float4*>(&lds.ysum[wave][tok][4 * quad]);
-        float4 o = *ys;
-        float v[4];
+            for (int q = 0; q < 4; ++q) {
+              const float a = __uint_as_float(static_cast<uint32_t>(v[q]));
+              const float b = __uint_as_float(static_cast<uint32_t>(v[q] >> 32));
+              const bf16_t ah = f32_to_bf16(a), bh = f32_to_bf16(b);
+              hi[q] = ah | (static_cast<uint32_t>(bh) << 16);
+              lo[q] = f32_to_bf16(a - bf16_to_f32(ah)) |
+                      (static_cast<uint32_t>(f32_to_bf16(b - bf16_to_f32(bh))) << 16);
+            }
+            *reinterpret_cast<u32x4_t*>(at) = hi;
+            *reinterpret_cast<u32x4_t*>(at + fpass * kChunk) = lo;
+          } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = static_cast<float>(acc[0][0][i]);
-          if (PL == 2) v[i] += static_cast<float>(acc[0][PL - 1][i]);
-          if (I8)
-            v[i] *= (shared ? p.ts_down : p.t_down)[static_cast<size_t>(e) * p.d + blk * 16 +
-                                                    4 * quad + i];
+            for (int q = 0; q < 4; ++q) reinterpret_cast<uint64_t*>(at)[q] = v[q];
+          }
         }
-        o.x = fmaf(gate, v[0], o.x);
-        o.y = fmaf(gate, v[1], o.y);
-        o.z = fmaf(gate, v[2], o.z);
-        o.w = fmaf(gate, v[3], o.w);
-        *ys = o;
       }
-      l += n;
+      __syncthreads();
+      const int ne = e1 - e0, units = cols * ne;
+      DownWalk<Acc, I8> walk(plan, ysum + wave * ywave, p, ffull, static_cast<size_t>(k0) * kChunk, n0,
+                             e0, ne, units * wave / kFewWaves, units * (wave + 1) / kFewWaves,
+                             stride);
+      stream_rows<Dot, PL>(walk, kbytes, oper, fpass * kChunk);
+      e0 = e1;
     }
-    __syncthreads();
-    const int t = tid >> 4, c = blk * 16 + (tid & 15);  // 16 T <= 256 threads
+  }
+  __syncthreads();
+  for (int i = tid; i < T * cols; i += kFewThreads) {
+    const int t = i / cols, c = i - t * cols;
     float v = 0.0f;
-    if (t < T) {
 #pragma unroll
-      for (int w = 0; w < kFewWaves; ++w) v += lds.ysum[w][t][tid & 15];
-    }
-    if (p.parts > 1) {
-      if (t < T) agent_store(p.ypart + (static_cast<size_t>(part) * T + t) * p.d + c, v);
-      drain_stores();
-      if (tid == 0)
-        s_word = __hip_atomic_fetch_add(col_count + blk, 1, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT) == p.parts - 1;
-      __syncthreads();
-      if (s_word && t < T) {
-        v = 0.0f;
-        for (int q = 0; q < p.parts; ++q)
-          v += agent_load(p.ypart + (static_cast<size_t>(q) * T + t) * p.d + c);
-        ActTraits<Y>::store(static_cast<Y*>(p.y) + static_cast<size_t>(t) * p.d + c, v);
-      }
-      __syncthreads();
-    } else if (t < T) {
-      ActTraits<Y>::store(static_cast<Y*>(p.y) + static_cast<size_t>(t) * p.d + c, v);
-    }
+    for (int w = 0; w < kFewWaves; ++w) v += ysum[w * ywave + c * T + t];
+    ActTraits<Y>::store(static_cast<Y*>(p.y) + static_cast<size_t>(t) * p.d + n0 + c, v);
   }
 }
 
@@ -530,34 +705,15 @@ static void route(const FewArgs& a, int ctrl, hipStream_t st) {
   else few_route_kernel<X, 16, INT8><<<grid, 256, 0, st>>>(a, ctrl);
 }
 
-template <class Op, typename Y>
+template <class Dot, typename Y>
 static void experts(const FewArgs& a, hipStream_t st) {
-  if (a.S == 0) few_ffn_kernel<Op, Y, 0><<<kFewGrid, kFewThreads, 0, st>>>(a);
-  else if (a.S == 1) few_ffn_kernel<Op, Y, 1><<<kFewGrid, kFewThreads, 0, st>>>(a);
-  else few_ffn_kernel<Op, Y, 2><<<kFewGrid, kFewThreads, 0, st>>>(a);
+  if (a.S == 0) few_ffn_kernel<Dot, Y, 0><<<kFewGrid, kFewThreads, 0, st>>>(a);
+  else if (a.S == 1) few_ffn_kernel<Dot, Y, 1><<<kFewGrid, kFewThreads, 0, st>>>(a);
+  else few_ffn_kernel<Dot, Y, 2><<<kFewGrid, kFewThreads, 0, st>>>(a);
 }
 
-// Parts of the column blocks: enough that the last round of workgroups is
-// nearly full (a narrow layer has fewer blocks than there are workgroups).
-static int column_parts(int d) {
-  const int blocks = d / 16;
-  int best = 1;
-  double least = 0.0;
-  for (int q = 1; q <= kFewMaxParts; ++q) {
-    const double rounds = static_cast<double>((blocks * q + kFewGrid - 1) / kFewGrid);
-    const double cost = rounds / q;  // of one round over whole blocks
-    if (q == 1 || cost < 0.9 * least) {
-      best = q;
-      least = cost;
-    }
-  }
-  return best;
-}
-
-hipError_t launch_few(const FewArgs& args, bool act_bf16, FewWeight w, hipStream_t st) {
-  if (args.T == 0) return hipSuccess;
-  FewArgs a = args;
-  a.parts = column_parts(a.d);
+hipError_t launch_few(const FewArgs& a, bool act_bf16, FewWeight w, hipStream_t st) {
+  if (a.T == 0) return hipSuccess;
   Shape s;
   s.T = a.T;
   s.E = a.E;
@@ -575,12 +731,12 @@ hipError_t launch_few(const FewArgs& args, bool act_bf16, FewWeight w, hipStream
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (w == FewWeight::kInt8) {
-    if (act_bf16) experts<OpI8, bf16_t>(a, st);
-    else experts<OpI8, float>(a, st);
+    if (act_bf16) experts<DotI8, bf16_t>(a, st);
+    else experts<DotI8, float>(a, st);
   } else if (w == FewWeight::kBf16) {
-    experts<OpBf16, bf16_t>(a, st);
+    experts<DotBf16, bf16_t>(a, st);
   } else {
-    experts<OpF32, float>(a, st);
+    experts<DotF32, float>(a, st);
   }
   return hipGetLastError();
 }

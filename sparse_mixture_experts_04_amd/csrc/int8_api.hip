@@ -41,7 +41,7 @@ moe_status check_few_desc(const moe_desc* d) {
   const moe_status st = check_ffn_desc(d);
   if (st != MOE_OK) return st;
   if (d->weight == MOE_MXFP4 || d->T > kFewMaxTokens || d->capacity_factor != 0.0f ||
-      d->d > 65536 || d->F > 65536)
+      d->d > kFewMaxWidth || d->F > kFewMaxWidth)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -86,7 +86,7 @@ FfnInt8Ws carve_ffn_int8(Carver& c, const Shape& s) {
 // Carves the workspace into a.
 void carve_few(Carver& c, const Shape& s, FewArgs& a) {
   const size_t rows = static_cast<size_t>(kFewTopK + s.S) * s.T;
-  a.z = c.take<double>(static_cast<size_t>(s.T) * (s.E + s.S));
+  a.zs = c.take<double2>(static_cast<size_t>(s.T) * (s.E + s.S));
   a.ctrl = c.take<int32_t>(few_ctrl_ints(s));
   a.topk = c.take<int32_t>(static_cast<size_t>(s.T) * kFewTopK);
   a.gates = c.take<float>(static_cast<size_t>(s.T) * (kFewTopK + s.S));
@@ -95,7 +95,6 @@ void carve_few(Carver& c, const Shape& s, FewArgs& a) {
   a.h = c.take<float>(rows * s.F);
   a.hq = c.take<int8_t>(rows * s.F);
   a.hs = c.take<float>(rows);
-  a.ypart = c.take<float>(static_cast<size_t>(kFewMaxParts) * s.T * s.d);
 }
 
 size_t few_ws_bytes(const Shape& s) {

@@ -1,0 +1,168 @@
+// Dot products of streamed weight rows with a few activation rows in LDS.
+//
+// A wave reads weight rows ("units") as contiguous KiB pieces ("chunks": 16
+// bytes per lane), one after another, and multiplies each with the 1 to 8
+// activation rows its expert holds; lane partial sums are added over the wave
+// at a unit's end.  Nothing is shared between waves, so there is no barrier in
+// the stream, and the units split evenly over any number of waves.
+//
+// What bounds it is the rate of the weight loads.  Reading a row in whole KiB
+// pieces matters: the matrix cores' fragment order, 16 rows at a time in pieces
+// of 64 or 128 bytes, reached 2 to 4 TB/s on the same weights.  A chunk costs 4
+// dot instructions per activation row whatever the type (v_dot2_f32_bf16,
+// v_dot4_i32_i8, v_fma_f32), 16 cycles of a SIMD's time; at 8 rows that is a
+// third of the time the chunk takes to arrive.
+//
+// kRing blocks of kBlock chunks are held in registers, all but one of them in
+// flight.  Loads are issued unconditionally (past the last unit the last block
+// is read again) so that the compiler can count them.
+#pragma once
+
+#include <type_traits>
+
+#include "select.h"
+#include "stream.h"
+
+namespace moe {
+
+constexpr int kChunk = 1024;     // bytes of a row per load instruction
+constexpr int kBlock = 2;        // chunks per block
+constexpr int kRing = 4;         // blocks in registers
+constexpr int kUnitRows = 8;     // activation rows of a unit, at most
+
+struct DotBf16 {
+  using Acc = float;
+  __device__ static void mul(u32x4_t w, u32x4_t x, float& a) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // through scalars: a bit cast of a vector's element takes element 0
+      const uint32_t wi = w[i], xi = x[i];
+      a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, wi),
+                                          __builtin_bit_cast(bf16x2_t, xi), a, false);
+    }
+  }
+};
+struct DotF32 {
+  using Acc = float;
+  __device__ static void mul(u32x4_t w, u32x4_t x, float& a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = fmaf(__uint_as_float(w[i]), __uint_as_float(x[i]), a);
+  }
+};
+struct DotI8 {
+  using Acc = int32_t;
+  __device__ static void mul(u32x4_t w, u32x4_t x, int32_t& a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a = __builtin_amdgcn_sdot4(static_cast<int>(w[i]), static_cast<int>(x[i]), a, false);
+  }
+};
+
+// Sum over the wave, the same on every lane, in a fixed order.
+template <class Acc>
+__device__ __forceinline__ Acc wave_total(Acc v) {
+  static_assert(sizeof(Acc) == 4, "32-bit sums");
+  const int lane = threadIdx.x & 63;
+  auto x = [&](auto step) __attribute__((always_inline)) {
+    v += __builtin_bit_cast(Acc, lane_xchg<decltype(step)::value>(__builtin_bit_cast(int, v), lane));
+  };
+  x(std::integral_constant<int, 0>{});
+  x(std::integral_constant<int, 1>{});
+  x(std::integral_constant<int, 2>{});
+  x(std::integral_constant<int, 3>{});
+  x(std::integral_constant<int, 4>{});
+  x(std::integral_constant<int, 5>{});
+  return v;
+}
+
+// Streams the units of one wave.  Walk tells where they are and takes the sums
+// (everything but the row offsets is the same on every lane):
+//   units()          number of units
+//   row(u)           address of the row's first byte of this pass; called with
+//                    u = 0, 1, 2, ... in order, each once
+//   enter(u, off)    before unit u is multiplied, in order: sets the LDS offsets
+//                    of its activation rows (lane's 16 bytes included) and
+//                    returns their number
+//   leave(u, n, acc) takes the n lane sums of unit u
+// kbytes: bytes of a row in this pass; planes of activation rows lie
+// plane_bytes apart (their sums are added).
+template <class Dot, int PL, class Walk>
+__device__ __forceinline__ void stream_rows(Walk& walk, int kbytes, const char* oper,
+                                            int plane_bytes) {
+  using Acc = typename Dot::Acc;
+  const int units = walk.units();
+  if (units <= 0) return;
+  const int lane = threadIdx.x & 63;
+  const int nkb = (kbytes + kBlock * kChunk - 1) / (kBlock * kChunk);
+  const int total = units * nkb;
+  u32x4_t w[kRing][kBlock];
+
+  // load side
+  int lu = 0, lk = 0;
+  const char* lrow = walk.row(0);
+  auto load = [&](u32x4_t (&f)[kBlock]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      int o = (lk * kBlock + j) * kChunk + lane * 16;
+      o = o < kbytes ? o : 0;  // past the row: any byte of it (times zero)
+      f[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(lrow + o));
+    }
+    if (lk + 1 < nkb) {
+      ++lk;
+    } else if (lu + 1 < units) {
+      ++lu;
+      lk = 0;
+      lrow = walk.row(lu);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) load(w[i]);
+
+  // multiply side
+  int cu = 0, ck = 0, rows = 0;
+  int off[kUnitRows];
+  Acc acc[kUnitRows];
+#pragma unroll
+  for (int r = 0; r < kUnitRows; ++r) {
+    acc[r] = Acc{0};
+    off[r] = 0;
+  }
+  rows = walk.enter(0, off);
+  for (int b = 0; b < total; b += kRing) {
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) {
+      if (b + i >= total) break;
+      load(w[(i + kRing - 1) % kRing]);
+      auto mul = [&](auto nr) __attribute__((always_inline)) {
+        constexpr int N = decltype(nr)::value;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+#pragma unroll
+          for (int j = 0; j < kBlock; ++j)
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+              Dot::mul(w[i][j],
+                       *reinterpret_cast<const u32x4_t*>(oper + off[r] + p * plane_bytes +
+                                                         (ck * kBlock + j) * kChunk),
+                       acc[r]);
+          // no more than two rows' operands in registers at once
+          if (r & 1) __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if (rows == 1) mul(std::integral_constant<int, 1>{});
+      else if (rows == 2) mul(std::integral_constant<int, 2>{});
+      else if (rows <= 4) mul(std::integral_constant<int, 4>{});
+      else mul(std::integral_constant<int, 8>{});
+      if (++ck == nkb) {
+        walk.leave(cu, rows, acc);
+        ck = 0;
+#pragma unroll
+        for (int r = 0; r < kUnitRows; ++r) acc[r] = Acc{0};
+        if (++cu < units) rows = walk.enter(cu, off);
+      }
+    }
+  }
+}
+
+}  // namespace moe

@@ -112,7 +112,7 @@ def test_forward_few_checks():
     need = size_of(size, d)[1]
     assert need > 0 and size(ref(d), None) == 1
     for kw, code in ((dict(T=17), 5), (dict(capacity_factor=1.25), 5), (dict(weight=L.MXFP4), 5),
-                     (dict(d=384), 5), (dict(F=64), 5), (dict(d=65536 + 256), 5),
+                     (dict(d=384), 5), (dict(F=64), 5), (dict(d=16384 + 256), 5),
                      (dict(k=8), 5), (dict(T=-1), 2), (dict(act=L.F32), 3),
                      (dict(gate_scale=0.0), 2), (dict(T=16), 0), (dict(S=0), 0), (dict(T=0), 0)):
         assert size_of(size, desc(**kw))[0] == code, kw
