@@ -37,22 +37,14 @@ __device__ __forceinline__ int32_t sload(const int32_t* base, int idx) {
 // XCD share both activation and weight tiles.
 constexpr int kBand = 8;
 
-// balanced: a group of L rows in t row tiles gets tiles of
-// base = 32 * ceil(L / (32 t)) rows (the last one the rest, at least one
-// row); otherwise row tile m starts at m * MT.
-__device__ __forceinline__ Item decode_item(long long it, const int* ts, int G, int n_tiles,
-                                            int MT, const int32_t* __restrict__ offsets, int T,
-                                            int E, bool balanced = false) {
-  int lo = 0, hi = G;  // find last g with ts[g] * n_tiles <= it
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<long long>(ts[mid]) * n_tiles <= it) lo = mid;
-    else hi = mid;
-  }
+// Item `it`, which lies in group g of grows rows.
+__device__ __forceinline__ Item place_item(long long it, const int* ts, int g, int n_tiles, int MT,
+                                           int grows, bool balanced) {
   Item r;
-  r.g = lo;
-  const int mt = ts[lo + 1] - ts[lo];
-  const int local = static_cast<int>(it - static_cast<long long>(ts[lo]) * n_tiles);
+  r.g = g;
+  r.grows = grows;
+  const int mt = ts[g + 1] - ts[g];
+  const int local = static_cast<int>(it - static_cast<long long>(ts[g]) * n_tiles);
   const int band = mt < kBand ? mt : kBand;
   const int full = mt / band;
   const int in_full = full * band * n_tiles;
@@ -68,12 +60,27 @@ __device__ __forceinline__ Item decode_item(long long it, const int* ts, int G, 
     r.n = rem / last;
     m = full * band + rem % last;
   }
-  r.grows = lo < E ? offsets[lo + 1] - offsets[lo] : T;
-  const int base = balanced ? (r.grows + 32 * mt - 1) / (32 * mt) * 32 : MT;
+  const int base = balanced ? (grows + 32 * mt - 1) / (32 * mt) * 32 : MT;
   r.m0 = m * base;
-  const int left = r.grows - r.m0;
+  const int left = grows - r.m0;
   r.rows = left < base ? left : base;
   return r;
+}
+
+// balanced: a group of L rows in t row tiles gets tiles of
+// base = 32 * ceil(L / (32 t)) rows (the last one the rest, at least one
+// row); otherwise row tile m starts at m * MT.
+__device__ __forceinline__ Item decode_item(long long it, const int* ts, int G, int n_tiles,
+                                            int MT, const int32_t* __restrict__ offsets, int T,
+                                            int E, bool balanced = false) {
+  int lo = 0, hi = G;  // find last g with ts[g] * n_tiles <= it
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<long long>(ts[mid]) * n_tiles <= it) lo = mid;
+    else hi = mid;
+  }
+  return place_item(it, ts, lo, n_tiles, MT,
+                    lo < E ? offsets[lo + 1] - offsets[lo] : T, balanced);
 }
 
 struct FfnArgs {

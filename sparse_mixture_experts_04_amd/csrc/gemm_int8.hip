@@ -3,6 +3,7 @@
 //
 // The sums are exact in int32 (K <= 131072), so the only rounding is the
 // scaling in fp32 and the store.
+#include "big_tile.h"
 #include "int8.h"
 #include "stream.h"
 
@@ -176,11 +177,259 @@ __global__ __launch_bounds__(256) void gemm_int8_stream_kernel(Int8Args p) {
   }
 }
 
-size_t gemm_int8_plan_ints(int groups) { return static_cast<size_t>(groups) + 64; }
+// ------------------------------------------------------------ large batches
+//
+// The bf16 experts' tile and K loop (big_tile.h) on 8-bit operands: the same
+// bytes per step hold twice the K, and the int8 matrix instruction does twice
+// the products in the same cycles.  Row tiles of up to 256 rows (or 128 where
+// groups hold few) x 256 weight rows; persistent workgroups take items from
+// per-XCD counters.
+using BigI8 = BigShape<256, 32, 3, 6, MmaI8>;
+using MidI8 = BigShape<128, 64, 3, 3, MmaI8>;
+static_assert(BigI8::LDS_ELEMS * 2 <= 147456 && MidI8::LDS_ELEMS * 2 <= 147456, "LDS");
 
-hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, hipStream_t st) {
-  (void)plan;
-  if (a.M == 0 && (a.S == 0 || a.T == 0)) return hipSuccess;
+constexpr int kPlanGroups = kInt8MaxGroups + 2;
+
+// Plan in the workspace: row tiles as an exclusive prefix over the groups
+// [kPlanGroups + 1], first rows and row counts [kPlanGroups each], then the work
+// counters of up to two products over the same rows.
+constexpr int kPlanLo = kPlanGroups + 1, kPlanRows = kPlanLo + kPlanGroups,
+              kPlanCtr = kPlanRows + kPlanGroups, kPlanInts = kPlanCtr + 2 * kXcds;
+
+__global__ __launch_bounds__(512) void int8_plan_kernel(Int8Args p, int mt,
+                                                        int32_t* __restrict__ plan) {
+  __shared__ int sc[512];
+  const int g = threadIdx.x, G = p.E + p.S;
+  int lo = 0, n = 0;
+  if (g < G) group_rows(p, g, lo, n);
+  const int nt = (n + mt - 1) / mt;
+  sc[g] = nt;
+  __syncthreads();
+  for (int off = 1; off < 512; off <<= 1) {
+    const int v = g >= off ? sc[g - off] : 0;
+    __syncthreads();
+    sc[g] += v;
+    __syncthreads();
+  }
+  if (g < G) {
+    plan[g] = sc[g] - nt;
+    plan[kPlanLo + g] = lo;
+    plan[kPlanRows + g] = n;
+  }
+  if (g == G - 1) plan[G] = sc[g];
+  if (g < 2 * kXcds) plan[kPlanCtr + g] = 0;
+}
+
+// 4 consecutive values of a scale row of n values, from column c on (0 past its
+// end).
+__device__ __forceinline__ void scale4(const float* t, int c, int n, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = c + i < n ? t[c + i] : 0.0f;
+}
+
+template <class C, bool GATED, bool OUT_BF16>
+__global__ __launch_bounds__(512, 1) void gemm_int8_big_kernel(Int8Args p,
+                                                               const int32_t* __restrict__ plan,
+                                                               int32_t* counters) {
+  __shared__ __attribute__((aligned(1024))) bf16_t lds[C::LDS_ELEMS];
+  __shared__ int ts[kPlanGroups + 1], glo[kPlanGroups], grows[kPlanGroups];
+  __shared__ long long s_item;
+  bf16_t* sA[C::NSA];
+  bf16_t* sB[C::NSB];
+#pragma unroll
+  for (int i = 0; i < C::NSA; ++i) sA[i] = lds + i * C::A_STAGE;
+#pragma unroll
+  for (int i = 0; i < C::NSB; ++i) sB[i] = lds + C::NSA * C::A_STAGE + i * C::B_STAGE;
+  constexpr int NOUT = GATED ? C::NB / 2 : C::NB;   // output columns of a tile
+  constexpr int OB = OUT_BF16 ? 2 : 4;              // bytes of an output value
+  // the staged output tile; fp32 outputs of a whole tile do not fit and go
+  // straight from the registers
+  constexpr bool STAGED = C::MT * NOUT * OB <= C::LDS_ELEMS * 2;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int G = p.E + p.S;
+  for (int g = tid; g <= G; g += C::THREADS) {
+    ts[g] = plan[g];
+    if (g < G) {
+      glo[g] = plan[kPlanLo + g];
+      grows[g] = plan[kPlanRows + g];
+    }
+  }
+  __syncthreads();
+  const int n_tiles = (p.N + NOUT - 1) / NOUT;
+  const long long total = static_cast<long long>(ts[G]) * n_tiles;
+  const int xcd = blockIdx.x % kXcds;
+  const int kld = p.Kp / 2;  // row length in 16-bit units
+  const int nk = kld / C::BK;
+  const size_t wstride = static_cast<size_t>(p.N) * kld;
+  const int lrow = lane / C::CPR;
+  const bf16_t* A = reinterpret_cast<const bf16_t*>(p.a);
+
+  for (;;) {
+    if (tid == 0) s_item = claim_item(counters, xcd, total);
+    __syncthreads();
+    const long long gitem = s_item;
+    if (gitem < 0) break;
+    int g = 0;
+    for (int hi = G; hi - g > 1;) {
+      const int mid = (g + hi) >> 1;
+      if (static_cast<long long>(ts[mid]) * n_tiles <= gitem) g = mid;
+      else hi = mid;
+    }
+    const Item item = place_item(gitem, ts, g, n_tiles, C::MT, grows[g], true);
+    const bool routed = g < p.E;
+    const int ge = routed ? g : g - p.E;
+    const int row0 = routed ? glo[g] : 0;
+    // row of a and of its scale for tile row r
+    auto source = [&](int r) -> long long {
+      const int rr = item.m0 + (r < item.rows ? r : item.rows - 1);
+      if (!routed) return GATED ? rr : static_cast<long long>(p.M) + static_cast<long long>(ge) * p.T + rr;
+      return GATED ? clampi(p.sorted_pair[row0 + rr] / p.k, 0, p.T - 1) : row0 + rr;
+    };
+    BigCtx<C> t;
+    if (wm == 1) {
+#pragma unroll
+      for (int q = 0; q < C::LPW_A; ++q) {
+        const int j = wn * C::LPW_A + q;
+        t.src[q] = A + source(j * C::RPL + lrow) * kld + src_chunk<C>(lane, j);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < C::LPW_B; ++q) {
+        const int j = wn * C::LPW_B + q;
+        const int R = j * C::RPL + lrow;  // LDS B row
+        const int cg = R >> 6, rl = R & 63;
+        const bool up = GATED && rl >= 32;
+        const int8_t* base = up ? (routed ? p.w1 : p.ws1) : (routed ? p.w0 : p.ws0);
+        int col = GATED ? item.n * NOUT + cg * 32 + (rl & 31) : item.n * NOUT + R;
+        col = col < p.N ? col : p.N - 1;
+        t.src[q] = reinterpret_cast<const bf16_t*>(base) + ge * wstride +
+                   static_cast<size_t>(col) * kld + src_chunk<C>(lane, j);
+      }
+    }
+    typename C::Acc acc[C::BM][C::BN];
+#pragma unroll
+    for (int i = 0; i < C::BM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::BN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    const int nblk = (item.rows + 31) >> 5;
+    const int nv = min((nblk - wm + 1) >> 1, C::BM);
+    if (wm == 0) big_kloop_nv<C, GATED, 0, C::BM>(t, nk, sA, sB, wave, lane, nv, acc);
+    else big_kloop_nv<C, GATED, 1, C::BM>(t, nk, sA, sB, wave, lane, nv, acc);
+    wait_vm<0>();
+    __syncthreads();
+
+    // ---- epilogue: block (i, j) holds the transposed product: lane l -> tile
+    // row (2i + wm) * 32 + l % 32, registers 4q..4q+3 -> output columns
+    // 8q + 4 (l / 32) + 0..3 of column block j (GATED: block 0 gate, 1 up).
+    // Staged: 16-byte chunk c of row r in slot c ^ (r % CPR) of the LDS tile.
+    const float* t0 = (routed ? p.t0 : p.ts0) + static_cast<size_t>(ge) * p.N;
+    const float* t1 = GATED ? (routed ? p.t1 : p.ts1) + static_cast<size_t>(ge) * p.N : nullptr;
+    char* out = static_cast<char*>(routed ? p.out : p.out_shared);
+    const size_t orow0 = routed ? static_cast<size_t>(row0) + item.m0
+                                : static_cast<size_t>(ge) * p.T + item.m0;
+    constexpr int CPR = NOUT * OB / 16;
+    char* tile = reinterpret_cast<char*>(lds);
+    float sr[C::BM];
+#pragma unroll
+    for (int i = 0; i < C::BM; ++i) sr[i] = p.a_scale[source((2 * i + wm) * 32 + (lane & 31))];
+    constexpr int JN = GATED ? 1 : C::BN;
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = (GATED ? wn * 32 : wn * 64 + j * 32) + 8 * q + 4 * (lane >> 5);
+        const int col = item.n * NOUT + c;
+        float s0[4], s1[4];
+        scale4(t0, col, p.N, s0);
+        if (GATED) scale4(t1, col, p.N, s1);
+#pragma unroll
+        for (int i = 0; i < C::BM; ++i) {
+          const int row = (2 * i + wm) * 32 + (lane & 31);
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = static_cast<float>(acc[i][j][4 * q + e]) * (sr[i] * s0[e]);
+            if (GATED) {
+              const float up = static_cast<float>(acc[i][1][4 * q + e]) * (sr[i] * s1[e]);
+              v[e] = v[e] / (1.0f + expf(-v[e])) * up;
+            }
+          }
+          if constexpr (STAGED && OUT_BF16) {
+            const uint32_t w0 = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+            const uint32_t w1 = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+            *reinterpret_cast<uint2*>(tile + row * NOUT * OB +
+                                      (((c >> 3) ^ (row & (CPR - 1))) << 4) + (c & 4) * 2) =
+                make_uint2(w0, w1);
+          } else if constexpr (STAGED) {
+            *reinterpret_cast<float4*>(tile + row * NOUT * OB +
+                                       (((c >> 2) ^ (row & (CPR - 1))) << 4)) =
+                make_float4(v[0], v[1], v[2], v[3]);
+          } else if (row < item.rows) {
+            float* o = reinterpret_cast<float*>(out) + (orow0 + row) * p.N + col;
+            if (p.N % 4 == 0 && col + 4 <= p.N) {
+              *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (col + e < p.N) o[e] = v[e];
+            }
+          }
+        }
+      }
+    }
+    if constexpr (STAGED) {
+      __syncthreads();
+      constexpr int PER = 16 / OB;  // values of a chunk
+      const int col0 = item.n * NOUT;
+      const bool whole = p.N % PER == 0;  // rows of y start on 16 bytes
+      for (int c = tid; c < item.rows * CPR; c += C::THREADS) {
+        const int row = c / CPR, ch = c % CPR;
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + row * NOUT * OB +
+                                                        ((ch ^ (row & (CPR - 1))) << 4));
+        const int col = col0 + ch * PER;
+        char* o = out + ((orow0 + row) * p.N + col) * OB;
+        if (whole) {
+          if (col < p.N) *reinterpret_cast<uint4*>(o) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            if (col + e >= p.N) break;
+            if (OUT_BF16) reinterpret_cast<bf16_t*>(o)[e] = static_cast<bf16_t>(w[e / 2] >> (16 * (e & 1)));
+            else reinterpret_cast<uint32_t*>(o)[e] = w[e % 4];
+          }
+        }
+      }
+    }
+  }
+}
+
+template <class C>
+static hipError_t run_big(const Int8Args& a, bool gated, const int32_t* plan, int32_t* ctr,
+                          hipStream_t st) {
+  const int grid = (device_cus_big() + kXcds - 1) / kXcds * kXcds;
+  if (gated) gemm_int8_big_kernel<C, true, false><<<grid, C::THREADS, 0, st>>>(a, plan, ctr);
+  else if (a.out_bf16) gemm_int8_big_kernel<C, false, true><<<grid, C::THREADS, 0, st>>>(a, plan, ctr);
+  else gemm_int8_big_kernel<C, false, false><<<grid, C::THREADS, 0, st>>>(a, plan, ctr);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ host
+
+size_t gemm_int8_plan_ints() { return kPlanInts; }
+
+// Rows of a row tile, by the mean rows of a group: 0 for the stream kernel.
+static int row_tile(const Int8Args& a) {
+  const long long mean = a.M / (a.E > 0 ? a.E : 1);
+  return mean < 48 ? 0 : mean < 160 ? 128 : 256;
+}
+
+static hipError_t run_stream(const Int8Args& a, bool gated, hipStream_t st) {
   const int nout = gated ? 16 : 32;
   // upper bound of the items: every group's last row tile may be partial
   const long long mean = a.M / (a.E > 0 ? a.E : 1);
@@ -200,6 +449,21 @@ hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, hipStr
     else gemm_int8_stream_kernel<false, 4><<<grid, 256, 0, st>>>(a);
   }
   return hipGetLastError();
+}
+
+hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, bool second,
+                            hipStream_t st) {
+  if (a.M == 0 && (a.S == 0 || a.T == 0)) return hipSuccess;
+  const int mt = row_tile(a);
+  if (mt == 0) return run_stream(a, gated, st);
+  if (!second) {
+    int8_plan_kernel<<<1, 512, 0, st>>>(a, mt, plan);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  int32_t* ctr = plan + kPlanCtr + (second ? kXcds : 0);
+  return mt == 128 ? run_big<MidI8>(a, gated, plan, ctr, st)
+                   : run_big<BigI8>(a, gated, plan, ctr, st);
 }
 
 }  // namespace moe

@@ -43,8 +43,11 @@ struct Int8Args {
   int M, N, Kp, E, S, T, k;
   bool out_bf16;          // plain: bf16 or fp32 output (GATED: fp32)
 };
-hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, hipStream_t st);
-// int32 words of plan that launch_gemm_int8 needs.
-size_t gemm_int8_plan_ints(int groups);
+// second: a second product over the same rows as the call before it with this
+// plan (the experts' down half after their gate/up half).
+hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, bool second,
+                            hipStream_t st);
+// int32 words of plan (workspace) that launch_gemm_int8 needs.
+size_t gemm_int8_plan_ints();
 
 }  // namespace moe
