@@ -394,8 +394,8 @@ moe_status moe_quantize_int8(int64_t rows, int32_t K, moe_dtype dtype, const voi
  * (int32), scaled in fp32 and rounded once to `out` (MOE_F32 or MOE_BF16).
  *   a [M, Kp], a_scale [M], w [E, N, Kp], w_scale [E, N], y [M, N];
  *   offsets int32 [E+1], non-decreasing; NULL with E = 1: group 0 has all M rows.
- * Rows outside every group keep what y held.  Offsets outside [0, M] or
- * decreasing are clamped, never followed out of bounds.
+ * Rows outside every group keep what y held.  An offset outside [0, M] counts as
+ * the nearest end of it, one smaller than an offset before it as that one.
  * M, N >= 0, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and M * max(N, Kp)
  * < 2^40, a and w 16-byte aligned. */
 typedef struct {

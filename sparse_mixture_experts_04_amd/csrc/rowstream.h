@@ -21,7 +21,7 @@
 #include <type_traits>
 
 #include "select.h"
-#include "stream.h"
+#include "agent.h"
 
 namespace moe {
 

@@ -165,18 +165,24 @@ def test_product_groups(offsets, scale):
     check_product(a, sa, w, t, y, off, before)
 
 
-def test_product_offsets_are_clamped():
-    M, N, K, E = 50, 64, 128, 4
+@pytest.mark.parametrize("scale", [1, 40])
+def test_product_offsets_are_clamped(scale):
+    """Offsets outside the rows there are count as the nearest row, and one smaller
+    than an offset before it as that one: no row lies in two groups."""
+    M, N, K, E = 50 * scale, 64, 128, 4
     a, w = rand_codes((M, K), 1), rand_codes((E, N, K), 2)
     sa, t = torch.ones(M, device=DEV), torch.ones((E, N), device=DEV)
     before = randn((M, N), 5)
-    for off, good in (([-7, 20, 10, 60, 2 ** 31 - 1], [(0, 0, 20), (2, 10, 50)]),
-                      ([60, 70, -1, -2, 5], [(3, 0, 5)])):
+    for off, good in (([-7, 20, 10, 60, 2 ** 31 - 1], [(0, 0, 20), (2, 20, 50)]),
+                      ([60, 70, -1, -2, 5], []),
+                      ([5, 3, 30, 20, 40], [(1, 5, 30), (3, 30, 40)])):
         y = before.clone()
+        off = [o if o > 2 ** 30 else o * scale for o in off]
         L.gemm_int8(a, sa, w, t, y, offsets=torch.tensor(off, dtype=torch.int32, device=DEV))
         ref = before.double()
         for e, lo, hi in good:
-            ref[lo:hi] = R.mul8(a[lo:hi], sa[lo:hi], w[e], t[e])[0]
+            r = slice(lo * scale, hi * scale)
+            ref[r] = R.mul8(a[r], sa[r], w[e], t[e])[0]
         assert ((y.double() - ref).abs() <= 4 * R.EPS32 * ref.abs()).all()
 
 
