@@ -11,8 +11,8 @@ __all__ = ["configs", "synth", "ops"]
 
 
 def __getattr__(name):
-    if name == "ops":
-        return importlib.import_module("._lib", __name__)
-    if name in ("configs", "synth"):
-        return importlib.import_module("." + name, __name__)
-    raise AttributeError(name)
+    if name not in __all__:
+        raise AttributeError(name)
+    module = importlib.import_module("._lib" if name == "ops" else "." + name, __name__)
+    globals()[name] = module  # found without this function from now on
+    return module

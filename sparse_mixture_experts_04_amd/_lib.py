@@ -436,39 +436,49 @@ def code_row(K):
     return (K + 127) // 128 * 128
 
 
-def _at(t, dev, dtype, shape, name):
-    """Address of a tensor that must be on `dev`, dense, of this dtype and shape."""
-    if (isinstance(t, torch.Tensor) and t.device == dev and t.dtype is dtype
-            and t.shape == shape and t.is_contiguous()):
+def _at(t, idx, dtype, shape, name):
+    """Address of a tensor that must be on GPU `idx`, dense, of this dtype and
+    shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == idx and t.is_contiguous()):
         return t.data_ptr()
-    _ptr(t, dtype, shape, name)
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
-    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    _ptr(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on cuda:{idx}, got {t.device}")
 
 
-def _on_gpu(t, name):
-    if not isinstance(t, torch.Tensor):
+def _on_gpu(x, name):
+    """Index of the GPU that tensor x is on."""
+    if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
-    return t.device
+    idx = x.get_device()
+    if idx < 0 or not x.is_cuda:
+        raise ValueError(f"{name} must be on a GPU device, got {x.device}")
+    return idx
 
 
-def _call(dev, fn, *args):
-    """fn(*args, stream) on dev's current stream, with dev the current device."""
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+# torch's current stream as a handle, without an object around it (8-bit and
+# few-token calls take some 10 us on the GPU, the object alone 2 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
 
 
-def _workspace(ws, need, dev, name):
-    if ws is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    if ws.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {ws.device}")
-    return ws
+def _call(idx, fn, *args):
+    """fn(*args, stream) on the current stream of GPU idx, with that GPU the
+    current device."""
+    if idx == torch.cuda.current_device():
+        return fn(*args, _raw_stream(idx))
+    with torch.cuda.device(idx):
+        return fn(*args, _raw_stream(idx))
+
+
+def _ws(ws, idx):
+    """Address and size of a workspace on GPU idx."""
+    if (isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8 and ws.get_device() == idx
+            and ws.is_contiguous()):
+        return ws.data_ptr(), ws.numel()
+    _ptr(ws, torch.uint8, None, "ws")
+    raise ValueError(f"ws must be a tensor on cuda:{idx}")
 
 
 def quantize_int8(x, codes=None, scales=None):
@@ -477,18 +487,19 @@ def quantize_int8(x, codes=None, scales=None):
     outputs that are not given."""
     dev = _on_gpu(x, "x")
     code = act_code(x.dtype)
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least one value")
-    K = x.shape[-1]
-    lead = x.shape[:-1]
+    K = shape[-1]
+    lead = shape[:-1]
+    out = (*lead, code_row(K))
     if codes is None:
-        codes = torch.empty((*lead, code_row(K)), dtype=torch.int8, device=dev)
+        codes = torch.empty(out, dtype=torch.int8, device=x.device)
     if scales is None:
-        scales = torch.empty(lead, dtype=torch.float32, device=dev)
-    rows = lead.numel()
+        scales = torch.empty(lead, dtype=torch.float32, device=x.device)
     _check("moe_quantize_int8", _call(
-        dev, lib.moe_quantize_int8, rows, K, code, _at(x, dev, x.dtype, x.shape, "x"),
-        _at(codes, dev, torch.int8, (*lead, code_row(K)), "codes"),
+        dev, lib.moe_quantize_int8, lead.numel(), K, code, _at(x, dev, x.dtype, shape, "x"),
+        _at(codes, dev, torch.int8, out, "codes"),
         _at(scales, dev, torch.float32, lead, "scales")))
     return codes, scales
 
@@ -516,15 +527,14 @@ def gemm_int8(a, a_scale, w, w_scale, y, offsets=None, ws=None):
         raise ValueError(f"gemm_int8: rows of codes are padded to a multiple of 128, got {Kp}")
     desc = GemmInt8Desc(M, N, Kp, E, act_code(y.dtype))
     if ws is None:
-        ws = gemm_int8_workspace(M, N, Kp, E, dev)
-    ws = _workspace(ws, 0, dev, "ws")
+        ws = gemm_int8_workspace(M, N, Kp, E, a.device)
     _check("moe_gemm_int8", _call(
         dev, lib.moe_gemm_int8, ctypes.byref(desc), _at(a, dev, torch.int8, (M, Kp), "a"),
         _at(a_scale, dev, torch.float32, (M,), "a_scale"),
         _at(w, dev, torch.int8, (E, N, Kp), "w"),
         _at(w_scale, dev, torch.float32, (E, N), "w_scale"),
         None if offsets is None else _at(offsets, dev, torch.int32, (E + 1,), "offsets"),
-        _at(y, dev, y.dtype, (M, N), "y"), _ptr(ws, torch.uint8, None, "ws"), ws.numel()))
+        _at(y, dev, y.dtype, (M, N), "y"), *_ws(ws, dev)))
 
 
 def make_weights_int8(w_router, w_gate, t_gate, w_up, t_up, w_down, t_down,
@@ -537,7 +547,7 @@ def make_weights_int8(w_router, w_gate, t_gate, w_up, t_up, w_down, t_down,
     E, F, d = w_gate.shape
     S = ws_gate.shape[0]
     wt = WeightsInt8()
-    wt.made_of = (E, F, d, S, torch.int8, dev)
+    wt.made_of = (E, F, d, S, torch.int8, w_gate.device)
     wt.w_router = (None if w_router is None else
                    _at(w_router, dev, torch.float32, (E + S, d), "w_router"))
     for n, prefix, parts in ((E, "", ((w_gate, t_gate), (w_up, t_up), (w_down, t_down))),
@@ -597,8 +607,8 @@ def expert_ffn_int8(desc, x, weights, offsets, sorted_pair, y_routed, y_shared, 
     """moe_expert_ffn_int8: expert_ffn with 8-bit weights (WeightsInt8); desc is
     the layer's ordinary descriptor."""
     dev = _on_gpu(x, "x")
-    _weights_for(desc, weights, dev, (WeightsInt8,), "expert_ffn_int8")
-    ws = expert_ffn_int8_workspace(desc, dev) if ws is None else _workspace(ws, 0, dev, "ws")
+    _weights_for(desc, weights, x.device, (WeightsInt8,), "expert_ffn_int8")
+    ws = expert_ffn_int8_workspace(desc, x.device) if ws is None else ws
     T, d, k, S, E = desc.T, desc.d, desc.k, desc.S, desc.E
     act, i32 = _act(desc), torch.int32
     _check("moe_expert_ffn_int8", _call(
@@ -607,7 +617,7 @@ def expert_ffn_int8(desc, x, weights, offsets, sorted_pair, y_routed, y_shared, 
         _at(sorted_pair, dev, i32, (T * k,), "sorted_pair"),
         _at(y_routed, dev, act, (T * k, d), "y_routed"),
         None if y_shared is None else _at(y_shared, dev, act, (S, T, d), "y_shared"),
-        _ptr(ws, torch.uint8, None, "ws"), ws.numel()))
+        *_ws(ws, dev)))
 
 
 def forward_few_workspace(desc, device):
@@ -620,8 +630,8 @@ def forward_few(desc, x, weights, bias, y, topk_idx=None, gates=None, ws=None):
     Weights of desc's dtype, moe_forward_few_int8 with WeightsInt8.  The bias is
     read, not updated.  Calls that overlap need a workspace each."""
     dev = _on_gpu(x, "x")
-    _weights_for(desc, weights, dev, (Weights, WeightsInt8), "forward_few")
-    ws = forward_few_workspace(desc, dev) if ws is None else _workspace(ws, 0, dev, "ws")
+    _weights_for(desc, weights, x.device, (Weights, WeightsInt8), "forward_few")
+    ws = forward_few_workspace(desc, x.device) if ws is None else ws
     T, d, k, S, E = desc.T, desc.d, desc.k, desc.S, desc.E
     act = _act(desc)
     int8 = type(weights) is WeightsInt8
@@ -631,4 +641,4 @@ def forward_few(desc, x, weights, bias, y, topk_idx=None, gates=None, ws=None):
         _at(bias, dev, torch.float32, (E,), "bias"), _at(y, dev, act, (T, d), "y"),
         None if topk_idx is None else _at(topk_idx, dev, torch.int32, (T, k), "topk_idx"),
         None if gates is None else _at(gates, dev, torch.float32, (T, k + S), "gates"),
-        _ptr(ws, torch.uint8, None, "ws"), ws.numel()))
+        *_ws(ws, dev)))

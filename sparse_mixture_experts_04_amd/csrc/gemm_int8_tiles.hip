@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kThreads, 4) void gemm_int8_tiles_kernel(Int8Args p
         auto load = [&](u32x4_t (&b)[2]) __attribute__((always_inline)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            b[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(lp + 16 * h));
+            b[h] = *reinterpret_cast<const u32x4_t*>(lp + 16 * h);
           if (ls + 1 < steps) {
             ++ls;
             lp += kStep;
