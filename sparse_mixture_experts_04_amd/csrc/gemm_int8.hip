@@ -3,6 +3,8 @@
 //
 // The sums are exact in int32 (K <= 131072), so the only rounding is the
 // scaling in fp32 and the store.
+#include <cmath>
+
 #include "big_tile.h"
 #include "int8_rows.h"
 
@@ -251,28 +253,53 @@ static hipError_t run_big(const Int8Args& a, bool gated, const int32_t* plan, in
 
 size_t gemm_int8_plan_ints() { return kPlanInts; }
 
-// Kernel of a product, by the mean rows of a group.
-enum class Path { kRows, kTiles, kMid, kBig };
-static Path path(const Int8Args& a) {
-  const long long mean = a.M / (a.E > 0 ? a.E : 1);
-  if (mean > 160) return Path::kBig;
-  if (mean > 16) return Path::kMid;
-  // 16-row weight tiles the groups have together, at least
-  const long long tiles = static_cast<long long>(a.M < a.E ? a.M : a.E) * (a.N / 16);
-  return mean <= 8 && tiles < 4096 ? Path::kRows : Path::kTiles;
+// Kernel of a product, by estimates of their times (us) fitted to measured ones.
+// They agree to the bit, so the choice is one of speed alone.  M is the rows, mu
+// the mean rows of a group, G the groups expected to have any:
+//   tiles  7 + the weights read once per 16 rows of a group, at 9 TB/s while
+//          they stay in the caches and 5.3 from memory
+//   128    22 + the slower of a tile's time (5.8 per 1000 of K; 0.042 per tile
+//          when they fill the device) and the weights read once at 5.3 TB/s
+//   256    27 + the same with 9.2 and 0.065
+// Measured (us; N x K, groups):
+//   rows                1     64    256   1024   4096   16 a group  96 a group
+//   tiles  2048x7168   15     17     34    110    404      310        1474
+//   128                56     57     68     64     88      227         270
+//   256                76     77     95     94     93      266         315
+//   (the last two columns 2048x2048, 256 groups); 256-row tiles lead from
+//   16384 rows of 2048x7168 on.
+enum class Path { kTiles, kMid, kBig };
+static Path path(const Int8Args& a, bool gated) {
+  const double n = gated ? 2.0 * a.N : a.N, k = a.Kp, mu = static_cast<double>(a.M) / a.E;
+  const double full = a.E == 1 ? 1.0 : a.E * (1.0 - std::exp(-mu));
+  const double weights = (full + a.S) * n * k * 1e-6;  // megabytes
+  // row tiles of MT rows: at least one a group with rows, half a tile wasted
+  auto row_tiles = [&](double mt) {
+    const double r = a.E == 1 ? std::ceil(a.M / mt) : full * std::fmax(1.0, mu / mt + 0.5);
+    return r + a.S * std::ceil(a.T / mt);
+  };
+  const double tiles = 7.0 + row_tiles(16) * n * k * 1e-6 / (weights < 200.0 ? 9.0 : 5.3);
+  const double cols = std::ceil(n / 256.0), stream = weights / 5.3;
+  auto large = [&](double mt, double fixed, double one, double each) {
+    return fixed + std::fmax(stream, k * 1e-3 * std::fmax(one, each * row_tiles(mt) * cols));
+  };
+  const double mid = large(128, 22.0, 5.8, 0.042), big = large(256, 27.0, 9.2, 0.065);
+  if (tiles <= mid && tiles <= big) return Path::kTiles;
+  return mid <= big ? Path::kMid : Path::kBig;
 }
 
-hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, bool second,
+hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, int& planned,
                             hipStream_t st) {
   if (a.M == 0 && (a.S == 0 || a.T == 0)) return hipSuccess;
-  const Path way = path(a);
-  if (way == Path::kRows) return launch_gemm_int8_rows(a, gated, st);
+  const Path way = path(a, gated);
   if (way == Path::kTiles) return launch_gemm_int8_tiles(a, gated, st);
   const int mt = way == Path::kMid ? 128 : 256;
+  const bool second = planned == mt;  // the call before this left a plan for these tiles
   if (!second) {
     int8_plan_kernel<<<1, 512, 0, st>>>(a, mt, plan);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    planned = mt;
   }
   int32_t* ctr = plan + kPlanCtr + (second ? kXcds : 0);
   return mt == 128 ? run_big<MidI8>(a, gated, plan, ctr, st)

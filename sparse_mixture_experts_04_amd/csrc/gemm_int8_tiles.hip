@@ -13,15 +13,18 @@
 //
 // Bound by the weight loads.  kRing steps of a wave are in registers, all but
 // one in flight; loads are issued unconditionally so that the compiler can
-// count them.  Against the row stream (gemm_int8_rows.hip) a byte of weights
-// costs one byte of LDS reads whatever the rows of the entry, not one per row.
-#include "agent.h"
+// count them; without the non-temporal hint, for the two loads of a step share
+// their lines (with it the T=64 experts took 864 us, without 794).  A stream of
+// whole weight rows multiplied by v_dot4 needs one LDS byte per weight byte and
+// row, this needs one whatever the rows: 8 rows a group, N=K=2048, 256 groups
+// 397 against 216 us.  The matrix and vector units are mostly idle.
 #include "int8_rows.h"
 
 namespace moe {
 
 namespace {
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;

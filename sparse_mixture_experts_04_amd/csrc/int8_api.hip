@@ -171,7 +171,8 @@ moe_status moe_gemm_int8(const moe_gemm_int8_desc* desc, const int8_t* a, const 
   g.E = desc->E;
   g.k = 1;
   g.out_bf16 = desc->out == MOE_BF16;
-  return hip_status(launch_gemm_int8(g, false, static_cast<int32_t*>(ws), false, stream));
+  int planned = 0;
+  return hip_status(launch_gemm_int8(g, false, static_cast<int32_t*>(ws), planned, stream));
 }
 
 moe_status moe_expert_ffn_int8_workspace_size(const moe_desc* desc, size_t* bytes) {
@@ -224,7 +225,8 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
   g.S = s.S;
   g.T = s.T;
   g.k = s.k;
-  if (e == hipSuccess) e = launch_gemm_int8(g, true, f.plan, false, stream);
+  int planned = 0;
+  if (e == hipSuccess) e = launch_gemm_int8(g, true, f.plan, planned, stream);
   if (e == hipSuccess) e = launch_quantize_int8(rows, s.F, false, f.h, f.hq, f.hs, stream);
   g.a = f.hq;
   g.a_scale = f.hs;
@@ -237,7 +239,7 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
   g.N = s.d;
   g.Kp = s.F;
   g.out_bf16 = s.bf16;
-  if (e == hipSuccess) e = launch_gemm_int8(g, false, f.plan, true, stream);
+  if (e == hipSuccess) e = launch_gemm_int8(g, false, f.plan, planned, stream);
   return hip_status(e);
 }
 

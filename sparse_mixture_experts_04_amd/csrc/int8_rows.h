@@ -92,7 +92,6 @@ __device__ __forceinline__ int entry_group(const EntryPlan& s, int G, int ent) {
   return g;
 }
 
-hipError_t launch_gemm_int8_rows(const Int8Args& a, bool gated, hipStream_t st);
 hipError_t launch_gemm_int8_tiles(const Int8Args& a, bool gated, hipStream_t st);
 
 }  // namespace moe
