@@ -5,22 +5,45 @@
 
 namespace moe {
 
-__device__ __forceinline__ int quant_code(float x, float amax, float inv) {
-  const float t = x * inv;
-  float r = rintf(t);
-  // !(..) also catches an inv that overflowed (amax below 127 / FLT_MAX)
-  if (!(fabsf(t - r) < 0.4999f))
-    r = static_cast<float>(rint(127.0 * static_cast<double>(x) / static_cast<double>(amax)));
-  return static_cast<int>(r);
+// Codes of 8 values, 4 to a word.  x * inv + 1.5 * 2^23 rounds the quotient to
+// the nearest integer, ties to even, and leaves it in the sum's low bits; the
+// remainder tells whether it lay near a border.
+__device__ __forceinline__ uint2 pack_codes(const float (&v)[8], float amax, float inv) {
+  constexpr float kMagic = 12582912.0f;
+  uint32_t bits[8];
+  float near = inv < INFINITY ? 0.0f : 1.0f;  // inv overflows for amax below 127 / FLT_MAX
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = fmaf(v[i], inv, kMagic);
+    near = fmaxf(near, fabsf(fmaf(v[i], inv, kMagic - f)));
+    bits[i] = __float_as_uint(f);
+  }
+  if (near >= 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      bits[i] = static_cast<uint32_t>(static_cast<int>(
+          rint(127.0 * static_cast<double>(v[i]) / static_cast<double>(amax))));
+  }
+  // the low bytes of four words
+  auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u),
+                                 __builtin_amdgcn_perm(b, a, 0x0c0c0400u), 0x05040100u);
+  };
+  return make_uint2(four(bits[0], bits[1], bits[2], bits[3]),
+                    four(bits[4], bits[5], bits[6], bits[7]));
 }
 
-__device__ __forceinline__ uint32_t pack_codes(const float* v, float amax, float inv) {
-  uint32_t w = 0;
+// Largest magnitude of 8 values as bits: an infinity or a NaN counts as more than
+// every finite value (0x7f800000 on).
+__device__ __forceinline__ uint32_t max_bits(const float (&v)[8], uint32_t m) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= (static_cast<uint32_t>(quant_code(v[i], amax, inv)) & 0xffu) << (8 * i);
-  return w;
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+    m = u > m ? u : m;
+  }
+  return m;
 }
+constexpr uint32_t kNotFinite = 0x7f800000u;
 
 // 8 values from p; `n` of them exist (VEC: all, and p is 16-byte aligned).
 template <typename T, bool VEC>
@@ -44,20 +67,21 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
   }
 }
 
-// max |x| of a row held by the NT threads of a workgroup as their own maxima
-// (`bad`: a value was not finite): the maximum, or infinity.
+// Largest of the maxima that the NT threads of a workgroup hold.
 template <int NT>
-__device__ __forceinline__ float row_amax(float m, bool bad) {
-  __shared__ float sm[NT / 64];
-  if (bad) m = INFINITY;
+__device__ __forceinline__ uint32_t row_max(uint32_t m) {
+  __shared__ uint32_t sm[NT / 64];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint32_t u = __shfl_xor(m, o);
+    m = u > m ? u : m;
+  }
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
   __syncthreads();
   m = sm[0];
 #pragma unroll
-  for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, sm[w]);
+  for (int w = 1; w < NT / 64; ++w) m = sm[w] > m ? sm[w] : m;
   return m;
 }
 
@@ -67,27 +91,23 @@ __device__ __forceinline__ float row_amax(float m, bool bad) {
 template <int NT, class Load, class Store>
 __device__ __forceinline__ float quantize_row(int K, int Kp, Load load, Store store) {
   const int chunks = (K + 7) / 8;
-  float m = 0.0f;
-  bool bad = false;
+  uint32_t top = 0;
   for (int c = threadIdx.x; c < chunks; c += NT) {
     float v[8];
     load(c, K - c * 8, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m = fmaxf(m, fabsf(v[i]));
-      bad = bad || !(fabsf(v[i]) < INFINITY);
-    }
+    top = max_bits(v, top);
   }
-  m = row_amax<NT>(m, bad);
-  const bool finite = m < INFINITY;
-  const bool live = finite && m > 0.0f;
+  top = row_max<NT>(top);
+  const float m = __uint_as_float(top);
+  const bool finite = top < kNotFinite;
+  const bool live = finite && top > 0;
   const float inv = 127.0f / m;
   for (int c = threadIdx.x; c < Kp / 8; c += NT) {
     uint2 w = make_uint2(0u, 0u);
     if (live && c < chunks) {
       float v[8];
       load(c, K - c * 8, v);
-      w = make_uint2(pack_codes(v, m, inv), pack_codes(v + 4, m, inv));
+      w = pack_codes(v, m, inv);
     }
     store(c, w);
   }

@@ -9,71 +9,124 @@
 // than the distance of any quotient of two fp32 values to a border it is not
 // on.  A row of zeros gets scale 0; a row holding a NaN or an infinity gets
 // codes 0 and scale NaN, so that only its own products become NaN.
+#include <type_traits>
+
 #include "int8_quant.h"
 
 namespace moe {
 
-// A row in chunks of 8 values, by a workgroup (TPR 256) or a wave (TPR 64);
-// it is read twice, the second time from the cache.
-template <typename T, int TPR, bool VEC>
-__global__ __launch_bounds__(256) void quantize_int8_kernel(const T* __restrict__ x,
-                                                            long long rows, int K, int Kp,
+// 8 values of a row in registers.
+struct Eight {
+  float v[8];
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ void hold(const T* p, int n, Eight& h) {
+  load8<T, VEC>(p, n, h.v);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void hold(const T* p, int, uint4& h) {
+  h = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void values(const Eight& h, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = h.v[i];
+}
+__device__ __forceinline__ void values(const uint4& h, float (&v)[8]) {
+  const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// A row of up to 512 NC values by a wave, four rows a workgroup: every chunk of 8
+// values a lane has is loaded before the first is used and stays in registers,
+// so the row is read once.
+template <typename T, int NC, bool VEC>
+__global__ __launch_bounds__(256) void quantize_int8_wave_kernel(const T* __restrict__ x,
+                                                                 long long rows, int K, int Kp,
+                                                                 int8_t* __restrict__ codes,
+                                                                 float* __restrict__ scales) {
+  const int lane = threadIdx.x & 63;
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;  // whole waves leave
+  const T* xr = x + row * K;
+  const int chunks = (K + 7) / 8;
+  // bf16 values stay as they were read, two to a register
+  using Held = typename std::conditional<VEC && sizeof(T) == 2, uint4, Eight>::type;
+  Held held[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = lane + 64 * j;
+    held[j] = Held{};
+    if (c < chunks) hold<T, VEC>(xr + c * 8, K - c * 8, held[j]);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    float v[8];
+    values(held[j], v);
+    top = max_bits(v, top);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint32_t u = __shfl_xor(top, o);
+    top = u > top ? u : top;
+  }
+  const float m = __uint_as_float(top);
+  const bool finite = top < kNotFinite;
+  const bool live = finite && top > 0;
+  const float inv = 127.0f / m;
+  int8_t* cr = codes + row * Kp;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = lane + 64 * j;
+    if (c >= Kp / 8) continue;
+    float v[8];
+    values(held[j], v);
+    *reinterpret_cast<uint2*>(cr + c * 8) = live ? pack_codes(v, m, inv) : make_uint2(0u, 0u);
+  }
+  if (lane == 0) scales[row] = finite ? m / 127.0f : NAN;
+}
+
+// A row by a workgroup, read twice, the second time from the cache: few rows,
+// where one row's latency counts, and rows too long for the kernel above.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void quantize_int8_kernel(const T* __restrict__ x, int K, int Kp,
                                                             int8_t* __restrict__ codes,
                                                             float* __restrict__ scales) {
-  if constexpr (TPR == 256) {
-    const long long row = blockIdx.x;
-    const float s = quantize_row<T, VEC, 256>(x + row * K, K, Kp, codes + row * Kp);
-    if (threadIdx.x == 0) scales[row] = s;
-  } else {
-    const int i0 = threadIdx.x & 63;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (row >= rows) return;  // whole waves leave
-    const T* xr = x + row * K;
-    float m = 0.0f;
-    bool bad = false;
-    const int chunks = (K + 7) / 8;
-    for (int c = i0; c < chunks; c += 64) {
-      float v[8];
-      load8<T, VEC>(xr + c * 8, K - c * 8, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m = fmaxf(m, fabsf(v[i]));
-        bad = bad || !(fabsf(v[i]) < INFINITY);
-      }
-    }
-    if (bad) m = INFINITY;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    const bool finite = m < INFINITY;
-    const bool live = finite && m > 0.0f;
-    const float inv = 127.0f / m;
-    int8_t* cr = codes + row * Kp;
-    for (int c = i0; c < Kp / 8; c += 64) {
-      uint2 w = make_uint2(0u, 0u);
-      if (live && c < chunks) {
-        float v[8];
-        load8<T, VEC>(xr + c * 8, K - c * 8, v);
-        w = make_uint2(pack_codes(v, m, inv), pack_codes(v + 4, m, inv));
-      }
-      *reinterpret_cast<uint2*>(cr + c * 8) = w;
-    }
-    if (i0 == 0) scales[row] = finite ? m / 127.0f : NAN;
-  }
+  const long long row = blockIdx.x;
+  const float s = quantize_row<T, VEC, 256>(x + row * K, K, Kp, codes + row * Kp);
+  if (threadIdx.x == 0) scales[row] = s;
+}
+
+template <typename T, int NC>
+static void run_wave(long long rows, int K, bool vec, const T* x, int8_t* codes, float* scales,
+                     hipStream_t st) {
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  const int Kp = static_cast<int>(code_row(K));
+  if (vec) quantize_int8_wave_kernel<T, NC, true><<<grid, 256, 0, st>>>(x, rows, K, Kp, codes, scales);
+  else quantize_int8_wave_kernel<T, NC, false><<<grid, 256, 0, st>>>(x, rows, K, Kp, codes, scales);
 }
 
 template <typename T>
 static hipError_t run_quantize(long long rows, int K, const T* x, int8_t* codes, float* scales,
                                hipStream_t st) {
-  const int Kp = static_cast<int>(code_row(K));
   const bool vec = K % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
-  if (rows <= 1024) {  // one workgroup per row: a row's latency counts
+  const int Kp = static_cast<int>(code_row(K));
+  if (rows <= 1024 || Kp > 8192) {
     const unsigned grid = static_cast<unsigned>(rows);
-    if (vec) quantize_int8_kernel<T, 256, true><<<grid, 256, 0, st>>>(x, rows, K, Kp, codes, scales);
-    else quantize_int8_kernel<T, 256, false><<<grid, 256, 0, st>>>(x, rows, K, Kp, codes, scales);
+    if (vec) quantize_int8_kernel<T, true><<<grid, 256, 0, st>>>(x, K, Kp, codes, scales);
+    else quantize_int8_kernel<T, false><<<grid, 256, 0, st>>>(x, K, Kp, codes, scales);
+  } else if (Kp <= 1024) {
+    run_wave<T, 2>(rows, K, vec, x, codes, scales, st);
+  } else if (Kp <= 2048) {
+    run_wave<T, 4>(rows, K, vec, x, codes, scales, st);
+  } else if (Kp <= 4096) {
+    run_wave<T, 8>(rows, K, vec, x, codes, scales, st);
   } else {
-    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-    if (vec) quantize_int8_kernel<T, 64, true><<<grid, 256, 0, st>>>(x, rows, K, Kp, codes, scales);
-    else quantize_int8_kernel<T, 64, false><<<grid, 256, 0, st>>>(x, rows, K, Kp, codes, scales);
+    run_wave<T, 16>(rows, K, vec, x, codes, scales, st);
   }
   return hipGetLastError();
 }

@@ -30,7 +30,9 @@ def rand_codes(shape, seed):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,K", [(1, 1), (1, 7168), (3, 7), (5, 128), (70, 1111), (1024, 130),
-                                    (1025, 8), (1030, 333), (2, 16384), (1, 131072)])
+                                    (1025, 8), (1030, 333), (2, 16384), (1, 131072),
+                                    (1100, 1030), (1100, 2050), (1300, 4100), (1100, 7168),
+                                    (1100, 8192), (1100, 8200)])
 def test_quantize_is_exact(rows, K, dtype):
     print(f"quantize rows={rows} K={K} {dtype}", flush=True)
     x = randn((rows, K), rows * 7 + K, dtype)
