@@ -449,8 +449,8 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
  * are T > 16, weight == MOE_MXFP4, d or F > 16384 and the shapes
  * moe_forward does not take).  topk_idx [T, 6] and gates [T, 6+S] are written
  * where given.  A token whose x holds a NaN or an infinity gets NaN gates or
- * outputs, its choice of experts is unspecified but valid; other tokens are
- * not touched by it.
+ * outputs, its choice of experts is unspecified but valid.  Results are bitwise
+ * reproducible and a token's do not depend on the other tokens' values.
  * moe_forward_few_int8 takes 8-bit weights: x is quantised per token, h per row
  * (from fp32).  Both calls take the workspace of
  * moe_forward_few_workspace_size; calls that overlap need one each. */

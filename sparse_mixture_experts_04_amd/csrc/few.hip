@@ -10,29 +10,38 @@
 //   gate/up      every workgroup's share ("chunk") of the shared experts'
 //                columns, which needs no routing and so hides the selection,
 //                then its share of the routed experts' columns;
-//   down         blocks of 16 output columns, all contributors of a block by
-//                one workgroup (or `parts` of them), so that each y is summed
-//                where it is made.
+//   down         its share of the output columns, all contributors of a column,
+//                so that each y is summed where it is made.
 //
 // Between the stages workgroups wait for flags that others set.  A wait ends
 // whatever else runs on the device: a flag says not started, started or done;
 // work that has been started is held by a running workgroup and finishes
 // (gate/up waits for the selection only, the selection for nothing), and work
 // that no workgroup has started is done by the one that waits for it.  Two
-// workgroups may then do the same piece: they write the same bits.  The down
-// stage is waited for by nobody, except that the last of a block's parts adds
-// them up.  (Handing items out by one counter cost 70 ns an item on this
-// device, more than an item's weights take.)
+// workgroups may then do the same piece: they write the same bits.  Nobody waits
+// for the down stage.  (Handing items out by one counter cost 70 ns an item on
+// this device, more than an item's weights take; release and acquire fences, a
+// pair for each of 4096 waves, 150 us a call.)
 //
-// No sum depends on timing: products are split over waves and parts by the
-// sizes alone, and added in a fixed order.
+// No sum depends on timing or on the other tokens' values: a dot product is
+// added over the same lanes in the same order wherever its row lies, and a
+// token's contributors in the order of moe_combine (its picks by rank, then the
+// shared experts).
 //
 // Precision: logits, affinities and gates in fp64 (the selection is that of
-// exact arithmetic but for keys within ~1e-15); products on the matrix cores
-// with fp32 (or exact int32) accumulation; h and the experts' outputs in fp32.
+// exact arithmetic but for keys within ~1e-15); products with fp32 (or exact
+// int32) accumulation; h and the experts' outputs in fp32, one rounding into y.
 // With bf16 weights h enters the down product as two bf16 terms (h = hi + lo
 // to 2^-17): the second product costs no memory traffic.  With 8-bit weights x
 // is quantised per token and h per row.
+//
+// Bound by the weight rows' loads (rowstream.h): T=16, d=7168, F=2048, bf16
+// reads 7.3 GB in 1.22 ms, 6.0 TB/s.  T=1 there takes 147 us of which the 704 MB
+// need 117 at that rate; the rest, and most of the 40 us of T=1 at d=2048, F=768
+// (75 MB), are fixed costs of about 4 us to the first load, 3 for the plan once
+// the picks are known, 5 for the wait before the down stage, 3 for the latency of
+// each stage's first loads, and the fetch of code that the weights have driven
+// out of the caches (some 0.4 us per 128 bytes: hence loops where they can be).
 #include <type_traits>
 
 #include "few.h"
@@ -62,18 +71,18 @@ __device__ __forceinline__ void load4(const bf16_t* p, double (&v)[4]) {
 // few_ffn_kernel.  INT8: block E + S + 1 + t quantises token t.  TM: tokens
 // rounded up to a power of two.
 template <typename X, int TM, bool INT8>
-__global__ __launch_bounds__(256) void few_route_kernel(FewArgs p, int ctrl_ints) {
+__global__ __launch_bounds__(512) void few_route_kernel(FewArgs p, int ctrl_ints) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x;
   const int rows = p.E + p.S;
   const X* x = static_cast<const X*>(p.x);
   if (b == rows) {
-    for (int i = tid; i < ctrl_ints; i += 256) p.ctrl[i] = 0;  // kIdle
+    for (int i = tid; i < ctrl_ints; i += 512) p.ctrl[i] = 0;  // kIdle
     return;
   }
   if (INT8 && b > rows) {
     const int t = b - rows - 1;
-    const float s = quantize_row<X, true, 256>(x + static_cast<size_t>(t) * p.d, p.d, p.d,
+    const float s = quantize_row<X, true, 512>(x + static_cast<size_t>(t) * p.d, p.d, p.d,
                                           p.xq + static_cast<size_t>(t) * p.d);
     if (tid == 0) p.xs[t] = s;
     return;
@@ -82,7 +91,7 @@ __global__ __launch_bounds__(256) void few_route_kernel(FewArgs p, int ctrl_ints
 #pragma unroll
   for (int t = 0; t < TM; ++t) acc[t] = 0.0;
   const float* w = p.w_router + static_cast<size_t>(b) * p.d;
-  for (int c = tid * 4; c < p.d; c += 1024) {
+  for (int c = tid * 4; c < p.d; c += 2048) {
     double wv[4];
     load4(w + c, wv);
 #pragma unroll
@@ -94,7 +103,7 @@ __global__ __launch_bounds__(256) void few_route_kernel(FewArgs p, int ctrl_ints
       for (int i = 0; i < 4; ++i) acc[t] = fma(xv[i], wv[i], acc[t]);
     }
   }
-  __shared__ double sum[4][TM];
+  __shared__ double sum[8][TM];
 #pragma unroll
   for (int t = 0; t < TM; ++t) {
     const double v = wave_sum(acc[t], lane);
@@ -102,7 +111,9 @@ __global__ __launch_bounds__(256) void few_route_kernel(FewArgs p, int ctrl_ints
   }
   __syncthreads();
   if (tid < p.T) {
-    const double z = ((sum[0][tid] + sum[1][tid]) + sum[2][tid]) + sum[3][tid];
+    double z = sum[0][tid];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) z += sum[i][tid];
     p.zs[static_cast<size_t>(tid) * rows + b] = double2{z, sigmoid64(z)};
   }
 }
@@ -172,6 +183,14 @@ __device__ __forceinline__ void few_select(const FewArgs& p, int t, int lane) {
 // States of a flag.
 enum { kIdle = 0, kStarted = 1, kDone = 2 };
 
+// i / n for 0 <= i < 2^20 and a quotient below 128 (inv = 1 / n): the product is off
+// by less than 128 * 2^-22, the quotient of i + 1/2 lies at least 1 / (2 n) from an
+// integer, and every n here is at most 8192.  An integer division is 40
+// instructions, all of them to be fetched.
+__device__ __forceinline__ int quotient(int i, float inv) {
+  return static_cast<int>((static_cast<float>(i) + 0.5f) * inv);
+}
+
 constexpr int kFewThreads = 1024;
 constexpr int kFewWaves = kFewThreads / 64;
 constexpr int kPatience = 64;  // polls before a waiter looks for work not started
@@ -228,7 +247,8 @@ constexpr int kFewEntries = kFewMaxTokens * kFewTopK + 2 * ((kFewMaxTokens + kUn
 struct FewPlan {
   int tok[kFewRows + kUnitRows];    // token of a list row
   int hrow[kFewRows + kUnitRows];   // its row of h
-  float gate[kFewRows + kUnitRows]; // its gate (times its scale of h, 8-bit weights)
+  float scale[kFewRows + kUnitRows];  // its scale of h (8-bit weights)
+  float gate[kFewRows];             // gates [T, 6 + S]
   int first[kFewEntries + 1];       // first list row of an entry
   int expert[kFewEntries + 1];      // its row of the weight stack
   int shared_entries, entries;
@@ -237,15 +257,18 @@ struct FewPlan {
 // Entries of the shared experts (all threads, a barrier after it).
 template <int S>
 __device__ __forceinline__ void plan_shared(const FewArgs& p, FewPlan& s) {
-  const int per = (p.T + kUnitRows - 1) / kUnitRows;
+  static_assert(S <= 2 && kFewMaxTokens <= 2 * kUnitRows, "two shared experts of two entries");
+  const int per = p.T > kUnitRows ? 2 : 1;
   const int tid = threadIdx.x;
   if (tid < S * p.T) {
-    s.tok[tid] = tid % p.T;
+    const int e = tid >= p.T ? 1 : 0, t = tid - e * p.T;
+    s.tok[tid] = t;
     s.hrow[tid] = p.T * kFewTopK + tid;
   }
   if (tid < S * per) {
-    s.first[tid] = tid / per * p.T + tid % per * kUnitRows;
-    s.expert[tid] = tid / per;
+    const int e = per == 2 ? tid >> 1 : tid, half = per == 2 ? tid & 1 : 0;
+    s.first[tid] = e * p.T + half * kUnitRows;
+    s.expert[tid] = e;
   }
   if (tid == 0) {
     s.shared_entries = S * per;
@@ -312,66 +335,77 @@ __device__ __forceinline__ void plan_routed(const FewArgs& p, FewPlan& s) {
   __syncthreads();
 }
 
-// LDS of a workgroup: sums (gate and up of kPartCols columns, or each wave's
-// share of its y), then activation rows.
+// LDS of a workgroup: sums (gate and up of kPartCols columns, or the down products
+// of its columns with every row of h), then activation rows.
 constexpr int kPool = 144 * 1024;
 constexpr int kPartCols = 512;     // gate/up columns between two epilogues
 constexpr int kPartBytes = kPartCols * 2 * kUnitRows * 4;
-static_assert(kFewWaves * (kFewMaxWidth / kFewGrid) * kFewMaxTokens * 4 + 8 * kUnitRows * kChunk <=
-                  kPool, "8 chunks of 8 rows beside the widest y");
+static_assert(kFewMaxWidth / kFewGrid * kFewRows * 4 + 8 * kUnitRows * kChunk <= kPool,
+              "8 chunks of 8 rows beside the widest layer's products");
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Gate/up columns c0..c1-1 of the list (entry ent0 + c / F, column c % F), two
-// units each; sums go to part[c - cbase].
+// The units of a workgroup go to its waves in turn (unit i kFewWaves + wave is
+// the wave's i-th): the waves read neighbouring rows at the same time, and their
+// shares differ by one unit at most.
+
+// Gate/up units of n columns from cbase on: unit 2 c is the W_gate row of column
+// cbase + c, 2 c + 1 its W_up row; sums go to part[c].  Column cbase is column f_
+// of entry ent_.
 template <class Acc>
 struct GateWalk {
   const FewPlan& plan;
   Acc (*part)[2][kUnitRows];
-  const char *wg, *wu;
+  const char* base;   // of the matrix stack this wave reads: W_gate or W_up
   size_t kfull;       // bytes of a weight row
-  int F, c0, n, cbase, ent0, xstride, lane;
+  int F, n, up, xstride, lane;
   bool more;          // not the first pass over K: add
-  // load side: the next unit
-  const char *lg, *lu2;
+  const char* lrow;   // load side: the next unit's row
   int lf, lent;
-  // multiply side
-  int f, ent;
+  int f, ent, rows, col;  // multiply side
+  static constexpr int kStep = kFewWaves / 2;  // columns from one unit to the next
 
-  __device__ __forceinline__ GateWalk(const FewPlan& pl, Acc (*pt)[2][kUnitRows], const void* g, const void* u,
-                      size_t kf, size_t koff, int F_, int c0_, int c1_, int cb, int e0, int xs,
-                      bool m)
-      : plan(pl), part(pt), wg(static_cast<const char*>(g) + koff),
-        wu(static_cast<const char*>(u) + koff), kfull(kf), F(F_), c0(c0_), n(c1_ - c0_), cbase(cb),
-        ent0(e0), xstride(xs), lane(threadIdx.x & 63), more(m) {
-    lent = ent = ent0 + c0 / F;
-    lf = f = c0 % F;
-    --f;
-    place();
+  __device__ __forceinline__ GateWalk(const FewPlan& pl, Acc (*pt)[2][kUnitRows], const void* g,
+                                      const void* u, size_t kf, size_t koff, int F_, int cols,
+                                      int wave, int ent_, int f_, int xs, bool m)
+      : plan(pl), part(pt), base(static_cast<const char*>(wave & 1 ? u : g) + koff), kfull(kf),
+        F(F_), n((2 * cols - wave + kFewWaves - 1) / kFewWaves), up(wave & 1), xstride(xs),
+        lane(threadIdx.x & 63), more(m) {
+    static_assert(kFewWaves % 2 == 0, "a wave reads one of the two matrices");
+    lent = ent_;
+    lf = f_ + (wave >> 1);
+    for (; lf >= F; lf -= F) ++lent;
+    ent = lent;
+    f = lf;
+    col = wave >> 1;
+    rows = 0;
+    lrow = nullptr;
+    if (n > 0) place();
   }
   __device__ __forceinline__ void place() {
-    const size_t o = (static_cast<size_t>(uniform(plan.expert[lent])) * F + lf) * kfull;
-    lg = wg + o;
-    lu2 = wu + o;
+    lrow = base + (static_cast<size_t>(uniform(plan.expert[lent])) * F + lf) * kfull;
   }
-  __device__ __forceinline__ int units() const { return 2 * n; }
+  __device__ __forceinline__ int units() const { return n; }
   __device__ __forceinline__ const char* row(int u) {
-    if (u & 1) return lu2;
     if (u > 0) {
-      lg += kfull;
-      lu2 += kfull;
-      if (++lf == F) {
-        lf = 0;
+      lrow += kStep * kfull;
+      lf += kStep;
+      if (lf >= F) {  // F >= 128: one entry further
+        lf -= F;
         ++lent;
         place();
       }
     }
-    return lg;
+    return lrow;
   }
   __device__ __forceinline__ int enter(int u, int (&off)[kUnitRows]) {
-    if (!(u & 1) && (++f == F || u == 0)) {
-      if (f == F) {
-        f = 0;
+    if (u > 0) {
+      f += kStep;
+      col += kStep;
+    }
+    if (u == 0 || f >= F) {
+      if (f >= F) {
+        f -= F;
         ++ent;
       }
       const int r0 = plan.first[ent];
@@ -382,8 +416,8 @@ struct GateWalk {
     }
     return rows;
   }
-  __device__ __forceinline__ void leave(int u, int nr, const Acc (&acc)[kUnitRows]) {
-    Acc* out = part[c0 - cbase + (u >> 1)][u & 1];
+  __device__ __forceinline__ void leave(int, int nr, const Acc (&acc)[kUnitRows]) {
+    Acc* out = part[col][up];
 #pragma unroll
     for (int r = 0; r < kUnitRows; ++r) {
       if (r >= nr) break;
@@ -391,64 +425,63 @@ struct GateWalk {
       if (lane == 0) out[r] = more ? out[r] + s : s;
     }
   }
-  int rows = 0;
 };
 
-// Down units u0..u1-1 of a pass over entries e0..e0+ne-1: column u / ne of the
-// workgroup's columns, entry e0 + u % ne.
+// Down units of a pass over entries e0..e0+ne-1: unit u is column u / ne of the
+// workgroup's columns and entry e0 + u % ne.
 template <class Acc, bool I8>
 struct DownWalk {
   const FewPlan& plan;
-  float* ysum;             // [columns, T]
-  int T;
+  float* yrow;             // [columns, rows of h]
+  int rows_h;
+  bool more;               // not the first pass over K: add
   const char *w, *ws;      // routed and shared W_down at the pass's K offset
   const float *t, *ts;     // 8-bit scales [E or S, d]
   size_t kfull;
-  int d, n0, e0, ne, u0, n, stride, lane, se, base;
+  int d, n0, e0, ne, n, stride, lane, se, base;
   int lcol, lent, col, ent;
-  float gate = 0.0f, scale = 0.0f;
-  int tok = 0;
+  float scale = 0.0f;      // of the unit's channel times this lane's row of h
+  int hrow = 0;            // this lane's row of h
 
-  __device__ __forceinline__ DownWalk(const FewPlan& pl, float* ys, const FewArgs& p,
-                      size_t kf, size_t koff, int n0_, int e0_, int ne_, int u0_, int u1_, int st)
-      : plan(pl), ysum(ys), T(p.T), w(static_cast<const char*>(p.w_down) + koff),
+  __device__ __forceinline__ DownWalk(const FewPlan& pl, float* ys, int rh, const FewArgs& p,
+                                      size_t kf, size_t koff, int n0_, int e0_, int ne_, int cols,
+                                      int wave, int st)
+      : plan(pl), yrow(ys), rows_h(rh), more(koff > 0), w(static_cast<const char*>(p.w_down) + koff),
         ws(static_cast<const char*>(p.ws_down) + koff), t(p.t_down), ts(p.ts_down), kfull(kf),
-        d(p.d), n0(n0_), e0(e0_), ne(ne_), u0(u0_), n(u1_ - u0_), stride(st),
-        lane(threadIdx.x & 63), se(uniform(pl.shared_entries)), base(pl.first[e0_]) {
-    lcol = col = n > 0 ? u0 / ne : 0;
-    lent = ent = n > 0 ? u0 % ne : 0;
+        d(p.d), n0(n0_), e0(e0_), ne(ne_), n((cols * ne_ - wave + kFewWaves - 1) / kFewWaves),
+        stride(st), lane(threadIdx.x & 63), se(uniform(pl.shared_entries)), base(pl.first[e0_]) {
+    lcol = col = 0;
+    lent = ent = wave;
+    for (; lent >= ne; lent -= ne) ++lcol;
+    ent = lent;
+    col = lcol;
   }
   __device__ __forceinline__ int units() const { return n; }
   __device__ __forceinline__ const char* row(int u) {
-    if (u > 0 && ++lent == ne) {
-      lent = 0;
-      ++lcol;
-    }
+    if (u > 0)
+      for (lent += kFewWaves; lent >= ne; lent -= ne) ++lcol;
     const int i = e0 + lent;
     return (i < se ? ws : w) +
            (static_cast<size_t>(uniform(plan.expert[i])) * d + n0 + lcol) * kfull;
   }
   __device__ __forceinline__ int enter(int u, int (&off)[kUnitRows]) {
-    if (u > 0 && ++ent == ne) {
-      ent = 0;
-      ++col;
-    }
+    if (u > 0)
+      for (ent += kFewWaves; ent >= ne; ent -= ne) ++col;
     const int i = e0 + ent, r0 = plan.first[i];
     const int rows = uniform(plan.first[i + 1] - r0);
 #pragma unroll
     for (int r = 0; r < kUnitRows; ++r)
       off[r] = (r0 - base + (r < rows ? r : 0)) * stride + lane * 16;
     const int mine = r0 + (lane < rows ? lane : 0);
-    gate = plan.gate[mine];
-    tok = plan.tok[mine];
+    hrow = plan.hrow[mine];
     if (I8) {
       const int32_t* tp = reinterpret_cast<const int32_t*>(i < se ? ts : t) +
                           static_cast<size_t>(uniform(plan.expert[i])) * d;
-      scale = __int_as_float(((const_words)tp)[n0 + col]);
+      scale = plan.scale[mine] * __int_as_float(((const_words)tp)[n0 + col]);
     }
     return rows;
   }
-  __device__ __forceinline__ void leave(int u, int nr, const Acc (&acc)[kUnitRows]) {
+  __device__ __forceinline__ void leave(int, int nr, const Acc (&acc)[kUnitRows]) {
     Acc mine{0};
 #pragma unroll
     for (int r = 0; r < kUnitRows; ++r) {
@@ -459,8 +492,8 @@ struct DownWalk {
     if (lane < nr) {
       float v = static_cast<float>(mine);
       if (I8) v *= scale;
-      float* y = ysum + col * T + tok;
-      *y = fmaf(gate, v, *y);
+      float* y = yrow + col * rows_h + hrow;
+      *y = more ? *y + v : v;
     }
   }
   // reads through the scalar cache do not count as vector loads
@@ -483,20 +516,52 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
   __shared__ int s_word;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const int grid = gridDim.x;
   const int T = p.T, F = p.F;
-  const int pairs = T * kFewTopK, rows = pairs + S * T;
+  const int rows = T * (kFewTopK + S);
   int32_t* chunk_flag = p.ctrl;                    // [grid]
   int32_t* token_flag = p.ctrl + kFewGrid;         // [T]
   int32_t* row_flag = token_flag + kFewMaxTokens;  // [rows] (8-bit weights)
   bool planned = false;
 
-  if (tid == 0 && agent_load(chunk_flag + blockIdx.x) == kIdle) {
-    if (blockIdx.x < T) agent_store(token_flag + blockIdx.x, kStarted);
-    agent_store(chunk_flag + blockIdx.x, kStarted);
+  if (tid == 0) {
+    const int state = agent_load(chunk_flag + blockIdx.x);
+    if (state == kIdle) {
+      if (blockIdx.x < T) agent_store(token_flag + blockIdx.x, kStarted);
+      agent_store(chunk_flag + blockIdx.x, kStarted);
+    }
+    s_word = state == kDone;  // started late: others have done this chunk
   }
   plan_shared<S>(p, plan);
   __syncthreads();
+  bool skip = s_word;
+
+  // The down stage: this workgroup's output columns, in passes over the
+  // contributors (and over K, for wide experts) of as many rows of h as fit.
+  // (Taken while the selection is waited for.)
+  int n0 = 0, cols = 0, ybytes = 0, fall = 0, fpass = 0, stride = 0, capacity = 0;
+  const size_t ffull = static_cast<size_t>(F) * ESZ;
+  float* yrow = reinterpret_cast<float*>(pool);
+  auto down_shape = [&]() __attribute__((always_inline)) {
+    n0 = static_cast<int>(p.d * blockIdx.x / kFewGrid);
+    cols = static_cast<int>(p.d * (blockIdx.x + 1) / kFewGrid) - n0;
+    fall = static_cast<int>((ffull + kChunk - 1) / kChunk);
+    ybytes = (cols * rows * 4 + kChunk - 1) / kChunk * kChunk;
+    // every entry fits a pass: 8 rows of fpass chunks
+    fpass = min((fall + 1) / 2 * 2, (kPool - ybytes) / kChunk / PL / kUnitRows / 2 * 2);
+    stride = fpass * kChunk * PL;  // of a row of h in oper
+    capacity = (kPool - ybytes) / stride;
+  };
+  using Down = DownWalk<Acc, I8>;
+  auto pass_end = [&](int e0) {  // entries e0..pass_end-1 make a pass
+    int e1 = e0 + 1;
+    while (e1 < plan.entries && plan.first[e1 + 1] - plan.first[e0] <= capacity) ++e1;
+    return e1;
+  };
+  auto down_walk = [&](int k0, int e0, int e1) __attribute__((always_inline)) {
+    return Down(plan, yrow, rows, p, ffull, static_cast<size_t>(k0) * kChunk, n0, e0, e1 - e0,
+                cols, wave, stride);
+  };
+  RowStream<Dot, PL, Down> down;
 
   // ---- gate/up: this workgroup's chunk, then any that nobody has started.
   // Passes over K of as many chunks of every token as `oper` holds.
@@ -507,8 +572,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
   const int kpass = min((kall + 1) / 2 * 2, (kPool - kPartBytes) / kChunk / T / 2 * 2);
   int staged = -1;  // first K chunk of the pass that oper holds
   int token = blockIdx.x < T ? static_cast<int>(blockIdx.x) : -1;  // to be selected here
-  for (int chunk = blockIdx.x; chunk >= 0;
-       chunk = wait_all(chunk_flag, grid, blockIdx.x, &s_word)) {
+  for (int chunk = blockIdx.x; chunk >= 0;) {
     for (int part = 0; part < 2;) {  // shared, then routed experts
       if (token >= 0) {
         if (wave == 0) few_select<S>(p, token, lane);
@@ -516,6 +580,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
         token = -1;
       }
       if (part == 1 && !planned) {
+        down_shape();
         token = wait_all(token_flag, T, 0, &s_word);
         if (token >= 0) continue;
         plan_routed<S>(p, plan);
@@ -524,22 +589,39 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
       // columns of this chunk: the workgroups that select tokens have no share of
       // the shared experts
       const int ent0 = part == 0 ? 0 : plan.shared_entries;
-      const long long n = static_cast<long long>(part == 0 ? plan.shared_entries
-                                                           : plan.entries - ent0) * F;
-      const int share = part == 0 ? chunk - T : chunk, of = part == 0 ? grid - T : grid;
-      int c = share < 0 ? 0 : static_cast<int>(n * share / of);
-      const int cend = share < 0 ? 0 : static_cast<int>(n * (share + 1) / of);
+      // (at most 104 entries of 16384 columns, times 256: 32 bits)
+      const unsigned n = static_cast<unsigned>(part == 0 ? plan.shared_entries
+                                                         : plan.entries - ent0) * F;
+      const int share = part == 0 ? chunk - T : chunk;
+      int c = 0, cend = 0;
+      if (skip) {
+      } else if (part == 1) {
+        c = static_cast<int>(n * share / kFewGrid);
+        cend = static_cast<int>(n * (share + 1) / kFewGrid);
+      } else if (share >= 0) {
+        const unsigned of = kFewGrid - T;
+        c = static_cast<int>(n * share / of);
+        cend = static_cast<int>(n * (share + 1) / of);
+      }
+      int ent = ent0 + c / F, f = c - (ent - ent0) * F;  // entry and column of c
       for (; c < cend; c += kPartCols) {
         const int c1 = min(c + kPartCols, cend);
         for (int k0 = 0; k0 < kall; k0 += kpass) {
           const int kbytes = static_cast<int>(min(kfull - static_cast<size_t>(k0) * kChunk,
                                                   static_cast<size_t>(kpass) * kChunk));
+          GateWalk<Acc> walk(plan, part_sums, part == 0 ? p.ws_gate : p.w_gate,
+                             part == 0 ? p.ws_up : p.w_up, kfull,
+                             static_cast<size_t>(k0) * kChunk, F, c1 - c, wave, ent, f,
+                             kpass * kChunk, k0 > 0);
+          RowStream<Dot, 1, GateWalk<Acc>> stream;
+          stream.begin(walk, kbytes);
           if (staged != k0) {  // x of every token, zeros behind its last value
             __syncthreads();
             const char* x = I8 ? reinterpret_cast<const char*>(p.xq) : static_cast<const char*>(p.x);
             const int pieces = kpass * (kChunk / 16);
+            const float inv = 1.0f / static_cast<float>(pieces);
             for (int i = tid; i < T * pieces; i += kFewThreads) {
-              const int t = i / pieces, o = (i - t * pieces) * 16;
+              const int t = quotient(i, inv), o = (i - t * pieces) * 16;
               u32x4_t v{0, 0, 0, 0};
               if (o < kbytes)
                 v = *reinterpret_cast<const u32x4_t*>(x + t * kfull +
@@ -549,35 +631,38 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
             staged = k0;
           }
           __syncthreads();
-          const int span = c1 - c;
-          GateWalk<Acc> walk(plan, part_sums, part == 0 ? p.ws_gate : p.w_gate,
-                             part == 0 ? p.ws_up : p.w_up, kfull,
-                             static_cast<size_t>(k0) * kChunk, F, c + span * wave / kFewWaves,
-                             c + span * (wave + 1) / kFewWaves, c, ent0, kpass * kChunk, k0 > 0);
-          stream_rows<Dot, 1>(walk, kbytes, oper, 0);
+          stream.run(walk, oper, 0);
         }
         __syncthreads();
         // h = silu(gate) * up
+        const float inv = 1.0f / static_cast<float>(c1 - c);
         for (int i = tid; i < (c1 - c) * kUnitRows; i += kFewThreads) {
-          const int r = i / (c1 - c), j = i - r * (c1 - c);
-          const int ent = ent0 + (c + j) / F, f = (c + j) % F;
-          const int lr = plan.first[ent] + r;
-          if (lr >= plan.first[ent + 1]) continue;
+          const int r = quotient(i, inv), j = i - r * (c1 - c);
+          int je = ent, jf = f + j;  // entry and column of c + j
+          for (; jf >= F; jf -= F) ++je;
+          const int lr = plan.first[je] + r;
+          if (lr >= plan.first[je + 1]) continue;
           float gt = static_cast<float>(part_sums[j][0][r]);
           float up = static_cast<float>(part_sums[j][1][r]);
           if (I8) {
             const float sx = p.xs[plan.tok[lr]];
-            const size_t at = static_cast<size_t>(plan.expert[ent]) * F + f;
+            const size_t at = static_cast<size_t>(plan.expert[je]) * F + jf;
             gt *= sx * (part == 0 ? p.ts_gate : p.t_gate)[at];
             up *= sx * (part == 0 ? p.ts_up : p.t_up)[at];
           }
-          agent_store(p.h + static_cast<size_t>(plan.hrow[lr]) * F + f,
+          agent_store(p.h + static_cast<size_t>(plan.hrow[lr]) * F + jf,
                       gt / (1.0f + expf(-gt)) * up);
         }
+        for (f += kPartCols; f >= F; f -= F) ++ent;
       }
       ++part;
     }
     mark_done(chunk_flag, chunk);
+    skip = false;
+    // the first weights of the down stage come while the others finish
+    Down walk = down_walk(0, 0, pass_end(0));
+    down.begin(walk, static_cast<int>(min(ffull, static_cast<size_t>(fpass) * kChunk)));
+    chunk = wait_all(chunk_flag, kFewGrid, blockIdx.x, &s_word);
   }
 
   // ---- 8-bit weights: row r of h quantised by workgroup r
@@ -606,41 +691,28 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     }
   }
 
-  // ---- down: this workgroup's output columns, in passes over the contributors
-  // (and over K, for wide experts) of as many rows of h as `oper` holds.
-  const int n0 = static_cast<int>(static_cast<long long>(p.d) * blockIdx.x / grid);
-  const int cols = static_cast<int>(static_cast<long long>(p.d) * (blockIdx.x + 1) / grid) - n0;
-  const size_t ffull = static_cast<size_t>(F) * ESZ;
-  const int fall = static_cast<int>((ffull + kChunk - 1) / kChunk);
-  const int ywave = cols * T;  // floats of a wave's share of y
-  float* ysum = reinterpret_cast<float*>(pool);
-  const int ybytes = (kFewWaves * ywave * 4 + kChunk - 1) / kChunk * kChunk;
-  oper = pool + ybytes;
-  // every entry fits a pass: 8 rows of fpass chunks
-  const int fpass = min((fall + 1) / 2 * 2, (kPool - ybytes) / kChunk / PL / kUnitRows / 2 * 2);
-  const int stride = fpass * kChunk * PL;  // of a row of h in oper
-  const int capacity = (kPool - ybytes) / stride;
-  for (int i = tid; i < kFewWaves * ywave; i += kFewThreads) ysum[i] = 0.0f;
-  for (int i = tid; i < rows; i += kFewThreads) {
-    const int hr = plan.hrow[i], t = plan.tok[i];
-    const int slot = hr < pairs ? hr % kFewTopK : kFewTopK + (hr - pairs) / T;
-    float g = agent_load(p.gates + t * (kFewTopK + S) + slot);
-    if (I8) g *= agent_load(p.hs + hr);
-    plan.gate[i] = g;
+  // ---- down: the passes
+  // (what the passes' barriers make visible)
+  if (tid < rows) {
+    plan.gate[tid] = agent_load(p.gates + tid);
+    if (I8) plan.scale[tid] = agent_load(p.hs + plan.hrow[tid]);
   }
+  oper = pool + ybytes;
   for (int k0 = 0; k0 < fall; k0 += fpass) {
     const int kbytes = static_cast<int>(min(ffull - static_cast<size_t>(k0) * kChunk,
                                             static_cast<size_t>(fpass) * kChunk));
     for (int e0 = 0; e0 < plan.entries;) {
-      const int first = plan.first[e0];
-      int e1 = e0 + 1;
-      while (e1 < plan.entries && plan.first[e1 + 1] - first <= capacity) ++e1;
+      const int first = plan.first[e0], e1 = pass_end(e0);
+      Down walk = down_walk(k0, e0, e1);
+      if (k0 > 0 || e0 > 0) down.begin(walk, kbytes);
+      else down.resume(walk);
       const int n = plan.first[e1] - first;
       __syncthreads();  // the pass before is done with oper
       // 8 values of K at a time, zeros behind the last
       const int pieces = fpass * kChunk / (8 * ESZ);
+      const float inv = 1.0f / static_cast<float>(pieces);
       for (int i = tid; i < n * pieces; i += kFewThreads) {
-        const int r = i / pieces, k = (i - r * pieces) * 8;
+        const int r = quotient(i, inv), k = (i - r * pieces) * 8;
         char* at = oper + r * stride + k * ESZ;
         const size_t src = static_cast<size_t>(plan.hrow[first + r]) * F +
                            static_cast<size_t>(k0) * kChunk / ESZ + k;
@@ -675,20 +747,20 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
         }
       }
       __syncthreads();
-      const int ne = e1 - e0, units = cols * ne;
-      DownWalk<Acc, I8> walk(plan, ysum + wave * ywave, p, ffull, static_cast<size_t>(k0) * kChunk, n0,
-                             e0, ne, units * wave / kFewWaves, units * (wave + 1) / kFewWaves,
-                             stride);
-      stream_rows<Dot, PL>(walk, kbytes, oper, fpass * kChunk);
+      down.run(walk, oper, fpass * kChunk);
       e0 = e1;
     }
   }
   __syncthreads();
   for (int i = tid; i < T * cols; i += kFewThreads) {
     const int t = i / cols, c = i - t * cols;
+    const float* g = plan.gate + t * (kFewTopK + S);
+    const float* y = yrow + c * rows;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) v += ysum[w * ywave + c * T + t];
+    for (int j = 0; j < kFewTopK; ++j) v = fmaf(g[j], y[t * kFewTopK + j], v);
+#pragma unroll
+    for (int s = 0; s < S; ++s) v = fmaf(g[kFewTopK + s], y[(kFewTopK + s) * T + t], v);
     ActTraits<Y>::store(static_cast<Y*>(p.y) + static_cast<size_t>(t) * p.d + n0 + c, v);
   }
 }
@@ -698,11 +770,11 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
 template <typename X, bool INT8>
 static void route(const FewArgs& a, int ctrl, hipStream_t st) {
   const unsigned grid = a.E + a.S + 1 + (INT8 ? a.T : 0);
-  if (a.T == 1) few_route_kernel<X, 1, INT8><<<grid, 256, 0, st>>>(a, ctrl);
-  else if (a.T == 2) few_route_kernel<X, 2, INT8><<<grid, 256, 0, st>>>(a, ctrl);
-  else if (a.T <= 4) few_route_kernel<X, 4, INT8><<<grid, 256, 0, st>>>(a, ctrl);
-  else if (a.T <= 8) few_route_kernel<X, 8, INT8><<<grid, 256, 0, st>>>(a, ctrl);
-  else few_route_kernel<X, 16, INT8><<<grid, 256, 0, st>>>(a, ctrl);
+  if (a.T == 1) few_route_kernel<X, 1, INT8><<<grid, 512, 0, st>>>(a, ctrl);
+  else if (a.T == 2) few_route_kernel<X, 2, INT8><<<grid, 512, 0, st>>>(a, ctrl);
+  else if (a.T <= 4) few_route_kernel<X, 4, INT8><<<grid, 512, 0, st>>>(a, ctrl);
+  else if (a.T <= 8) few_route_kernel<X, 8, INT8><<<grid, 512, 0, st>>>(a, ctrl);
+  else few_route_kernel<X, 16, INT8><<<grid, 512, 0, st>>>(a, ctrl);
 }
 
 template <class Dot, typename Y>

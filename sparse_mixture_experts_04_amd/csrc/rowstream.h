@@ -76,7 +76,7 @@ __device__ __forceinline__ Acc wave_total(Acc v) {
   return v;
 }
 
-// Streams the units of one wave.  Walk tells where they are and takes the sums
+// The stream of one wave's units.  Walk tells where they are and takes the sums
 // (everything but the row offsets is the same on every lane):
 //   units()          number of units
 //   row(u)           address of the row's first byte of this pass; called with
@@ -85,23 +85,19 @@ __device__ __forceinline__ Acc wave_total(Acc v) {
 //                    of its activation rows (lane's 16 bytes included) and
 //                    returns their number
 //   leave(u, n, acc) takes the n lane sums of unit u
-// kbytes: bytes of a row in this pass; planes of activation rows lie
-// plane_bytes apart (their sums are added).
+// begin() issues the first loads; it needs the weights' addresses only, so it
+// comes before what the activation rows wait for.  run() does the rest.
+// kbytes: bytes of a row in this pass; planes of activation rows lie plane_bytes
+// apart (their sums are added).
 template <class Dot, int PL, class Walk>
-__device__ __forceinline__ void stream_rows(Walk& walk, int kbytes, const char* oper,
-                                            int plane_bytes) {
+struct RowStream {
   using Acc = typename Dot::Acc;
-  const int units = walk.units();
-  if (units <= 0) return;
-  const int lane = threadIdx.x & 63;
-  const int nkb = (kbytes + kBlock * kChunk - 1) / (kBlock * kChunk);
-  const int total = units * nkb;
   u32x4_t w[kRing][kBlock];
+  const char* lrow;  // load side: the next block is block lk of unit lu
+  int lu, lk, units, kbytes, nkb;
 
-  // load side
-  int lu = 0, lk = 0;
-  const char* lrow = walk.row(0);
-  auto load = [&](u32x4_t (&f)[kBlock]) __attribute__((always_inline)) {
+  __device__ __forceinline__ void load(Walk& walk, u32x4_t (&f)[kBlock]) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < kBlock; ++j) {
       int o = (lk * kBlock + j) * kChunk + lane * 16;
@@ -115,54 +111,71 @@ __device__ __forceinline__ void stream_rows(Walk& walk, int kbytes, const char* 
       lk = 0;
       lrow = walk.row(lu);
     }
-  };
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) load(w[i]);
-
-  // multiply side
-  int cu = 0, ck = 0, rows = 0;
-  int off[kUnitRows];
-  Acc acc[kUnitRows];
-#pragma unroll
-  for (int r = 0; r < kUnitRows; ++r) {
-    acc[r] = Acc{0};
-    off[r] = 0;
   }
-  rows = walk.enter(0, off);
-  for (int b = 0; b < total; b += kRing) {
+
+  __device__ __forceinline__ void begin(Walk& walk, int kb) {
+    units = walk.units();
+    kbytes = kb;
+    nkb = (kb + kBlock * kChunk - 1) / (kBlock * kChunk);
+    lu = lk = 0;
+    if (units <= 0) return;
+    lrow = walk.row(0);
 #pragma unroll
-    for (int i = 0; i < kRing; ++i) {
-      if (b + i >= total) break;
-      load(w[(i + kRing - 1) % kRing]);
-      auto mul = [&](auto nr) __attribute__((always_inline)) {
-        constexpr int N = decltype(nr)::value;
+    for (int i = 0; i < kRing - 1; ++i) load(walk, w[i]);
+  }
+
+  // Brings the load side of a walk made anew to where begin() left it.
+  __device__ __forceinline__ void resume(Walk& walk) {
+    for (int u = 1; u <= lu; ++u) walk.row(u);
+  }
+
+  __device__ __forceinline__ void run(Walk& walk, const char* oper, int plane_bytes) {
+    const int total = units * nkb;
+    if (total <= 0) return;
+    int cu = 0, ck = 0;
+    int off[kUnitRows];
+    Acc acc[kUnitRows];
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
+    for (int r = 0; r < kUnitRows; ++r) {
+      acc[r] = Acc{0};
+      off[r] = 0;
+    }
+    int rows = walk.enter(0, off);
+    for (int b = 0; b < total; b += kRing) {
 #pragma unroll
-          for (int j = 0; j < kBlock; ++j)
+      for (int i = 0; i < kRing; ++i) {
+        if (b + i >= total) break;
+        load(walk, w[(i + kRing - 1) % kRing]);
+        auto mul = [&](auto nr) __attribute__((always_inline)) {
+          constexpr int N = decltype(nr)::value;
 #pragma unroll
-            for (int p = 0; p < PL; ++p)
-              Dot::mul(w[i][j],
-                       *reinterpret_cast<const u32x4_t*>(oper + off[r] + p * plane_bytes +
-                                                         (ck * kBlock + j) * kChunk),
-                       acc[r]);
-          // no more than two rows' operands in registers at once
-          if (r & 1) __builtin_amdgcn_sched_barrier(0);
+          for (int r = 0; r < N; ++r) {
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j)
+#pragma unroll
+              for (int p = 0; p < PL; ++p)
+                Dot::mul(w[i][j],
+                         *reinterpret_cast<const u32x4_t*>(oper + off[r] + p * plane_bytes +
+                                                           (ck * kBlock + j) * kChunk),
+                         acc[r]);
+            // no more than two rows' operands in registers at once
+            if (r & 1) __builtin_amdgcn_sched_barrier(0);
+          }
+        };
+        if (rows == 1) mul(std::integral_constant<int, 1>{});
+        else if (rows == 2) mul(std::integral_constant<int, 2>{});
+        else if (rows <= 4) mul(std::integral_constant<int, 4>{});
+        else mul(std::integral_constant<int, 8>{});
+        if (++ck == nkb) {
+          walk.leave(cu, rows, acc);
+          ck = 0;
+#pragma unroll
+          for (int r = 0; r < kUnitRows; ++r) acc[r] = Acc{0};
+          if (++cu < units) rows = walk.enter(cu, off);
         }
-      };
-      if (rows == 1) mul(std::integral_constant<int, 1>{});
-      else if (rows == 2) mul(std::integral_constant<int, 2>{});
-      else if (rows <= 4) mul(std::integral_constant<int, 4>{});
-      else mul(std::integral_constant<int, 8>{});
-      if (++ck == nkb) {
-        walk.leave(cu, rows, acc);
-        ck = 0;
-#pragma unroll
-        for (int r = 0; r < kUnitRows; ++r) acc[r] = Acc{0};
-        if (++cu < units) rows = walk.enter(cu, off);
       }
     }
   }
-}
+};
 
 }  // namespace moe
