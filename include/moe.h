@@ -451,6 +451,7 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
  * where given.  A token whose x holds a NaN or an infinity gets NaN gates or
  * outputs, its choice of experts is unspecified but valid.  Results are bitwise
  * reproducible and a token's do not depend on the other tokens' values.
+ * x and y must not share memory (MOE_ERR_UNSUPPORTED).
  * moe_forward_few_int8 takes 8-bit weights: x is quantised per token, h per row
  * (from fp32).  Both calls take the workspace of
  * moe_forward_few_workspace_size; calls that overlap need one each. */

@@ -206,6 +206,8 @@ def with_router_planes(weights, planes):
         raise ValueError("planes must be a contiguous bfloat16 tensor from router_planes")
     wt = Weights.from_buffer_copy(weights)
     wt.w_router_planes = planes.data_ptr() if planes is not None else None
+    if hasattr(weights, "made_of"):
+        wt.made_of = weights.made_of
     return wt
 
 
@@ -521,6 +523,7 @@ def gemm_int8(a, a_scale, w, w_scale, y, offsets=None, ws=None):
     dev = _on_gpu(a, "a")
     if a.dim() != 2 or w.dim() != 3:
         raise ValueError("gemm_int8 takes a [M, Kp] and w [E, N, Kp]")
+    _on_gpu(y, "y")
     M, Kp = a.shape
     E, N, _ = w.shape
     if Kp == 0 or Kp % 128:
@@ -628,7 +631,8 @@ def forward_few_workspace(desc, device):
 def forward_few(desc, x, weights, bias, y, topk_idx=None, gates=None, ws=None):
     """The whole layer for 1 to 16 tokens in two kernels: moe_forward_few with
     Weights of desc's dtype, moe_forward_few_int8 with WeightsInt8.  The bias is
-    read, not updated.  Calls that overlap need a workspace each."""
+    read, not updated; x and y must not share memory.  Calls that overlap need a
+    workspace each."""
     dev = _on_gpu(x, "x")
     _weights_for(desc, weights, x.device, (Weights, WeightsInt8), "forward_few")
     ws = forward_few_workspace(desc, x.device) if ws is None else ws

@@ -46,6 +46,14 @@ moe_status check_few_desc(const moe_desc* d) {
   return MOE_OK;
 }
 
+// Whether the T tokens' x and y share memory: a workgroup of the few-token layer
+// that starts late may still read x when others store y.
+bool in_place(const Shape& s, const void* x, const void* y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t n = static_cast<uintptr_t>(s.T) * s.d * (s.bf16 ? 2 : 4);
+  return a < b + n && b < a + n;
+}
+
 // Every matrix that is read in 16-byte pieces (pointers a layer does not use
 // may hold anything).
 bool weights_aligned(const Shape& s, std::initializer_list<const void*> routed,
@@ -261,7 +269,7 @@ moe_status moe_forward_few(const moe_desc* desc, const void* x, const moe_weight
   if (s.T > 0 && (!x || !y)) return MOE_ERR_NULL;
   // MXFP4 codes are a quarter of the bytes this call would read
   if (w->sc_gate || w->sc_up || w->sc_down) return MOE_ERR_DTYPE;
-  if (!aligned16(x) || !aligned16(w->w_router) ||
+  if (in_place(s, x, y) || !aligned16(x) || !aligned16(w->w_router) ||
       !weights_aligned(s, {w->w_gate, w->w_up, w->w_down}, {w->ws_gate, w->ws_up, w->ws_down}))
     return MOE_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < few_ws_bytes(s)) return MOE_ERR_WORKSPACE;
@@ -283,7 +291,7 @@ moe_status moe_forward_few_int8(const moe_desc* desc, const void* x, const moe_w
   const Shape s = to_shape(desc);
   if (!int8_weights_ok(w, s) || !w->w_router || !bias) return MOE_ERR_NULL;
   if (s.T > 0 && (!x || !y)) return MOE_ERR_NULL;
-  if (!aligned16(x) || !aligned16(w->w_router) ||
+  if (in_place(s, x, y) || !aligned16(x) || !aligned16(w->w_router) ||
       !weights_aligned(s, {w->w_gate, w->w_up, w->w_down}, {w->ws_gate, w->ws_up, w->ws_down}))
     return MOE_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < few_ws_bytes(s)) return MOE_ERR_WORKSPACE;

@@ -83,6 +83,73 @@ def test_layer_matches_64_bits(shape, form):
     assert torch.equal(y, y3)
 
 
+def gpu_layer(T, d, F, E, S, act, seed):
+    """A layer drawn on the GPU (large ones take long to draw on the host)."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    dt = torch.float32 if act == "f32" else torch.bfloat16
+
+    def normal(*shape, std=1.0, dtype=dt):
+        return (torch.randn(shape, generator=g, device=DEV) * std).to(dtype)
+    inp = {"x": normal(T, d), "w_router": normal(E + S, d, std=d ** -0.5, dtype=torch.float32),
+           "bias": normal(E, std=0.05, dtype=torch.float32)}
+    for n, c in (("w", E), ("ws", S)):
+        inp[n + "_gate"] = normal(c, F, d, std=d ** -0.5)
+        inp[n + "_up"] = normal(c, F, d, std=d ** -0.5)
+        inp[n + "_down"] = normal(c, d, F, std=F ** -0.5)
+    return inp
+
+
+@pytest.mark.parametrize("form", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("T,d,F,E,S", [(16, 7168, 128, 64, 2), (1, 16384, 128, 64, 1),
+                                       (16, 16384, 128, 64, 0), (3, 256, 16384, 64, 1),
+                                       (16, 256, 8192, 64, 2), (16, 4096, 3200, 64, 1)])
+def test_wide_layers(T, d, F, E, S, form):
+    """Widths that take several passes over K in either stage."""
+    print(f"few wide T={T} d={d} F={F} S={S} {form}", flush=True)
+    act = "f32" if form == "f32" else "bf16"
+    cfg = MoEConfig("few_wide", T=T, d=d, F=F, E=E, S=S, act=act)
+    inp = gpu_layer(T, d, F, E, S, act, T + d + F)
+    desc = L.make_desc(T, d, F, inp["x"].dtype, E=E, S=S)
+    w, q = L.int8_weights(inp) if form == "int8" else (L.weights_from(inp), inp)
+    y, idx, g = few(desc, inp, w)
+    check(cfg, desc, inp, q, form == "int8", y, idx, g)
+    del w, q, inp
+    torch.cuda.empty_cache()
+
+
+def test_refuses_y_over_x():
+    cfg = MoEConfig("few_alias", T=4, d=256, F=128, act="bf16", E=64)
+    inp, desc, w, _ = setup(cfg)
+    with pytest.raises(L.MoEError, match="UNSUPPORTED"):
+        L.forward_few(desc, inp["x"], w, inp["bias"], inp["x"])
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_beside_other_work(int8):
+    """While large products hold the compute units, workgroups of the layer start
+    late or one after another."""
+    cfg = MoEConfig("few_busy", T=9, d=1024, F=512, act="bf16")
+    inp, desc, w, _ = setup(cfg, int8)
+    want = few(desc, inp, w)[0]
+    a = torch.randn((8192, 8192), device=DEV, dtype=torch.bfloat16)
+    side, own = torch.cuda.Stream(), torch.cuda.Stream()
+    ws = L.forward_few_workspace(desc, DEV)
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                a @ a
+        with torch.cuda.stream(own):
+            for _ in range(4):
+                L.forward_few(desc, inp["x"], w, inp["bias"], out, ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("int8", [False, True])
 def test_every_token_the_same(int8):
     """All 16 tokens pick the same six experts: full row tiles."""

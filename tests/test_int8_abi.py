@@ -117,21 +117,25 @@ def test_forward_few_checks():
                      (dict(gate_scale=0.0), 2), (dict(T=16), 0), (dict(S=0), 0), (dict(T=0), 0)):
         assert size_of(size, desc(**kw))[0] == code, kw
     w = L.Weights(*([0x1000] * 7))
-    assert few(ref(d), P, ref(w), P, P, None, None, P, need - 1, None) == 4
-    assert few(ref(d), P, None, P, P, None, None, P, need, None) == 1
-    assert few(ref(d), None, ref(w), P, P, None, None, P, need, None) == 1
+    Y = ctypes.c_void_p(0x100000)          # apart from x
+    for y in (P, ctypes.c_void_p(0x1000 + 8 * 512 * 2 - 16), ctypes.c_void_p(0x800)):
+        assert few(ref(d), P, ref(w), P, y, None, None, P, need, None) == 5    # overlaps x
+        assert few8(ref(d), P, ref(w8()), P, y, None, None, P, need, None) == 5
+    assert few(ref(d), P, ref(w), P, Y, None, None, P, need - 1, None) == 4
+    assert few(ref(d), P, None, P, Y, None, None, P, need, None) == 1
+    assert few(ref(d), None, ref(w), P, Y, None, None, P, need, None) == 1
     assert few(ref(d), P, ref(w), None, P, None, None, P, need, None) == 1
     assert few(ref(d), P, ref(w), P, None, None, None, P, need, None) == 1
-    assert few(ref(d), ODD, ref(w), P, P, None, None, P, need, None) == 5
-    assert few(ref(d), P, ref(L.Weights(0x1000, 0x1004, *([0x1000] * 5))), P, P, None, None, P,
+    assert few(ref(d), ODD, ref(w), P, Y, None, None, P, need, None) == 5
+    assert few(ref(d), P, ref(L.Weights(0x1000, 0x1004, *([0x1000] * 5))), P, Y, None, None, P,
                need, None) == 5
     # MXFP4 matrices are a quarter of what this call reads
     fp4 = L.Weights(*([0x1000] * 10))
-    assert few(ref(d), P, ref(fp4), P, P, None, None, P, need, None) == 3
-    assert few8(ref(d), P, ref(w8(w_router=None)), P, P, None, None, P, need, None) == 1
-    assert few8(ref(d), P, ref(w8(t_down=None)), P, P, None, None, P, need, None) == 1
-    assert few8(ref(d), P, ref(w8(w_down=0x1008)), P, P, None, None, P, need, None) == 5
-    assert few8(ref(d), P, ref(w8()), P, P, None, None, None, need, None) == 4
+    assert few(ref(d), P, ref(fp4), P, Y, None, None, P, need, None) == 3
+    assert few8(ref(d), P, ref(w8(w_router=None)), P, Y, None, None, P, need, None) == 1
+    assert few8(ref(d), P, ref(w8(t_down=None)), P, Y, None, None, P, need, None) == 1
+    assert few8(ref(d), P, ref(w8(w_down=0x1008)), P, Y, None, None, P, need, None) == 5
+    assert few8(ref(d), P, ref(w8()), P, Y, None, None, None, need, None) == 4
     assert few(ref(desc(T=0)), None, ref(w), P, None, None, None, P, need, None) == 0
 
 

@@ -119,7 +119,10 @@ def check_product(a, sa, w, t, y, offsets=None, untouched=None):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 1), (1, 768, 2048), (3, 5, 130), (16, 33, 128), (17, 257, 200), (33, 16, 4000),
     (64, 64, 64), (65, 300, 384), (127, 129, 1000), (200, 256, 7168), (257, 513, 640),
-    (600, 1000, 513), (1500, 770, 256), (2, 7168, 2048)])
+    (600, 1000, 513), (1500, 770, 256), (2, 7168, 2048),
+    # 128-row and 256-row tiles, whole and ragged columns
+    (4096, 513, 7168), (4096, 520, 7168), (9000, 1030, 2048), (9001, 1027, 2048),
+    (20000, 768, 2048)])
 def test_product_sizes(M, N, K, out):
     print(f"gemm_int8 M={M} N={N} K={K} {out}", flush=True)
     kp = L.code_row(K)
@@ -154,10 +157,12 @@ OFFSETS = [
 
 
 @pytest.mark.parametrize("offsets", OFFSETS)
-@pytest.mark.parametrize("scale", [1, 17, 60])
-def test_product_groups(offsets, scale):
+@pytest.mark.parametrize("scale,N,K", [(1, 130, 256), (17, 130, 256), (60, 130, 256),
+                                       (100, 1030, 2048), (400, 1030, 2048)])
+def test_product_groups(offsets, scale, N, K):
+    print(f"groups {offsets} x {scale}", flush=True)
     off = [o * scale for o in offsets]
-    M, N, K, E = 40 * scale, 130, 256, len(off) - 1
+    M, E = 40 * scale, len(off) - 1
     a, w = rand_codes((M, K), 1), rand_codes((E, N, K), 2)
     sa = torch.rand(M, generator=gen(3), device=DEV) + 0.1
     t = torch.rand((E, N), generator=gen(4), device=DEV) + 0.1
@@ -222,9 +227,10 @@ def test_product_refusals():
         L.gemm_int8(a, sa, w, t, y, offsets=off, ws=torch.empty(8, dtype=torch.uint8, device=DEV))
 
 
-def test_product_other_stream_and_graph():
-    M, N, K, E = 300, 200, 512, 3
-    off = torch.tensor([0, 90, 90, 300], dtype=torch.int32, device=DEV)
+@pytest.mark.parametrize("M,N,K", [(300, 200, 512), (4096, 1024, 2048), (12000, 1030, 2048)])
+def test_product_other_stream_and_graph(M, N, K):
+    E = 3
+    off = torch.tensor([0, M // 3, M // 3, M], dtype=torch.int32, device=DEV)
     x, w = randn((M, K), 1, BF16), rand_codes((E, N, K), 2)
     t = torch.rand((E, N), generator=gen(4), device=DEV)
     ref = torch.empty((M, N), dtype=BF16, device=DEV)
@@ -265,6 +271,8 @@ FFN = [
     MoEConfig("i8_many", T=2300, d=256, F=256, act="bf16", E=64, S=1),
     MoEConfig("i8_no_shared", T=700, d=512, F=128, act="bf16", E=128, S=0),
     MoEConfig("i8_wide", T=5200, d=256, F=640, act="bf16", E=128, S=1),
+    MoEConfig("i8_big", T=6000, d=1024, F=768, act="bf16", E=64, S=2),
+    MoEConfig("i8_big_f32", T=6000, d=1024, F=768, act="f32", E=64, S=1),
 ]
 
 
@@ -329,8 +337,9 @@ def test_experts_match_64_bits(i):
     assert within(out, (g * yd).sum(1), 16 * R.EPS32 * (g * yd).abs().sum(1))
 
 
-def test_experts_capacity_leaves_other_rows():
-    cfg = MoEConfig("i8_cap", T=400, d=256, F=128, act="bf16", E=64, S=1, capacity_factor=1.0)
+@pytest.mark.parametrize("T,d,F", [(400, 256, 128), (6000, 1024, 768)])
+def test_experts_capacity_leaves_other_rows(T, d, F):
+    cfg = MoEConfig("i8_cap", T=T, d=d, F=F, act="bf16", E=64, S=1, capacity_factor=1.0)
     inp = layer(cfg)
     desc = L.make_desc(cfg.T, cfg.d, cfg.F, BF16, E=cfg.E, S=cfg.S, capacity_factor=1.0)
     r = routed(cfg, desc, inp)
