@@ -33,7 +33,7 @@ struct FewArgs {
   int32_t* topk_out;       // [T, 6] or null
   float* gates_out;        // [T, 6 + S] or null
   // workspace; rows of h are the 6 T pairs, then shared expert s's T rows
-  double2* zs;             // [T, E+S] logits and their sigmoids
+  double2* zs;             // [T, E+S] log sigmoid (logsumexp gates) and sigmoid of z
   int32_t* topk;           // [T, 6]
   float* gates;            // [T, 6 + S]
   int32_t* ctrl;           // few_ctrl_ints

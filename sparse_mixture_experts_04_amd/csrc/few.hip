@@ -67,7 +67,7 @@ __device__ __forceinline__ void load4(const bf16_t* p, double (&v)[4]) {
 }
 
 // Block b < E + S: the logits of router row b for all tokens (products exact
-// in fp64, sums in a fixed order) and their sigmoids.  Block E + S clears the control block of
+// in fp64, sums in a fixed order) as sigmoids (and their logarithms).  Block E + S clears the control block of
 // few_ffn_kernel.  INT8: block E + S + 1 + t quantises token t.  TM: tokens
 // rounded up to a power of two.
 template <typename X, int TM, bool INT8>
@@ -114,7 +114,9 @@ __global__ __launch_bounds__(512) void few_route_kernel(FewArgs p, int ctrl_ints
     double z = sum[0][tid];
 #pragma unroll
     for (int i = 1; i < 8; ++i) z += sum[i][tid];
-    p.zs[static_cast<size_t>(tid) * rows + b] = double2{z, sigmoid64(z)};
+    // log sigmoid(z) for gates by logsumexp, and sigmoid(z)
+    const double l = p.logsumexp ? fmin(z, 0.0) - log1p(exp(-fabs(z))) : 0.0;
+    p.zs[static_cast<size_t>(tid) * rows + b] = double2{l, sigmoid64(z)};
   }
 }
 
@@ -160,16 +162,14 @@ __device__ __forceinline__ void few_select(const FewArgs& p, int t, int lane) {
   // lane j < 6 + S: contributor j
   const bool mine = lane < kFewTopK + S;
   const double2 v = mine ? zs[id] : double2{0.0, 0.0};
-  double g;
-  if (p.logsumexp) {  // exp(l - logsumexp l), l = logsigmoid(z)
-    const double l = fmin(v.x, 0.0) - log1p(exp(-fabs(v.x)));
-    double m = mine ? l : -INFINITY;
+  double e = v.y;  // the gates are e / sum e, times gate_scale
+  if (p.logsumexp) {  // exp(l - logsumexp l) = exp(l - m) / sum exp(l - m)
+    double m = mine ? v.x : -INFINITY;
     int who = lane;
     wave_argmax(m, who, lane);
-    g = exp(l - (m + log(wave_sum(mine ? exp(l - m) : 0.0, lane)))) * p.gate_scale;
-  } else {
-    g = v.y / (wave_sum(v.y, lane) / p.gate_scale);
+    e = mine ? exp(v.x - m) : 0.0;
   }
+  const double g = e / (wave_sum(e, lane) / p.gate_scale);
   if (!mine) return;
   const int at = t * (kFewTopK + S) + lane;
   agent_store(p.gates + at, static_cast<float>(g));
@@ -256,23 +256,23 @@ struct FewPlan {
 
 // Entries of the shared experts (all threads, a barrier after it).
 template <int S>
-__device__ __forceinline__ void plan_shared(const FewArgs& p, FewPlan& s) {
+__device__ __forceinline__ void plan_shared(int T, FewPlan& s) {
   static_assert(S <= 2 && kFewMaxTokens <= 2 * kUnitRows, "two shared experts of two entries");
-  const int per = p.T > kUnitRows ? 2 : 1;
+  const int per = T > kUnitRows ? 2 : 1;
   const int tid = threadIdx.x;
-  if (tid < S * p.T) {
-    const int e = tid >= p.T ? 1 : 0, t = tid - e * p.T;
+  if (tid < S * T) {
+    const int e = tid >= T ? 1 : 0, t = tid - e * T;
     s.tok[tid] = t;
-    s.hrow[tid] = p.T * kFewTopK + tid;
+    s.hrow[tid] = T * kFewTopK + tid;
   }
   if (tid < S * per) {
     const int e = per == 2 ? tid >> 1 : tid, half = per == 2 ? tid & 1 : 0;
-    s.first[tid] = e * p.T + half * kUnitRows;
+    s.first[tid] = e * T + half * kUnitRows;
     s.expert[tid] = e;
   }
   if (tid == 0) {
     s.shared_entries = S * per;
-    s.first[S * per] = S * p.T;
+    s.first[S * per] = S * T;
   }
 }
 
@@ -506,8 +506,21 @@ template <> struct FewTraits<DotBf16> { static constexpr int ESZ = 2, PLANES = 2
 template <> struct FewTraits<DotF32> { static constexpr int ESZ = 4, PLANES = 1; };
 template <> struct FewTraits<DotI8> { static constexpr int ESZ = 1, PLANES = 1; };
 
+// The kernel's arguments, read again where they are needed.  Kept from the start,
+// they take most of the scalar registers through every loop, and what does not
+// fit is spilled: with that the kernel was 5 to 25% slower.
+__device__ __forceinline__ FewArgs args_again() {
+  typedef const FewArgs __attribute__((address_space(4)))* arg_ptr;
+  arg_ptr k = (arg_ptr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(k));  // not the loads from before
+  FewArgs a;
+  __builtin_memcpy(&a, (const FewArgs*)k, sizeof(a));
+  return a;
+}
+
+// The arguments (args_again reads them).
 template <class Dot, typename Y, int S>
-__global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
+__global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs) {
   using Acc = typename Dot::Acc;
   constexpr int ESZ = FewTraits<Dot>::ESZ, PL = FewTraits<Dot>::PLANES;
   constexpr bool I8 = ESZ == 1;
@@ -516,10 +529,11 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
   __shared__ int s_word;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
-  const int T = p.T, F = p.F;
+  const FewArgs p0 = args_again();
+  const int T = p0.T, F = p0.F, d = p0.d;
   const int rows = T * (kFewTopK + S);
-  int32_t* chunk_flag = p.ctrl;                    // [grid]
-  int32_t* token_flag = p.ctrl + kFewGrid;         // [T]
+  int32_t* chunk_flag = p0.ctrl;                   // [grid]
+  int32_t* token_flag = chunk_flag + kFewGrid;     // [T]
   int32_t* row_flag = token_flag + kFewMaxTokens;  // [rows] (8-bit weights)
   bool planned = false;
 
@@ -531,7 +545,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     }
     s_word = state == kDone;  // started late: others have done this chunk
   }
-  plan_shared<S>(p, plan);
+  plan_shared<S>(T, plan);
   __syncthreads();
   bool skip = s_word;
 
@@ -542,8 +556,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
   const size_t ffull = static_cast<size_t>(F) * ESZ;
   float* yrow = reinterpret_cast<float*>(pool);
   auto down_shape = [&]() __attribute__((always_inline)) {
-    n0 = static_cast<int>(p.d * blockIdx.x / kFewGrid);
-    cols = static_cast<int>(p.d * (blockIdx.x + 1) / kFewGrid) - n0;
+    n0 = static_cast<int>(d * blockIdx.x / kFewGrid);
+    cols = static_cast<int>(d * (blockIdx.x + 1) / kFewGrid) - n0;
     fall = static_cast<int>((ffull + kChunk - 1) / kChunk);
     ybytes = (cols * rows * 4 + kChunk - 1) / kChunk * kChunk;
     // every entry fits a pass: 8 rows of fpass chunks
@@ -558,14 +572,14 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     return e1;
   };
   auto down_walk = [&](int k0, int e0, int e1) __attribute__((always_inline)) {
-    return Down(plan, yrow, rows, p, ffull, static_cast<size_t>(k0) * kChunk, n0, e0, e1 - e0,
+    return Down(plan, yrow, rows, args_again(), ffull, static_cast<size_t>(k0) * kChunk, n0, e0, e1 - e0,
                 cols, wave, stride);
   };
   RowStream<Dot, PL, Down> down;
 
   // ---- gate/up: this workgroup's chunk, then any that nobody has started.
   // Passes over K of as many chunks of every token as `oper` holds.
-  const size_t kfull = static_cast<size_t>(p.d) * ESZ;
+  const size_t kfull = static_cast<size_t>(d) * ESZ;
   const int kall = static_cast<int>((kfull + kChunk - 1) / kChunk);
   auto part_sums = reinterpret_cast<Acc(*)[2][kUnitRows]>(pool);
   char* oper = pool + kPartBytes;
@@ -575,7 +589,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
   for (int chunk = blockIdx.x; chunk >= 0;) {
     for (int part = 0; part < 2;) {  // shared, then routed experts
       if (token >= 0) {
-        if (wave == 0) few_select<S>(p, token, lane);
+        if (wave == 0) few_select<S>(args_again(), token, lane);
         mark_done(token_flag, token);
         token = -1;
       }
@@ -583,7 +597,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
         down_shape();
         token = wait_all(token_flag, T, 0, &s_word);
         if (token >= 0) continue;
-        plan_routed<S>(p, plan);
+        plan_routed<S>(args_again(), plan);
         planned = true;
       }
       // columns of this chunk: the workgroups that select tokens have no share of
@@ -609,6 +623,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
         for (int k0 = 0; k0 < kall; k0 += kpass) {
           const int kbytes = static_cast<int>(min(kfull - static_cast<size_t>(k0) * kChunk,
                                                   static_cast<size_t>(kpass) * kChunk));
+          const FewArgs p = args_again();
           GateWalk<Acc> walk(plan, part_sums, part == 0 ? p.ws_gate : p.w_gate,
                              part == 0 ? p.ws_up : p.w_up, kfull,
                              static_cast<size_t>(k0) * kChunk, F, c1 - c, wave, ent, f,
@@ -635,6 +650,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
         }
         __syncthreads();
         // h = silu(gate) * up
+        const FewArgs p = args_again();
         const float inv = 1.0f / static_cast<float>(c1 - c);
         for (int i = tid; i < (c1 - c) * kUnitRows; i += kFewThreads) {
           const int r = quotient(i, inv), j = i - r * (c1 - c);
@@ -673,6 +689,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     for (int r = static_cast<int>(blockIdx.x) < rows ? static_cast<int>(blockIdx.x) : -2;
          r != -1; r = wait_all(row_flag, rows, blockIdx.x % rows, &s_word)) {
       if (r < 0) continue;
+      const FewArgs p = args_again();
       const uint64_t* hr = reinterpret_cast<const uint64_t*>(p.h + static_cast<size_t>(r) * F);
       uint64_t* qr = reinterpret_cast<uint64_t*>(p.hq + static_cast<size_t>(r) * F);
       const float s = quantize_row<kFewThreads>(
@@ -694,6 +711,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
   // ---- down: the passes
   // (what the passes' barriers make visible)
   if (tid < rows) {
+    const FewArgs p = args_again();
     plan.gate[tid] = agent_load(p.gates + tid);
     if (I8) plan.scale[tid] = agent_load(p.hs + plan.hrow[tid]);
   }
@@ -709,6 +727,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
       const int n = plan.first[e1] - first;
       __syncthreads();  // the pass before is done with oper
       // 8 values of K at a time, zeros behind the last
+      const FewArgs p = args_again();
       const int pieces = fpass * kChunk / (8 * ESZ);
       const float inv = 1.0f / static_cast<float>(pieces);
       for (int i = tid; i < n * pieces; i += kFewThreads) {
@@ -752,6 +771,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     }
   }
   __syncthreads();
+  const FewArgs p = args_again();
   for (int i = tid; i < T * cols; i += kFewThreads) {
     const int t = i / cols, c = i - t * cols;
     const float* g = plan.gate + t * (kFewTopK + S);
@@ -761,7 +781,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs p) {
     for (int j = 0; j < kFewTopK; ++j) v = fmaf(g[j], y[t * kFewTopK + j], v);
 #pragma unroll
     for (int s = 0; s < S; ++s) v = fmaf(g[kFewTopK + s], y[(kFewTopK + s) * T + t], v);
-    ActTraits<Y>::store(static_cast<Y*>(p.y) + static_cast<size_t>(t) * p.d + n0 + c, v);
+    ActTraits<Y>::store(static_cast<Y*>(p.y) + static_cast<size_t>(t) * d + n0 + c, v);
   }
 }
 

@@ -15,7 +15,13 @@
 //
 // kRing blocks of kBlock chunks are held in registers, all but one of them in
 // flight.  Loads are issued unconditionally (past the last unit the last block
-// is read again) so that the compiler can count them.
+// is read again) so that the compiler can count them.  Small is fast here: code
+// that the weights have driven out of the caches costs 0.4 us per 128 bytes, and
+// a register too many (scratch memory) cost the whole kernel 10 to 20%.  Measured
+// on the few-token layer, us at T=1 d=2048 F=768 / T=1 d=7168 F=2048 / T=16 there:
+// ring 6 of 2 chunks 56 / 174 / 1516, 4 of 2 43 / 152 / 1244, 4 of 1 35 / 145 /
+// 1261, and with products of 1, 3 and 8 rows instead of 1, 2, 4 and 8 (and the
+// kernel's arguments not held in registers) 30 / 120 / 1192.
 #pragma once
 
 #include <type_traits>
@@ -26,7 +32,7 @@
 namespace moe {
 
 constexpr int kChunk = 1024;     // bytes of a row per load instruction
-constexpr int kBlock = 2;        // chunks per block
+constexpr int kBlock = 1;        // chunks per block
 constexpr int kRing = 4;         // blocks in registers
 constexpr int kUnitRows = 8;     // activation rows of a unit, at most
 
@@ -163,8 +169,7 @@ struct RowStream {
           }
         };
         if (rows == 1) mul(std::integral_constant<int, 1>{});
-        else if (rows == 2) mul(std::integral_constant<int, 2>{});
-        else if (rows <= 4) mul(std::integral_constant<int, 4>{});
+        else if (rows <= 3) mul(std::integral_constant<int, 3>{});
         else mul(std::integral_constant<int, 8>{});
         if (++ck == nkb) {
           walk.leave(cu, rows, acc);
