@@ -299,19 +299,20 @@ def time_stages(cfg, inp, desc, w, steps, torch, L, synth):
     return stages, kernels, counts.cpu()
 
 
-def traffic_for(kernel_file, profile):
+def traffic_for(kernel_files, profile):
     """HBM bytes per launch from the committed counter summary, or None when
-    the kernel source changed since the counters were taken."""
+    the kernel's sources changed since the counters were taken."""
     import hashlib
     path = os.path.join(ROOT, "profiles", profile)
     if not os.path.exists(path):
         return None
     with open(path) as f:
         rec = json.load(f)
-    src = os.path.join(ROOT, "sparse_mixture_experts_04_amd", "csrc", kernel_file)
-    with open(src, "rb") as f:
-        digest = hashlib.sha256(f.read()).hexdigest()
-    if rec.get("source_sha256") != digest:
+    digest = hashlib.sha256()
+    for name in kernel_files:
+        with open(os.path.join(ROOT, "sparse_mixture_experts_04_amd", "csrc", name), "rb") as f:
+            digest.update(f.read())
+    if rec.get("source_sha256") != digest.hexdigest():
         return None
     return rec.get("bytes_per_launch")
 
@@ -914,7 +915,8 @@ def main():
                      "frac": round(gu_tflops / PEAK_BF16_TFLOPS, 4),
                      "flop_per_launch": f_gu, "rows": rows,
                      "ms_per_launch": round(kernels["gate_up_gemm"], 4),
-                     "traffic": traffic_for("ffn_big.hip", "ffn_big_gate_up_D_traffic.json")},
+                     "traffic": traffic_for(("ffn_big.hip", "big_tile.h"),
+                                           "ffn_big_gate_up_D_traffic.json")},
     }
     max_load = counts.max().item()
     result["max_over_mean_load"] = round(max_load / (cfg.T * cfg.k / cfg.E), 3)

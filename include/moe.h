@@ -392,12 +392,14 @@ moe_status moe_quantize_int8(int64_t rows, int32_t K, moe_dtype dtype, const voi
 /* Grouped product: y[m, n] = a_scale[m] w_scale[e, n] sum_k a[m, k] w[e, n, k]
  * for the rows m of group e, offsets[e] <= m < offsets[e+1]; the sum is exact
  * (int32), scaled in fp32 and rounded once to `out` (MOE_F32 or MOE_BF16).
+ * The two scales are multiplied first: where a_scale[m] w_scale[e, n] is beyond
+ * fp32's normal range (2^-126 to 2^128), y is inexact, infinite or NaN.
  *   a [M, Kp], a_scale [M], w [E, N, Kp], w_scale [E, N], y [M, N];
  *   offsets int32 [E+1], non-decreasing; NULL with E = 1: group 0 has all M rows.
  * Rows outside every group keep what y held.  An offset outside [0, M] counts as
  * the nearest end of it, one smaller than an offset before it as that one.
- * M, N >= 0, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and M * max(N, Kp)
- * < 2^40, a and w 16-byte aligned. */
+ * N >= 0, 0 <= M <= 2^31 - 1024, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and
+ * M * max(N, Kp) < 2^40, a, w and y 16-byte aligned. */
 typedef struct {
   int32_t M, N, K, E;
   moe_dtype out;

@@ -13,6 +13,8 @@ inline long long code_row(long long K) { return (K + kCodeRow - 1) / kCodeRow * 
 // 127^2 * 131072 < 2^31.
 constexpr int kInt8MaxK = 131072;
 constexpr int kInt8MaxGroups = 256;
+// Rows of a product, at most: row numbers rounded up to a tile stay in 32 bits.
+constexpr long long kInt8MaxRows = (1LL << 31) - 1024;
 
 // Rows of fp32 or bf16 values to codes [rows, code_row(K)] and scales [rows].
 hipError_t launch_quantize_int8(long long rows, int K, bool bf16, const void* x, int8_t* codes,

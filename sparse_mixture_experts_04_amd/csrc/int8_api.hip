@@ -18,7 +18,8 @@ moe_status check_gemm(const moe_gemm_int8_desc* d) {
   if (!d) return MOE_ERR_NULL;
   if (d->M < 0 || d->N < 0 || d->K <= 0 || d->E <= 0) return MOE_ERR_SHAPE;
   if (d->out != MOE_F32 && d->out != MOE_BF16) return MOE_ERR_DTYPE;
-  if (d->K > kInt8MaxK || d->E > kInt8MaxGroups) return MOE_ERR_UNSUPPORTED;
+  if (d->K > kInt8MaxK || d->E > kInt8MaxGroups || d->M > kInt8MaxRows)
+    return MOE_ERR_UNSUPPORTED;
   const long long lim = 1LL << 40, kp = code_row(d->K);
   const long long wide = d->N > kp ? d->N : kp;
   if (static_cast<long long>(d->E) * d->N >= lim / kp || d->M >= lim / wide)
@@ -33,7 +34,7 @@ moe_status check_int8_desc(const moe_desc* d) {
   if (d->weight == MOE_MXFP4) return MOE_ERR_DTYPE;
   if (d->d > kInt8MaxK || d->F > kInt8MaxK) return MOE_ERR_UNSUPPORTED;
   // int32 row numbers: the shared experts' rows follow the T * k routed ones
-  if (static_cast<long long>(d->T) * (d->k + d->S) >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(d->T) * (d->k + d->S) > kInt8MaxRows) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

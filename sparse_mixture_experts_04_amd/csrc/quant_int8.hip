@@ -133,9 +133,19 @@ static hipError_t run_quantize(long long rows, int K, const T* x, int8_t* codes,
 
 hipError_t launch_quantize_int8(long long rows, int K, bool bf16, const void* x, int8_t* codes,
                                 float* scales, hipStream_t st) {
-  if (rows == 0) return hipSuccess;
-  return bf16 ? run_quantize(rows, K, static_cast<const bf16_t*>(x), codes, scales, st)
-              : run_quantize(rows, K, static_cast<const float*>(x), codes, scales, st);
+  // a launch takes fewer than 2^32 threads, and a row up to 256 of them
+  constexpr long long kRowsPerLaunch = 1LL << 23;
+  const long long Kp = code_row(K);
+  for (long long r = 0; r < rows; r += kRowsPerLaunch) {
+    const long long n = rows - r < kRowsPerLaunch ? rows - r : kRowsPerLaunch;
+    const hipError_t e =
+        bf16 ? run_quantize(n, K, static_cast<const bf16_t*>(x) + r * K, codes + r * Kp,
+                            scales + r, st)
+             : run_quantize(n, K, static_cast<const float*>(x) + r * K, codes + r * Kp,
+                            scales + r, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

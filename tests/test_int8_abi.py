@@ -51,7 +51,8 @@ def test_quantize_checks():
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), 2), (dict(N=-1), 2), (dict(K=0), 2), (dict(E=0), 2), (dict(out=2), 3),
     (dict(K=131073), 5), (dict(E=257), 5), (dict(E=256, N=1 << 24, K=1 << 14), 5),
-    (dict(M=1 << 30, K=1 << 11), 5), (dict(), 0), (dict(M=0), 0), (dict(K=131072), 0),
+    (dict(M=1 << 30, K=1 << 11), 5), (dict(M=(1 << 31) - 1023), 5),
+    (dict(M=(1 << 31) - 1024), 0), (dict(), 0), (dict(M=0), 0), (dict(K=131072), 0),
 ])
 def test_gemm_desc(kw, code):
     d = L.GemmInt8Desc(**{**dict(M=4, N=8, K=100, E=1, out=L.BF16), **kw})

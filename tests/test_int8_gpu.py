@@ -83,6 +83,15 @@ def test_quantize_zero_and_nonfinite_rows():
     assert not y[1].any()
 
 
+def test_quantize_more_rows_than_a_launch():
+    rows, K = (1 << 23) + 1037, 3
+    x = randn((rows, K), 8, BF16)
+    codes, scales = L.quantize_int8(x)
+    for r in (slice(0, 4096), slice((1 << 23) - 4096, rows)):
+        assert torch.equal(codes[r], R.padded(R.codes64(x[r])[0]))
+    assert torch.equal(scales, x.float().abs().amax(1) / torch.full((), 127.0, device=DEV))
+
+
 def test_quantize_views_and_stacks():
     big = randn((9, 301), 5, BF16).view(-1)
     x = big[1:1 + 8 * 301].view(8, 301)          # an address that 16 does not divide
@@ -122,7 +131,9 @@ def check_product(a, sa, w, t, y, offsets=None, untouched=None):
     (600, 1000, 513), (1500, 770, 256), (2, 7168, 2048),
     # 128-row and 256-row tiles, whole and ragged columns
     (4096, 513, 7168), (4096, 520, 7168), (9000, 1030, 2048), (9001, 1027, 2048),
-    (20000, 768, 2048)])
+    (20000, 768, 2048),
+    # one and a few K steps of the large tiles
+    (60000, 520, 128), (60000, 2050, 128), (40000, 520, 300)])
 def test_product_sizes(M, N, K, out):
     print(f"gemm_int8 M={M} N={N} K={K} {out}", flush=True)
     kp = L.code_row(K)
