@@ -21,34 +21,11 @@ using BigI8 = BigShape<256, 32, 3, 6, MmaI8>;
 using MidI8 = BigShape<128, 64, 3, 3, MmaI8>;
 static_assert(BigI8::LDS_ELEMS * 2 <= 147456 && MidI8::LDS_ELEMS * 2 <= 147456, "LDS");
 
-// Plan in the workspace: row tiles as an exclusive prefix over the groups
-// [kPlanGroups + 1], first rows and row counts [kPlanGroups each], then the work
-// counters of up to two products over the same rows.
-constexpr int kPlanLo = kPlanGroups + 1, kPlanRows = kPlanLo + kPlanGroups,
-              kPlanCtr = kPlanRows + kPlanGroups, kPlanInts = kPlanCtr + 2 * kXcds;
+// Work counters in the workspace: a set of kXcds for each of up to two products.
+constexpr int kCounters = 2 * kXcds;
 
-__global__ __launch_bounds__(512) void int8_plan_kernel(Int8Args p, int mt,
-                                                        int32_t* __restrict__ plan) {
-  __shared__ int sc[512];
-  const int g = threadIdx.x, G = p.E + p.S;
-  int lo = 0, n = 0;
-  group_rows<512>(p, lo, n);
-  const int nt = (n + mt - 1) / mt;
-  sc[g] = nt;
-  __syncthreads();
-  for (int off = 1; off < 512; off <<= 1) {
-    const int v = g >= off ? sc[g - off] : 0;
-    __syncthreads();
-    sc[g] += v;
-    __syncthreads();
-  }
-  if (g < G) {
-    plan[g] = sc[g] - nt;
-    plan[kPlanLo + g] = lo;
-    plan[kPlanRows + g] = n;
-  }
-  if (g == G - 1) plan[G] = sc[g];
-  if (g < 2 * kXcds) plan[kPlanCtr + g] = 0;
+__global__ void int8_counters_kernel(int32_t* counters) {
+  if (threadIdx.x < kCounters) counters[threadIdx.x] = 0;
 }
 
 // 4 consecutive values of a scale row of n values, from column c on (0 past its
@@ -60,10 +37,9 @@ __device__ __forceinline__ void scale4(const float* t, int c, int n, float (&v)[
 
 template <class C, bool GATED, bool OUT_BF16>
 __global__ __launch_bounds__(512, 1) void gemm_int8_big_kernel(Int8Args p,
-                                                               const int32_t* __restrict__ plan,
                                                                int32_t* counters) {
   __shared__ __attribute__((aligned(1024))) bf16_t lds[C::LDS_ELEMS];
-  __shared__ int ts[kPlanGroups + 1], glo[kPlanGroups], grows[kPlanGroups];
+  __shared__ EntryPlan plan;
   __shared__ long long s_item;
   bf16_t* sA[C::NSA];
   bf16_t* sB[C::NSB];
@@ -81,16 +57,9 @@ __global__ __launch_bounds__(512, 1) void gemm_int8_big_kernel(Int8Args p,
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int G = p.E + p.S;
-  for (int g = tid; g <= G; g += C::THREADS) {
-    ts[g] = plan[g];
-    if (g < G) {
-      glo[g] = plan[kPlanLo + g];
-      grows[g] = plan[kPlanRows + g];
-    }
-  }
-  __syncthreads();
+  make_entries<C::THREADS, C::MT>(p, plan);
   const int n_tiles = (p.N + NOUT - 1) / NOUT;
-  const long long total = static_cast<long long>(ts[G]) * n_tiles;
+  const long long total = static_cast<long long>(plan.start[G]) * n_tiles;
   const int xcd = blockIdx.x % kXcds;
   const int kld = p.Kp / 2;  // row length in 16-bit units
   const int nk = kld / C::BK;
@@ -98,21 +67,23 @@ __global__ __launch_bounds__(512, 1) void gemm_int8_big_kernel(Int8Args p,
   const int lrow = lane / C::CPR;
   const bf16_t* A = reinterpret_cast<const bf16_t*>(p.a);
 
-  for (;;) {
-    if (tid == 0) s_item = claim_item(counters, xcd, total);
-    __syncthreads();
-    const long long gitem = s_item;
-    if (gitem < 0) break;
-    int g = 0;
-    for (int hi = G; hi - g > 1;) {
-      const int mid = (g + hi) >> 1;
-      if (static_cast<long long>(ts[mid]) * n_tiles <= gitem) g = mid;
-      else hi = mid;
+  const long long chunk = (total + kXcds - 1) / kXcds;
+  for (long long mine = blockIdx.x / kXcds;; mine += gridDim.x / kXcds) {
+    long long gitem = xcd * chunk + mine;
+    if (counters) {
+      if (tid == 0) s_item = claim_item(counters, xcd, total);
+      __syncthreads();
+      gitem = s_item;
+      if (gitem < 0) break;
+    } else {
+      if (mine >= chunk || gitem >= total) break;
+      __syncthreads();  // the item before is done with the LDS
     }
-    const Item item = place_item(gitem, ts, g, n_tiles, C::MT, grows[g], true);
+    const int g = entry_group(plan, G, static_cast<int>(gitem / n_tiles));
+    const Item item = place_item(gitem, plan.start, g, n_tiles, C::MT, plan.rows[g], true);
     const bool routed = g < p.E;
     const int ge = routed ? g : g - p.E;
-    const int row0 = routed ? glo[g] : 0;
+    const int row0 = routed ? plan.lo[g] : 0;
     // row of a and of its scale for tile row r
     auto source = [&](int r) -> long long {
       return source_row<GATED>(p, routed, ge, row0,
@@ -240,18 +211,17 @@ __global__ __launch_bounds__(512, 1) void gemm_int8_big_kernel(Int8Args p,
 }
 
 template <class C>
-static hipError_t run_big(const Int8Args& a, bool gated, const int32_t* plan, int32_t* ctr,
-                          hipStream_t st) {
+static hipError_t run_big(const Int8Args& a, bool gated, int32_t* ctr, hipStream_t st) {
   const int grid = (device_cus_big() + kXcds - 1) / kXcds * kXcds;
-  if (gated) gemm_int8_big_kernel<C, true, false><<<grid, C::THREADS, 0, st>>>(a, plan, ctr);
-  else if (a.out_bf16) gemm_int8_big_kernel<C, false, true><<<grid, C::THREADS, 0, st>>>(a, plan, ctr);
-  else gemm_int8_big_kernel<C, false, false><<<grid, C::THREADS, 0, st>>>(a, plan, ctr);
+  if (gated) gemm_int8_big_kernel<C, true, false><<<grid, C::THREADS, 0, st>>>(a, ctr);
+  else if (a.out_bf16) gemm_int8_big_kernel<C, false, true><<<grid, C::THREADS, 0, st>>>(a, ctr);
+  else gemm_int8_big_kernel<C, false, false><<<grid, C::THREADS, 0, st>>>(a, ctr);
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ host
 
-size_t gemm_int8_plan_ints() { return kPlanInts; }
+size_t gemm_int8_counter_ints() { return kCounters; }
 
 // Kernel of a product, by estimates of their times (us) fitted to measured ones.
 // They agree to the bit, so the choice is one of speed alone.  M is the rows, mu
@@ -288,22 +258,39 @@ static Path path(const Int8Args& a, bool gated) {
   return mid <= big ? Path::kMid : Path::kBig;
 }
 
-hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, int& planned,
+// Whether the workgroups of the large tiles take their items from counters: it
+// evens out groups that end in a part of a tile, and costs a launch that clears
+// the counters (5 us) and 5 to 10 us of atomics at both ends of the kernel.  From
+// about 16 items a workgroup on, where there are groups.  Measured (us; counters
+// with their launch / fixed shares):
+//   items a workgroup   1 (3655x3920x1393)       58 / 36
+//                       2 (16384x2048x7168)     263 / 235
+//                       3 (24576x768x2048, 256 groups)   134 / 120
+//                       7 (prefill experts' gate/up, K 2048)   255 / 256
+//                       40 (large experts' gate/up, K 7168)    4128 / 4353
+static bool by_counters(const Int8Args& a, bool gated, int mt) {
+  if (a.E == 1 && a.S == 0) return false;
+  const long long rows = a.M + static_cast<long long>(a.S) * a.T;
+  const long long cols = (a.N + (gated ? 127 : 255)) / (gated ? 128 : 256);
+  return rows / mt * cols >= 16LL * device_cus_big();
+}
+
+hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* counters, bool& cleared,
                             hipStream_t st) {
   if (a.M == 0 && (a.S == 0 || a.T == 0)) return hipSuccess;
   const Path way = path(a, gated);
   if (way == Path::kTiles) return launch_gemm_int8_tiles(a, gated, st);
-  const int mt = way == Path::kMid ? 128 : 256;
-  const bool second = planned == mt;  // the call before this left a plan for these tiles
-  if (!second) {
-    int8_plan_kernel<<<1, 512, 0, st>>>(a, mt, plan);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    planned = mt;
+  int32_t* ctr = nullptr;
+  if (by_counters(a, gated, way == Path::kMid ? MidI8::MT : BigI8::MT)) {
+    ctr = counters + (cleared ? kXcds : 0);
+    if (!cleared) {
+      int8_counters_kernel<<<1, 64, 0, st>>>(counters);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      cleared = true;
+    }
   }
-  int32_t* ctr = plan + kPlanCtr + (second ? kXcds : 0);
-  return mt == 128 ? run_big<MidI8>(a, gated, plan, ctr, st)
-                   : run_big<BigI8>(a, gated, plan, ctr, st);
+  return way == Path::kMid ? run_big<MidI8>(a, gated, ctr, st) : run_big<BigI8>(a, gated, ctr, st);
 }
 
 }  // namespace moe

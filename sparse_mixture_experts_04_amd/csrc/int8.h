@@ -45,12 +45,10 @@ struct Int8Args {
   int M, N, Kp, E, S, T, k;
   bool out_bf16;          // plain: bf16 or fp32 output (GATED: fp32)
 };
-// planned: row tile of the plan that a call before this one, over the same
-// rows, left in `plan` (0: none); set to this one's.  Two calls at most share
-// a plan, which holds two sets of work counters.
-hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* plan, int& planned,
+// counters: gemm_int8_counter_ints() of workspace, for up to two products in turn.
+// cleared: whether a call before this one has cleared them; set when this one has.
+hipError_t launch_gemm_int8(const Int8Args& a, bool gated, int32_t* counters, bool& cleared,
                             hipStream_t st);
-// int32 words of plan (workspace) that launch_gemm_int8 needs.
-size_t gemm_int8_plan_ints();
+size_t gemm_int8_counter_ints();
 
 }  // namespace moe

@@ -78,7 +78,7 @@ struct FfnInt8Ws {
   float* h;
   int8_t* hq;
   float* hs;
-  int32_t* plan;
+  int32_t* counters;
 };
 FfnInt8Ws carve_ffn_int8(Carver& c, const Shape& s) {
   FfnInt8Ws w;
@@ -88,7 +88,7 @@ FfnInt8Ws carve_ffn_int8(Carver& c, const Shape& s) {
   w.h = c.take<float>(rows * s.F);
   w.hq = c.take<int8_t>(rows * s.F);
   w.hs = c.take<float>(rows);
-  w.plan = c.take<int32_t>(gemm_int8_plan_ints());
+  w.counters = c.take<int32_t>(gemm_int8_counter_ints());
   return w;
 }
 
@@ -154,7 +154,7 @@ moe_status moe_gemm_int8_workspace_size(const moe_gemm_int8_desc* desc, size_t* 
   if (!bytes) return MOE_ERR_NULL;
   const moe_status st = check_gemm(desc);
   if (st != MOE_OK) return st;
-  *bytes = gemm_int8_plan_ints() * sizeof(int32_t);
+  *bytes = gemm_int8_counter_ints() * sizeof(int32_t);
   return MOE_OK;
 }
 
@@ -166,7 +166,7 @@ moe_status moe_gemm_int8(const moe_gemm_int8_desc* desc, const int8_t* a, const 
   if (desc->M == 0 || desc->N == 0) return MOE_OK;
   if (!a || !a_scale || !w || !w_scale || !y || (!offsets && desc->E != 1)) return MOE_ERR_NULL;
   if (!aligned16(a) || !aligned16(w) || !aligned16(y)) return MOE_ERR_UNSUPPORTED;
-  if (!ws || ws_bytes < gemm_int8_plan_ints() * sizeof(int32_t)) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < gemm_int8_counter_ints() * sizeof(int32_t)) return MOE_ERR_WORKSPACE;
   Int8Args g{};
   g.a = a;
   g.a_scale = a_scale;
@@ -180,8 +180,8 @@ moe_status moe_gemm_int8(const moe_gemm_int8_desc* desc, const int8_t* a, const 
   g.E = desc->E;
   g.k = 1;
   g.out_bf16 = desc->out == MOE_BF16;
-  int planned = 0;
-  return hip_status(launch_gemm_int8(g, false, static_cast<int32_t*>(ws), planned, stream));
+  bool cleared = false;
+  return hip_status(launch_gemm_int8(g, false, static_cast<int32_t*>(ws), cleared, stream));
 }
 
 moe_status moe_expert_ffn_int8_workspace_size(const moe_desc* desc, size_t* bytes) {
@@ -234,8 +234,8 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
   g.S = s.S;
   g.T = s.T;
   g.k = s.k;
-  int planned = 0;
-  if (e == hipSuccess) e = launch_gemm_int8(g, true, f.plan, planned, stream);
+  bool cleared = false;
+  if (e == hipSuccess) e = launch_gemm_int8(g, true, f.counters, cleared, stream);
   if (e == hipSuccess) e = launch_quantize_int8(rows, s.F, false, f.h, f.hq, f.hs, stream);
   g.a = f.hq;
   g.a_scale = f.hs;
@@ -248,7 +248,7 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
   g.N = s.d;
   g.Kp = s.F;
   g.out_bf16 = s.bf16;
-  if (e == hipSuccess) e = launch_gemm_int8(g, false, f.plan, planned, stream);
+  if (e == hipSuccess) e = launch_gemm_int8(g, false, f.counters, cleared, stream);
   return hip_status(e);
 }
 

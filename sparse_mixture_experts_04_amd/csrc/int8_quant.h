@@ -45,25 +45,36 @@ __device__ __forceinline__ uint32_t max_bits(const float (&v)[8], uint32_t m) {
 }
 constexpr uint32_t kNotFinite = 0x7f800000u;
 
-// 8 values from p; `n` of them exist (VEC: all, and p is 16-byte aligned).
+// 8 values from p as they lie in memory, `n` of them in the row (VEC: all, and p is
+// 16-byte aligned; otherwise aligned to a value, which a wide load takes too).
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void hold8(const T* p, int n, uint4 (&h)[sizeof(T) / 2]) {
+  if (VEC) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else if constexpr (VEC) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) h[i] = reinterpret_cast<const uint4*>(p)[i];
+  } else if (n >= 8) {
+    __builtin_memcpy(h, p, sizeof(h));
   } else {
+    T v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? ActTraits<T>::load(p + i) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : T{0};
+    __builtin_memcpy(h, v, sizeof(h));
+  }
+}
+__device__ __forceinline__ void values(const uint4 (&h)[1], float (&v)[8]) {
+  const uint32_t w[4] = {h[0].x, h[0].y, h[0].z, h[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void values(const uint4 (&h)[2], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(w[j]);
   }
 }
 
@@ -118,7 +129,12 @@ __device__ __forceinline__ float quantize_row(int K, int Kp, Load load, Store st
 template <typename T, bool VEC, int NT>
 __device__ __forceinline__ float quantize_row(const T* xr, int K, int Kp, int8_t* cr) {
   return quantize_row<NT>(
-      K, Kp, [&](int c, int n, float (&v)[8]) { load8<T, VEC>(xr + c * 8, n, v); },
+      K, Kp,
+      [&](int c, int n, float (&v)[8]) {
+        uint4 h[sizeof(T) / 2];
+        hold8<T, VEC>(xr + c * 8, n, h);
+        values(h, v);
+      },
       [&](int c, uint2 w) { *reinterpret_cast<uint2*>(cr + c * 8) = w; });
 }
 

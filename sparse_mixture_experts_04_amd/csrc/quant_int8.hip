@@ -9,36 +9,9 @@
 // than the distance of any quotient of two fp32 values to a border it is not
 // on.  A row of zeros gets scale 0; a row holding a NaN or an infinity gets
 // codes 0 and scale NaN, so that only its own products become NaN.
-#include <type_traits>
-
 #include "int8_quant.h"
 
 namespace moe {
-
-// 8 values of a row in registers.
-struct Eight {
-  float v[8];
-};
-template <typename T, bool VEC>
-__device__ __forceinline__ void hold(const T* p, int n, Eight& h) {
-  load8<T, VEC>(p, n, h.v);
-}
-template <typename T, bool VEC>
-__device__ __forceinline__ void hold(const T* p, int, uint4& h) {
-  h = *reinterpret_cast<const uint4*>(p);
-}
-__device__ __forceinline__ void values(const Eight& h, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = h.v[i];
-}
-__device__ __forceinline__ void values(const uint4& h, float (&v)[8]) {
-  const uint32_t w[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 
 // A row of up to 512 NC values by a wave, four rows a workgroup: every chunk of 8
 // values a lane has is loaded before the first is used and stays in registers,
@@ -53,14 +26,13 @@ __global__ __launch_bounds__(256) void quantize_int8_wave_kernel(const T* __rest
   if (row >= rows) return;  // whole waves leave
   const T* xr = x + row * K;
   const int chunks = (K + 7) / 8;
-  // bf16 values stay as they were read, two to a register
-  using Held = typename std::conditional<VEC && sizeof(T) == 2, uint4, Eight>::type;
-  Held held[NC];
+  uint4 held[NC][sizeof(T) / 2];  // as they were read
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = lane + 64 * j;
-    held[j] = Held{};
-    if (c < chunks) hold<T, VEC>(xr + c * 8, K - c * 8, held[j]);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) held[j][i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < chunks) hold8<T, VEC>(xr + c * 8, K - c * 8, held[j]);
   }
   uint32_t top = 0;
 #pragma unroll
