@@ -227,17 +227,18 @@ size_t gemm_int8_counter_ints() { return kCounters; }
 // They agree to the bit, so the choice is one of speed alone.  M is the rows, mu
 // the mean rows of a group, G the groups expected to have any:
 //   tiles  7 + the weights read once per 16 rows of a group, at 9 TB/s while
-//          they stay in the caches and 5.3 from memory
-//   128    22 + the slower of a tile's time (5.8 per 1000 of K; 0.042 per tile
-//          when they fill the device) and the weights read once at 5.3 TB/s
-//   256    27 + the same with 9.2 and 0.065
+//          they stay in the caches and 5.3 from memory, + 3 for each turn of the
+//          256 workgroups to stage 16 rows
+//   128    11 + the slower of the weights read once at 5.3 TB/s and the rounds of
+//          256 tiles: a full one 7.6 per 1000 of K, one of few tiles 5, and 5 more
+//          for each round after the first
+//   256    13.7 + the same with 14.2 and 8.4
 // Measured (us; N x K, groups):
-//   rows                1     64    256   1024   4096   16 a group  96 a group
-//   tiles  2048x7168   15     17     34    110    404      310        1474
-//   128                56     57     68     64     88      227         270
-//   256                76     77     95     94     93      266         315
-//   (the last two columns 2048x2048, 256 groups); 256-row tiles lead from
-//   16384 rows of 2048x7168 on.
+//   rows              1     64    256   1024   4096   12000   16384   4 a group  96 a group
+//   tiles 2048x7168  15     16     34    110    402    1183    1587      194        1474
+//   128              35     35     46     48     67     177     241      205         261
+//   256              55     55     73     75     82     188     218      241         300
+//   (the last two columns 2048x2048, 256 groups)
 enum class Path { kTiles, kMid, kBig };
 static Path path(const Int8Args& a, bool gated) {
   const double n = gated ? 2.0 * a.N : a.N, k = a.Kp, mu = static_cast<double>(a.M) / a.E;
@@ -248,12 +249,15 @@ static Path path(const Int8Args& a, bool gated) {
     const double r = a.E == 1 ? std::ceil(a.M / mt) : full * std::fmax(1.0, mu / mt + 0.5);
     return r + a.S * std::ceil(a.T / mt);
   };
-  const double tiles = 7.0 + row_tiles(16) * n * k * 1e-6 / (weights < 200.0 ? 9.0 : 5.3);
+  const double r16 = row_tiles(16);
+  const double tiles = 7.0 + r16 * n * k * 1e-6 / (weights < 200.0 ? 9.0 : 5.3) + r16 * 3.0 / 256.0;
   const double cols = std::ceil(n / 256.0), stream = weights / 5.3;
-  auto large = [&](double mt, double fixed, double one, double each) {
-    return fixed + std::fmax(stream, k * 1e-3 * std::fmax(one, each * row_tiles(mt) * cols));
+  auto large = [&](double mt, double fixed, double few, double all) {
+    const double t = row_tiles(mt) * cols / 256.0, before = std::ceil(t) - 1.0;
+    return fixed + std::fmax(stream, 5.0 * before + k * 1e-3 * (before * all + few +
+                                                                (all - few) * (t - before)));
   };
-  const double mid = large(128, 22.0, 5.8, 0.042), big = large(256, 27.0, 9.2, 0.065);
+  const double mid = large(128, 11.0, 5.0, 7.6), big = large(256, 13.7, 8.4, 14.2);
   if (tiles <= mid && tiles <= big) return Path::kTiles;
   return mid <= big ? Path::kMid : Path::kBig;
 }
