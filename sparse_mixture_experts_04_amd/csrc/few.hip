@@ -36,12 +36,14 @@
 // is quantised per token and h per row.
 //
 // Bound by the weight rows' loads (rowstream.h): T=16, d=7168, F=2048, bf16
-// reads 7.3 GB in 1.22 ms, 6.0 TB/s.  T=1 there takes 147 us of which the 704 MB
-// need 117 at that rate; the rest, and most of the 40 us of T=1 at d=2048, F=768
-// (75 MB), are fixed costs of about 4 us to the first load, 3 for the plan once
-// the picks are known, 5 for the wait before the down stage, 3 for the latency of
-// each stage's first loads, and the fetch of code that the weights have driven
-// out of the caches (some 0.4 us per 128 bytes: hence loops where they can be).
+// reads 7.3 GB in 1.19 ms, 6.1 TB/s; T=1 there 704 MB in 116 us, as fast; T=4 with
+// 8-bit weights 1.1 GB in 178 us.  At T=1, d=2048, F=768 the 75 MB need 12 us and
+// the kernel takes 27: the selection (9 us, of which the shared experts' share
+// hides half), the plan once the picks are known, the wait before the down stage
+// and the latency of each stage's first loads, and the fetch of code that the
+// weights have driven out of the caches (some 0.4 us per 128 bytes: hence loops
+// where they can be).  few_route_kernel adds 4 to 5 us, 13.6 at T=16, d=7168, where
+// each of its workgroups reads all of x.
 #include <type_traits>
 
 #include "few.h"

@@ -15,8 +15,15 @@ namespace moe {
 // The bf16 experts' tile and K loop (big_tile.h) on 8-bit operands: the same
 // bytes per step hold twice the K, and the int8 matrix instruction does twice
 // the products in the same cycles.  Row tiles of up to 256 rows (or 128 where
-// groups hold few) x 256 weight rows; persistent workgroups take items from
-// per-XCD counters.
+// groups hold few) x 256 weight rows; each XCD's workgroups share a contiguous
+// run of the items, evenly or by a counter (by_counters).
+//
+// Bound by the matrix instructions: 16384x2048x7168 takes 235 us, 2.05 POP/s (the
+// 8192^3 product of the vendor's library 2.09 here); the experts of a large
+// batch (d=7168, F=2048, 131072 rows in ragged groups) run at 1.89 POP/s gate/up
+// and 1.60 down, where K is short and the epilogue (scales, bf16, the staged
+// tile) a seventh of a tile's time.  With few rows a group it streams the
+// weights: T=64 there reads 4.05 GB in 489 + 290 us, 5.2 TB/s.
 using BigI8 = BigShape<256, 32, 3, 6, MmaI8>;
 using MidI8 = BigShape<128, 64, 3, 3, MmaI8>;
 static_assert(BigI8::LDS_ELEMS * 2 <= 147456 && MidI8::LDS_ELEMS * 2 <= 147456, "LDS");
