@@ -124,6 +124,24 @@ __global__ __launch_bounds__(512) void few_route_kernel(FewArgs p, int ctrl_ints
 
 // --------------------------------------------------------------- the experts
 
+// exp(x) for x <= 0, to a few 2^-53: x = n ln 2 + r with |r| <= ln 2 / 2, and the
+// Taylor series of exp(r) to r^13 / 13! (the next term is below 2^-56) in a loop
+// whose factors come from memory.  The library's exp is straight-line code with
+// its constants in registers: two of those spilled, and scratch memory costs the
+// whole kernel (8-bit, T=4, d=7168: 184 us with it, 177 without).
+__device__ const double kOneOver[14] = {0.0, 1.0, 1.0 / 2, 1.0 / 3, 1.0 / 4, 1.0 / 5, 1.0 / 6,
+                                        1.0 / 7, 1.0 / 8, 1.0 / 9, 1.0 / 10, 1.0 / 11, 1.0 / 12,
+                                        1.0 / 13};
+__device__ __forceinline__ double few_exp(double x) {
+  const double n = rint(x * 1.4426950408889634);
+  // ln 2 = 45426 / 65536 + the rest; n times the first part is exact
+  const double r = fma(n, -1.4286068203094173e-06, fma(n, -45426.0 / 65536.0, x));
+  double e = 1.0;
+#pragma unroll 1
+  for (int k = 13; k > 0; --k) e = fma(e, r * kOneOver[k], 1.0);
+  return ldexp(e, static_cast<int>(fmax(n, -2000.0)));
+}
+
 // Top-6 and gates of token t by one wave, in little code: a workgroup that runs
 // this waits for every line of it to come from memory (the weights have
 // streamed it out of the caches since the last call), so the rounds are a loop
@@ -169,7 +187,7 @@ __device__ __forceinline__ void few_select(const FewArgs& p, int t, int lane) {
     double m = mine ? v.x : -INFINITY;
     int who = lane;
     wave_argmax(m, who, lane);
-    e = mine ? exp(v.x - m) : 0.0;
+    e = mine ? few_exp(v.x - m) : 0.0;
   }
   const double g = e / (wave_sum(e, lane) / p.gate_scale);
   if (!mine) return;
@@ -419,12 +437,11 @@ struct GateWalk {
     return rows;
   }
   __device__ __forceinline__ void leave(int, int nr, const Acc (&acc)[kUnitRows]) {
-    Acc* out = part[col][up];
-#pragma unroll
-    for (int r = 0; r < kUnitRows; ++r) {
-      if (r >= nr) break;
-      const Acc s = wave_total(acc[r]);
-      if (lane == 0) out[r] = more ? out[r] + s : s;
+    const Acc s = row_totals(nr, acc, lane);
+    const int r = total_row(lane);
+    if ((lane & 7) == 0 && r < nr) {
+      Acc* out = part[col][up] + r;
+      *out = more ? *out + s : s;
     }
   }
 };
@@ -442,8 +459,8 @@ struct DownWalk {
   size_t kfull;
   int d, n0, e0, ne, n, stride, lane, se, base;
   int lcol, lent, col, ent;
-  float scale = 0.0f;      // of the unit's channel times this lane's row of h
-  int hrow = 0;            // this lane's row of h
+  float channel = 0.0f;    // 8-bit scale of the unit's channel
+  int mine = 0;            // list row whose sum this lane gets (total_row)
 
   __device__ __forceinline__ DownWalk(const FewPlan& pl, float* ys, int rh, const FewArgs& p,
                                       size_t kf, size_t koff, int n0_, int e0_, int ne_, int cols,
@@ -474,27 +491,21 @@ struct DownWalk {
 #pragma unroll
     for (int r = 0; r < kUnitRows; ++r)
       off[r] = (r0 - base + (r < rows ? r : 0)) * stride + lane * 16;
-    const int mine = r0 + (lane < rows ? lane : 0);
-    hrow = plan.hrow[mine];
+    const int tr = total_row(lane);
+    mine = r0 + (tr < rows ? tr : 0);
     if (I8) {
       const int32_t* tp = reinterpret_cast<const int32_t*>(i < se ? ts : t) +
                           static_cast<size_t>(uniform(plan.expert[i])) * d;
-      scale = plan.scale[mine] * __int_as_float(((const_words)tp)[n0 + col]);
+      channel = __int_as_float(((const_words)tp)[n0 + col]);
     }
     return rows;
   }
   __device__ __forceinline__ void leave(int, int nr, const Acc (&acc)[kUnitRows]) {
-    Acc mine{0};
-#pragma unroll
-    for (int r = 0; r < kUnitRows; ++r) {
-      if (r >= nr) break;
-      const Acc s = wave_total(acc[r]);
-      mine = lane == r ? s : mine;
-    }
-    if (lane < nr) {
-      float v = static_cast<float>(mine);
-      if (I8) v *= scale;
-      float* y = yrow + col * rows_h + hrow;
+    const Acc s = row_totals(nr, acc, lane);
+    if ((lane & 7) == 0 && total_row(lane) < nr) {
+      float v = static_cast<float>(s);
+      if (I8) v *= plan.scale[mine] * channel;
+      float* y = yrow + col * rows_h + plan.hrow[mine];
       *y = more ? *y + v : v;
     }
   }
@@ -563,7 +574,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs) {
     fall = static_cast<int>((ffull + kChunk - 1) / kChunk);
     ybytes = (cols * rows * 4 + kChunk - 1) / kChunk * kChunk;
     // every entry fits a pass: 8 rows of fpass chunks
-    fpass = min((fall + 1) / 2 * 2, (kPool - ybytes) / kChunk / PL / kUnitRows / 2 * 2);
+    fpass = min(fall, (kPool - ybytes) / kChunk / PL / kUnitRows);
     stride = fpass * kChunk * PL;  // of a row of h in oper
     capacity = (kPool - ybytes) / stride;
   };
@@ -585,7 +596,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_ffn_kernel(FewArgs) {
   const int kall = static_cast<int>((kfull + kChunk - 1) / kChunk);
   auto part_sums = reinterpret_cast<Acc(*)[2][kUnitRows]>(pool);
   char* oper = pool + kPartBytes;
-  const int kpass = min((kall + 1) / 2 * 2, (kPool - kPartBytes) / kChunk / T / 2 * 2);
+  const int kpass = min(kall, (kPool - kPartBytes) / kChunk / T);
   int staged = -1;  // first K chunk of the pass that oper holds
   int token = blockIdx.x < T ? static_cast<int>(blockIdx.x) : -1;  // to be selected here
   for (int chunk = blockIdx.x; chunk >= 0;) {

@@ -3,7 +3,7 @@
 // A wave reads weight rows ("units") as contiguous KiB pieces ("chunks": 16
 // bytes per lane), one after another, and multiplies each with the 1 to 8
 // activation rows its expert holds; lane partial sums are added over the wave
-// at a unit's end.  Nothing is shared between waves, so there is no barrier in
+// at a unit's end (row_totals).  Nothing is shared between waves, so there is no barrier in
 // the stream, and the units split evenly over any number of waves.
 //
 // What bounds it is the rate of the weight loads.  Reading a row in whole KiB
@@ -65,20 +65,42 @@ struct DotI8 {
   }
 };
 
-// Sum over the wave, the same on every lane, in a fixed order.
+// Sums over the wave of up to kUnitRows values a lane: lane l gets that of row
+// total_row(l).  A swap of half a wave (or of every other 16 lanes) between two
+// rows' values makes one value of both, so 8 rows take 10 exchanges instead of
+// 48.  Every row is added in the same order, by lanes 32 apart, then 16, then
+// within 16, whatever its place and the number of rows.
+__device__ __forceinline__ int total_row(int lane) {
+  return (lane >> 5 & 1) | (lane >> 3 & 2) | (lane >> 1 & 4);
+}
 template <class Acc>
-__device__ __forceinline__ Acc wave_total(Acc v) {
-  static_assert(sizeof(Acc) == 4, "32-bit sums");
-  const int lane = threadIdx.x & 63;
-  auto x = [&](auto step) __attribute__((always_inline)) {
-    v += __builtin_bit_cast(Acc, lane_xchg<decltype(step)::value>(__builtin_bit_cast(int, v), lane));
+__device__ __forceinline__ Acc row_totals(int nr, const Acc (&acc)[kUnitRows], int lane) {
+  static_assert(sizeof(Acc) == 4 && kUnitRows == 8, "32-bit sums of 8 rows");
+  auto fold32 = [](Acc a, Acc b) __attribute__((always_inline)) {  // a's in the low half, b's in the high
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a),
+                                                    __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(Acc, x) + __builtin_bit_cast(Acc, y);
   };
-  x(std::integral_constant<int, 0>{});
-  x(std::integral_constant<int, 1>{});
-  x(std::integral_constant<int, 2>{});
-  x(std::integral_constant<int, 3>{});
-  x(std::integral_constant<int, 4>{});
-  x(std::integral_constant<int, 5>{});
+  auto fold16 = [](Acc a, Acc b) __attribute__((always_inline)) {  // a's in even rows of 16, b's in odd
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
+                                                    __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(Acc, x) + __builtin_bit_cast(Acc, y);
+  };
+  auto other = [&](auto step, Acc v) __attribute__((always_inline)) {
+    return __builtin_bit_cast(Acc, lane_xchg<decltype(step)::value>(__builtin_bit_cast(int, v), lane));
+  };
+  Acc v = fold16(fold32(acc[0], acc[1]), fold32(acc[2], acc[3])), give = v;
+  if (nr > 4) {
+    const Acc w = fold16(fold32(acc[4], acc[5]), fold32(acc[6], acc[7]));
+    give = lane & 8 ? v : w;
+    v = lane & 8 ? w : v;
+  }
+  v += other(std::integral_constant<int, 3>{}, give);
+  v += other(std::integral_constant<int, 2>{}, v);
+  v += other(std::integral_constant<int, 1>{}, v);
+  v += other(std::integral_constant<int, 0>{}, v);
   return v;
 }
 
