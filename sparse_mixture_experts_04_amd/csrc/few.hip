@@ -36,14 +36,17 @@
 // is quantised per token and h per row.
 //
 // Bound by the weight rows' loads (rowstream.h): T=16, d=7168, F=2048, bf16
-// reads 7.3 GB in 1.19 ms, 6.1 TB/s; T=1 there 704 MB in 116 us, as fast; T=4 with
-// 8-bit weights 1.1 GB in 178 us.  At T=1, d=2048, F=768 the 75 MB need 12 us and
+// reads 7.3 GB in 1.16 ms, 6.3 TB/s; T=1 there 704 MB in 115 us, 6.1 TB/s; T=4 with
+// 8-bit weights 1.1 GB in 171 us.  At T=1, d=2048, F=768 the 75 MB need 12 us and
 // the kernel takes 27: the selection (9 us, of which the shared experts' share
 // hides half), the plan once the picks are known, the wait before the down stage
 // and the latency of each stage's first loads, and the fetch of code that the
 // weights have driven out of the caches (some 0.4 us per 128 bytes: hence loops
 // where they can be).  few_route_kernel adds 4 to 5 us, 13.6 at T=16, d=7168, where
-// each of its workgroups reads all of x.
+// each of its workgroups reads all of x (512 threads a half of the tokens each: 14.9).
+// Many experts of short rows are bound by what a row costs besides its bytes, in
+// the down stage above all: T=16, d=1280, F=256 takes 67 us for the 26 that its
+// 157 MB need; 82 entries of 1280 rows of 512 bytes, 1 us a row and wave.
 #include <type_traits>
 
 #include "few.h"
