@@ -36,7 +36,7 @@
 // is quantised per token and h per row.
 //
 // Bound by the weight rows' loads (rowstream.h): T=16, d=7168, F=2048, bf16
-// reads 7.3 GB in 1.16 ms, 6.3 TB/s; T=1 there 704 MB in 115 us, 6.1 TB/s; T=4 with
+// reads 7.3 GB in 1.16 to 1.23 ms, 6.0 to 6.3 TB/s; T=1 there 704 MB in 115 us, 6.1 TB/s; T=4 with
 // 8-bit weights 1.1 GB in 171 us.  At T=1, d=2048, F=768 the 75 MB need 12 us and
 // the kernel takes 27: the selection (9 us, of which the shared experts' share
 // hides half), the plan once the picks are known, the wait before the down stage
