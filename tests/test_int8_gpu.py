@@ -169,7 +169,8 @@ OFFSETS = [
 
 @pytest.mark.parametrize("offsets", OFFSETS)
 @pytest.mark.parametrize("scale,N,K", [(1, 130, 256), (17, 130, 256), (60, 130, 256),
-                                       (100, 1030, 2048), (400, 1030, 2048)])
+                                       (100, 1030, 2048), (400, 1030, 2048),
+                                       (1800, 4096, 128)])    # items by counters
 def test_product_groups(offsets, scale, N, K):
     print(f"groups {offsets} x {scale}", flush=True)
     off = [o * scale for o in offsets]
@@ -238,7 +239,8 @@ def test_product_refusals():
         L.gemm_int8(a, sa, w, t, y, offsets=off, ws=torch.empty(8, dtype=torch.uint8, device=DEV))
 
 
-@pytest.mark.parametrize("M,N,K", [(300, 200, 512), (4096, 1024, 2048), (12000, 1030, 2048)])
+@pytest.mark.parametrize("M,N,K", [(300, 200, 512), (4096, 1024, 2048), (12000, 1030, 2048),
+                                   (72000, 4096, 128)])
 def test_product_other_stream_and_graph(M, N, K):
     E = 3
     off = torch.tensor([0, M // 3, M // 3, M], dtype=torch.int32, device=DEV)
@@ -284,6 +286,8 @@ FFN = [
     MoEConfig("i8_wide", T=5200, d=256, F=640, act="bf16", E=128, S=1),
     MoEConfig("i8_big", T=6000, d=1024, F=768, act="bf16", E=64, S=2),
     MoEConfig("i8_big_f32", T=6000, d=1024, F=768, act="f32", E=64, S=1),
+    # both products take their items from counters
+    MoEConfig("i8_counters", T=24000, d=1536, F=768, act="bf16", E=64, S=2),
 ]
 
 
