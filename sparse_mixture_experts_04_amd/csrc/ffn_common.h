@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.h"
+#include "items.h"
 
 namespace moe {
 
@@ -10,14 +11,6 @@ namespace moe {
 // Number of XCDs, and of the per-XCD work counters stored after
 // tile_start[E+S].
 constexpr int kXcds = 8;
-
-struct Item {
-  int g;      // group
-  int m0;     // first row of the tile inside the group
-  int rows;   // valid rows in the tile
-  int n;      // column tile
-  int grows;  // rows of the group
-};
 
 // A wave-uniform read of device memory through the scalar data cache: its
 // completion is counted by lgkmcnt, not vmcnt, so using the value does not
@@ -28,48 +21,10 @@ __device__ __forceinline__ int32_t sload(const int32_t* base, int idx) {
   return ((const_scalar_i32)base)[__builtin_amdgcn_readfirstlane(idx)];
 }
 
-// Binary search over tile_start (in LDS), then the item's place in its
-// group.  A group's row tiles are taken in bands of up to kBand tiles; a
-// band's items run column tile outer, row tile inner.  Routed experts at
-// large batch have a few row tiles (one band: each weight tile is read from
-// HBM once while all of the expert's rows use it); the shared experts'
-// many row tiles go band by band, so the workgroups running together on an
-// XCD share both activation and weight tiles.
-constexpr int kBand = 8;
-
-// Item `it`, which lies in group g of grows rows.
-__device__ __forceinline__ Item place_item(long long it, const int* ts, int g, int n_tiles, int MT,
-                                           int grows, bool balanced) {
-  Item r;
-  r.g = g;
-  r.grows = grows;
-  const int mt = ts[g + 1] - ts[g];
-  const int local = static_cast<int>(it - static_cast<long long>(ts[g]) * n_tiles);
-  const int band = mt < kBand ? mt : kBand;
-  const int full = mt / band;
-  const int in_full = full * band * n_tiles;
-  int m;
-  if (local < in_full) {
-    const int b = local / (band * n_tiles);
-    const int rem = local - b * band * n_tiles;
-    r.n = rem / band;
-    m = b * band + rem % band;
-  } else {
-    const int last = mt - full * band;
-    const int rem = local - in_full;
-    r.n = rem / last;
-    m = full * band + rem % last;
-  }
-  const int base = balanced ? (grows + 32 * mt - 1) / (32 * mt) * 32 : MT;
-  r.m0 = m * base;
-  const int left = grows - r.m0;
-  r.rows = left < base ? left : base;
-  return r;
-}
-
 // balanced: a group of L rows in t row tiles gets tiles of
 // base = 32 * ceil(L / (32 t)) rows (the last one the rest, at least one
-// row); otherwise row tile m starts at m * MT.
+// row); otherwise row tile m starts at m * MT.  Binary search over tile_start
+// (in LDS), then the item's place in its group.
 __device__ __forceinline__ Item decode_item(long long it, const int* ts, int G, int n_tiles,
                                             int MT, const int32_t* __restrict__ offsets, int T,
                                             int E, bool balanced = false) {
