@@ -398,7 +398,7 @@ moe_status moe_quantize_int8(int64_t rows, int32_t K, moe_dtype dtype, const voi
  *   offsets int32 [E+1], non-decreasing; NULL with E = 1: group 0 has all M rows.
  * Rows outside every group keep what y held.  An offset outside [0, M] counts as
  * the nearest end of it, one smaller than an offset before it as that one.
- * N >= 0, 0 <= M <= 2^31 - 1024, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and
+ * 0 <= M, N <= 2^31 - 1024, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and
  * M * max(N, Kp) < 2^40, a, w and y 16-byte aligned. */
 typedef struct {
   int32_t M, N, K, E;

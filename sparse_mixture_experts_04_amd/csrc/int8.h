@@ -13,7 +13,7 @@ inline long long code_row(long long K) { return (K + kCodeRow - 1) / kCodeRow * 
 // 127^2 * 131072 < 2^31.
 constexpr int kInt8MaxK = 131072;
 constexpr int kInt8MaxGroups = 256;
-// Rows of a product, at most: row numbers rounded up to a tile stay in 32 bits.
+// Rows and columns of a product, at most: rounded up to a tile they stay in 32 bits.
 constexpr long long kInt8MaxRows = (1LL << 31) - 1024;
 
 // Rows of fp32 or bf16 values to codes [rows, code_row(K)] and scales [rows].

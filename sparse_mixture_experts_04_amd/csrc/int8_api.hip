@@ -18,7 +18,7 @@ moe_status check_gemm(const moe_gemm_int8_desc* d) {
   if (!d) return MOE_ERR_NULL;
   if (d->M < 0 || d->N < 0 || d->K <= 0 || d->E <= 0) return MOE_ERR_SHAPE;
   if (d->out != MOE_F32 && d->out != MOE_BF16) return MOE_ERR_DTYPE;
-  if (d->K > kInt8MaxK || d->E > kInt8MaxGroups || d->M > kInt8MaxRows)
+  if (d->K > kInt8MaxK || d->E > kInt8MaxGroups || d->M > kInt8MaxRows || d->N > kInt8MaxRows)
     return MOE_ERR_UNSUPPORTED;
   const long long lim = 1LL << 40, kp = code_row(d->K);
   const long long wide = d->N > kp ? d->N : kp;
