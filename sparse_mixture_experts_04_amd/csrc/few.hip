@@ -129,20 +129,23 @@ __global__ __launch_bounds__(512) void few_route_kernel(FewArgs p, int ctrl_ints
 
 // exp(x) for x <= 0, to a few 2^-53: x = n ln 2 + r with |r| <= ln 2 / 2, and the
 // Taylor series of exp(r) to r^13 / 13! (the next term is below 2^-56) in a loop
-// whose factors come from memory.  The library's exp is straight-line code with
+// whose factors come from memory.  Below -800, where exp(x) is 0 in fp64 all the
+// same, the argument is -800: r is small only while n fits the 53 bits of its
+// products, and logits reach 1e80.  The library's exp is straight-line code with
 // its constants in registers: two of those spilled, and scratch memory costs the
 // whole kernel (8-bit, T=4, d=7168: 184 us with it, 177 without).
 __device__ const double kOneOver[14] = {0.0, 1.0, 1.0 / 2, 1.0 / 3, 1.0 / 4, 1.0 / 5, 1.0 / 6,
                                         1.0 / 7, 1.0 / 8, 1.0 / 9, 1.0 / 10, 1.0 / 11, 1.0 / 12,
                                         1.0 / 13};
 __device__ __forceinline__ double few_exp(double x) {
+  x = x < -800.0 ? -800.0 : x;  // a NaN stays
   const double n = rint(x * 1.4426950408889634);
   // ln 2 = 45426 / 65536 + the rest; n times the first part is exact
   const double r = fma(n, -1.4286068203094173e-06, fma(n, -45426.0 / 65536.0, x));
   double e = 1.0;
 #pragma unroll 1
   for (int k = 13; k > 0; --k) e = fma(e, r * kOneOver[k], 1.0);
-  return ldexp(e, static_cast<int>(fmax(n, -2000.0)));
+  return ldexp(e, static_cast<int>(fmax(n, -2000.0)));  // fmax: a NaN has no integer
 }
 
 // Top-6 and gates of token t by one wave, in little code: a workgroup that runs
