@@ -383,6 +383,9 @@ moe_status moe_forward_marked(const moe_desc* desc, const void* x,
  * holds a NaN or an infinity has codes 0 and scale NaN (the products of that
  * row are NaN, no others are).
  *
+ * The workspaces of the calls below are 16-byte aligned (MOE_ERR_UNSUPPORTED
+ * otherwise).
+ *
  * moe_quantize_int8: x [rows, K] (MOE_F32 or MOE_BF16, dense, aligned to its
  * element) -> codes [rows, Kp] (16-byte aligned), scales [rows].  rows >= 0,
  * 1 <= K <= 131072; rows up to 2^31 - 1.  No workspace. */

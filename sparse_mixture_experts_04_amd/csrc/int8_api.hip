@@ -14,6 +14,12 @@ namespace {
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// A workspace of `need` bytes at an address that its atomics can take.
+moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  return aligned16(ws) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
 moe_status check_gemm(const moe_gemm_int8_desc* d) {
   if (!d) return MOE_ERR_NULL;
   if (d->M < 0 || d->N < 0 || d->K <= 0 || d->E <= 0) return MOE_ERR_SHAPE;
@@ -161,12 +167,13 @@ moe_status moe_gemm_int8_workspace_size(const moe_gemm_int8_desc* desc, size_t* 
 moe_status moe_gemm_int8(const moe_gemm_int8_desc* desc, const int8_t* a, const float* a_scale,
                          const int8_t* w, const float* w_scale, const int32_t* offsets, void* y,
                          void* ws, size_t ws_bytes, hipStream_t stream) {
-  const moe_status st = check_gemm(desc);
+  moe_status st = check_gemm(desc);
   if (st != MOE_OK) return st;
   if (desc->M == 0 || desc->N == 0) return MOE_OK;
   if (!a || !a_scale || !w || !w_scale || !y || (!offsets && desc->E != 1)) return MOE_ERR_NULL;
   if (!aligned16(a) || !aligned16(w) || !aligned16(y)) return MOE_ERR_UNSUPPORTED;
-  if (!ws || ws_bytes < gemm_int8_counter_ints() * sizeof(int32_t)) return MOE_ERR_WORKSPACE;
+  st = check_ws(ws, ws_bytes, gemm_int8_counter_ints() * sizeof(int32_t));
+  if (st != MOE_OK) return st;
   Int8Args g{};
   g.a = a;
   g.a_scale = a_scale;
@@ -198,7 +205,7 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
                                const int32_t* offsets, const int32_t* sorted_pair, void* y_routed,
                                void* y_shared, void* ws, size_t ws_bytes, hipStream_t stream) {
   size_t need = 0;
-  const moe_status st = moe_expert_ffn_int8_workspace_size(desc, &need);
+  moe_status st = moe_expert_ffn_int8_workspace_size(desc, &need);
   if (st != MOE_OK) return st;
   const Shape s = to_shape(desc);
   if (!int8_weights_ok(w, s) || !offsets) return MOE_ERR_NULL;
@@ -206,7 +213,7 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
   if (!aligned16(x) || !aligned16(y_routed) || (s.S > 0 && !aligned16(y_shared)) ||
       !weights_aligned(s, {w->w_gate, w->w_up, w->w_down}, {w->ws_gate, w->ws_up, w->ws_down}))
     return MOE_ERR_UNSUPPORTED;
-  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if ((st = check_ws(ws, ws_bytes, need)) != MOE_OK) return st;
   if (s.T == 0) return MOE_OK;
   Carver c{static_cast<char*>(ws)};
   const FfnInt8Ws f = carve_ffn_int8(c, s);
@@ -263,7 +270,7 @@ moe_status moe_forward_few_workspace_size(const moe_desc* desc, size_t* bytes) {
 moe_status moe_forward_few(const moe_desc* desc, const void* x, const moe_weights* w,
                            const float* bias, void* y, int32_t* topk_idx, float* gates, void* ws,
                            size_t ws_bytes, hipStream_t stream) {
-  const moe_status st = check_few_desc(desc);
+  moe_status st = check_few_desc(desc);
   if (st != MOE_OK) return st;
   const Shape s = to_shape(desc);
   if (!weights_ok(w, s) || !w->w_router || !bias) return MOE_ERR_NULL;
@@ -273,7 +280,7 @@ moe_status moe_forward_few(const moe_desc* desc, const void* x, const moe_weight
   if (in_place(s, x, y) || !aligned16(x) || !aligned16(w->w_router) ||
       !weights_aligned(s, {w->w_gate, w->w_up, w->w_down}, {w->ws_gate, w->ws_up, w->ws_down}))
     return MOE_ERR_UNSUPPORTED;
-  if (!ws || ws_bytes < few_ws_bytes(s)) return MOE_ERR_WORKSPACE;
+  if ((st = check_ws(ws, ws_bytes, few_ws_bytes(s))) != MOE_OK) return st;
   FewArgs a = few_args(s, x, w->w_router, bias, y, topk_idx, gates, ws);
   a.w_gate = w->w_gate;
   a.w_up = w->w_up;
@@ -287,7 +294,7 @@ moe_status moe_forward_few(const moe_desc* desc, const void* x, const moe_weight
 moe_status moe_forward_few_int8(const moe_desc* desc, const void* x, const moe_weights_int8* w,
                                 const float* bias, void* y, int32_t* topk_idx, float* gates,
                                 void* ws, size_t ws_bytes, hipStream_t stream) {
-  const moe_status st = check_few_desc(desc);
+  moe_status st = check_few_desc(desc);
   if (st != MOE_OK) return st;
   const Shape s = to_shape(desc);
   if (!int8_weights_ok(w, s) || !w->w_router || !bias) return MOE_ERR_NULL;
@@ -295,7 +302,7 @@ moe_status moe_forward_few_int8(const moe_desc* desc, const void* x, const moe_w
   if (in_place(s, x, y) || !aligned16(x) || !aligned16(w->w_router) ||
       !weights_aligned(s, {w->w_gate, w->w_up, w->w_down}, {w->ws_gate, w->ws_up, w->ws_down}))
     return MOE_ERR_UNSUPPORTED;
-  if (!ws || ws_bytes < few_ws_bytes(s)) return MOE_ERR_WORKSPACE;
+  if ((st = check_ws(ws, ws_bytes, few_ws_bytes(s))) != MOE_OK) return st;
   FewArgs a = few_args(s, x, w->w_router, bias, y, topk_idx, gates, ws);
   a.w_gate = w->w_gate;
   a.w_up = w->w_up;

@@ -25,3 +25,25 @@ def test_columns_up_to_a_tile_below_32_bits(N, code):
     """Columns rounded up to a tile have to stay in 32 bits, as rows do: past
     2^31 - 16 columns there were no tiles at all and y was left unwritten."""
     assert gemm_status(N=N) == code
+
+
+def test_workspaces_are_16_byte_aligned():
+    """Counters and flags in a workspace are accessed by atomics, which fault at an
+    address that is not a multiple of their size; so a part of a larger buffer has
+    to start on 16 bytes, as tensors do."""
+    odd = [ctypes.c_void_p(0x1000 + i) for i in (1, 2, 4, 8, 15)]
+    Y = ctypes.c_void_p(0x100000)
+    big = 1 << 30
+    g = L.GemmInt8Desc(4, 8, 128, 1, L.BF16)
+    d = L.Desc(8, 512, 128, 256, 2, 6, L.BF16, L.BF16, L.GATE_RATIO, 1.0, 0.0)
+    w, w8 = L.Weights(*([0x1000] * 7)), L.WeightsInt8(*([0x1000] * 13))
+    for ws in odd:
+        assert lib.moe_gemm_int8(ctypes.byref(g), P, P, P, P, None, Y, ws, big, None) == 5
+        assert lib.moe_expert_ffn_int8(ctypes.byref(d), P, ctypes.byref(w8), P, P, Y, Y, ws, big,
+                                       None) == 5
+        assert lib.moe_forward_few(ctypes.byref(d), P, ctypes.byref(w), P, Y, None, None, ws, big,
+                                   None) == 5
+        assert lib.moe_forward_few_int8(ctypes.byref(d), P, ctypes.byref(w8), P, Y, None, None, ws,
+                                        big, None) == 5
+        # too small comes first, as for an aligned one
+        assert lib.moe_gemm_int8(ctypes.byref(g), P, P, P, P, None, Y, ws, 0, None) == 4
