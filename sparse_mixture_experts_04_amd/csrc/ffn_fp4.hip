@@ -125,7 +125,7 @@ struct Fp4Cfg {
 
 __device__ __forceinline__ void dma4(const void* src, uint32_t lds_addr) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_addr);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                :
                : "v"(src), "s"(m0)
                : "m0");
@@ -133,7 +133,7 @@ __device__ __forceinline__ void dma4(const void* src, uint32_t lds_addr) {
 
 __device__ __forceinline__ void dma16_lds(const void* src, uint32_t lds_addr) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_addr);
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(src), "s"(m0)
                : "m0");

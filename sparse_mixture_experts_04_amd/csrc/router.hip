@@ -289,7 +289,7 @@ __global__ __launch_bounds__(256) void router_logits_bf16(
 #pragma unroll
     for (int q = 0; q < LPW; ++q) {
       const uint32_t m0 = __builtin_amdgcn_readfirstlane(ring_base + slot * SE * 2 + dst_off[q]);
-      asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+      asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                    :
                    : "v"(src[q] + ko), "s"(m0)
                    : "m0");
