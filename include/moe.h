@@ -399,6 +399,7 @@ moe_status moe_quantize_int8(int64_t rows, int32_t K, moe_dtype dtype, const voi
  * fp32's normal range (2^-126 to 2^128), y is inexact, infinite or NaN.
  *   a [M, Kp], a_scale [M], w [E, N, Kp], w_scale [E, N], y [M, N];
  *   offsets int32 [E+1], non-decreasing; NULL with E = 1: group 0 has all M rows.
+ * y shares no memory with the inputs.
  * Rows outside every group keep what y held.  An offset outside [0, M] counts as
  * the nearest end of it, one smaller than an offset before it as that one.
  * 0 <= M, N <= 2^31 - 1024, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and
@@ -436,7 +437,8 @@ typedef struct {
 
 /* Every expert's whole FFN with 8-bit weights: moe_expert_ffn's inputs and
  * outputs.  x is quantised per token, h = silu(gate) * up is taken in fp32 and
- * quantised per row, y_routed and y_shared are rounded once to act.  The
+ * quantised per row, y_routed and y_shared are rounded once to act (scales are
+ * multiplied as in moe_gemm_int8, with the same limits on their product).  The
  * descriptor is that of the layer without 8-bit weights (act == weight), the
  * same that moe_router, moe_dispatch and moe_combine take around this call.
  * Rows of y_routed from offsets[E] on keep what they held. */
@@ -453,9 +455,14 @@ moe_status moe_expert_ffn_int8(const moe_desc* desc, const void* x, const moe_we
  * not updated; capacity_factor must be 0 (MOE_ERR_UNSUPPORTED otherwise, as
  * are T > 16, weight == MOE_MXFP4, d or F > 16384 and the shapes
  * moe_forward does not take).  topk_idx [T, 6] and gates [T, 6+S] are written
- * where given.  A token whose x holds a NaN or an infinity gets NaN gates or
- * outputs, its choice of experts is unspecified but valid.  Results are bitwise
- * reproducible and a token's do not depend on the other tokens' values.
+ * where given.  A token whose x holds a NaN or an infinity gets outputs that are
+ * NaN or infinite (its gates may be NaN too), its choice of experts is unspecified
+ * but valid.  Results are bitwise reproducible and a token's do not depend on the
+ * other tokens' values.  (Weights and bias are finite, as for every call.)
+ * Beside moe_forward with the same bf16 weights (E=256, S=2, us a call): d=2048,
+ * F=768, T=1 31 against 84, T=16 161-167 against 178-180; d=7168, F=2048, T=1
+ * 124-132 against 188-195, T=4 360-397 against 425-436, T=16 1108-1202 against
+ * 1196-1204.
  * x and y must not share memory (MOE_ERR_UNSUPPORTED).
  * moe_forward_few_int8 takes 8-bit weights: x is quantised per token, h per row
  * (from fp32).  Both calls take the workspace of

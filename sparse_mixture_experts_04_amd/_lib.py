@@ -402,7 +402,8 @@ def bias_update(desc, counts, gamma, bias):
 
 
 def forward(desc, x, weights, bias, gamma, y, routing=None, ws=None, events=None):
-    """moe_forward.  ``routing`` is an optional dict of output tensors with
+    """moe_forward (for up to 16 tokens forward_few takes less time and rounds
+    less often; it updates no bias).  ``routing`` is an optional dict of output tensors with
     keys topk_idx, gates, margin, counts, offsets, sorted_pair, pair_pos.
     With ``events`` (7 torch.cuda.Event, enable_timing=True, each recorded
     once beforehand) it calls moe_forward_marked, which records them after

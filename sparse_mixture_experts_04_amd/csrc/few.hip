@@ -30,19 +30,21 @@
 //
 // Precision: logits, affinities and gates in fp64 (the selection is that of
 // exact arithmetic but for keys within ~1e-15); products with fp32 (or exact
-// int32) accumulation; h and the experts' outputs in fp32, one rounding into y.
+// int32, in the down product per pass over K) accumulation; h and the experts'
+// outputs in fp32, one rounding into y.
 // With bf16 weights h enters the down product as two bf16 terms (h = hi + lo
 // to 2^-17): the second product costs no memory traffic.  With 8-bit weights x
 // is quantised per token and h per row.
 //
 // Bound by the weight rows' loads (rowstream.h): T=16, d=7168, F=2048, bf16
-// reads 7.3 GB in 1.16 to 1.23 ms, 6.0 to 6.3 TB/s; T=1 there 704 MB in 115 us, 6.1 TB/s; T=4 with
-// 8-bit weights 1.1 GB in 171 us.  At T=1, d=2048, F=768 the 75 MB need 12 us and
-// the kernel takes 27: the selection (9 us, of which the shared experts' share
-// hides half), the plan once the picks are known, the wait before the down stage
-// and the latency of each stage's first loads, and the fetch of code that the
-// weights have driven out of the caches (some 0.4 us per 128 bytes: hence loops
-// where they can be).  few_route_kernel adds 4 to 5 us, 13.6 at T=16, d=7168, where
+// reads 7.63 GB in 1.20 to 1.23 ms, 6.2 to 6.3 TB/s; T=1 there 706 MB in 119 us,
+// 5.9 TB/s; T=4 with 8-bit weights 0.98 GB in 175 to 179 us, 5.5 TB/s (bytes as
+// counted).  At T=1, d=2048, F=768 the 77 MB need 12 us and the kernel takes 27:
+// the selection (9 us, of which the shared experts' share hides half), the plan
+// once the picks are known, the wait before the down stage and the latency of each
+// stage's first loads, and the fetch of code that the weights have driven out of
+// the caches (some 0.4 us per 128 bytes: hence loops where they can be).
+// few_route_kernel adds 4 to 5 us, 13.6 at T=16, d=7168, where
 // each of its workgroups reads all of x (512 threads a half of the tokens each: 14.9).
 // Many experts of short rows are bound by what a row costs besides its bytes, in
 // the down stage above all: T=16, d=1280, F=256 takes 67 us for the 26 that its

@@ -18,12 +18,16 @@ namespace moe {
 // groups hold few) x 256 weight rows; each XCD's workgroups share a contiguous
 // run of the items, evenly or by a counter (by_counters).
 //
-// Bound by the matrix instructions: 16384x2048x7168 takes 235 us, 2.05 POP/s (the
-// 8192^3 product of the vendor's library 2.09 here); the experts of a large
-// batch (d=7168, F=2048, 131072 rows in ragged groups) run at 1.89 POP/s gate/up
-// and 1.60 down, where K is short and the epilogue (scales, bf16, the staged
+// Large products run at the rate of the matrix instructions' own library product
+// (8192^3 2.09 POP/s here): 16384x2048x7168 takes 218 to 241 us, 2.0 to 2.2 POP/s,
+// the matrix units busy in 56% of the cycles of a clock that the load pulls down
+// to 1.8 GHz (of 2.4), memory at 1.8 TB/s.  The experts of a large batch (d=7168,
+// F=2048, 131072 rows in ragged groups) run at 1.9 POP/s gate/up (52% busy) and
+// 1.6 down (42%), where K is short and the epilogue (scales, bf16, the staged
 // tile) a seventh of a tile's time.  With few rows a group it streams the
-// weights: T=64 there reads 4.05 GB in 489 + 290 us, 5.2 TB/s.
+// weights: T=64 there reads 2.71 + 1.36 GB in 500 + 298 us, 5.4 and 4.6 TB/s.
+// The 256-row forms use all 256 registers; the gated and the bf16 one keep one or
+// two more in scratch memory, stored before the K loop and read after it.
 using BigI8 = BigShape<256, 32, 3, 6, MmaI8>;
 using MidI8 = BigShape<128, 64, 3, 3, MmaI8>;
 static_assert(BigI8::LDS_ELEMS * 2 <= 147456 && MidI8::LDS_ELEMS * 2 <= 147456, "LDS");

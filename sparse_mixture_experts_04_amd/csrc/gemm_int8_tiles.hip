@@ -14,8 +14,9 @@
 // Bound by the weight loads.  kRing steps of a wave are in registers, all but
 // one in flight; loads are issued unconditionally so that the compiler can
 // count them; without the non-temporal hint, for the two loads of a step share
-// their lines (with it the T=64 experts took 864 us, without 794).  A stream of
-// whole weight rows multiplied by v_dot4 needs one LDS byte per weight byte and
+// their lines (the experts of T=64, d=7168, F=2048, which now take the 128-row
+// tiles, ran on this kernel in 864 us with it and 794 without).  A stream of whole
+// weight rows multiplied by v_dot4 needs one LDS byte per weight byte and
 // row, this needs one whatever the rows: 8 rows a group, N=K=2048, 256 groups
 // 397 against 216 us.  The matrix and vector units are mostly idle.
 #include "int8_rows.h"
