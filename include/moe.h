@@ -399,6 +399,7 @@ moe_status moe_quantize_int8(int64_t rows, int32_t K, moe_dtype dtype, const voi
  * fp32's normal range (2^-126 to 2^128), y is inexact, infinite or NaN.
  *   a [M, Kp], a_scale [M], w [E, N, Kp], w_scale [E, N], y [M, N];
  *   offsets int32 [E+1], non-decreasing; NULL with E = 1: group 0 has all M rows.
+ * Codes are -127 to 127 (-128 too for K <= 130944, where the sums still fit int32);
  * y shares no memory with the inputs.
  * Rows outside every group keep what y held.  An offset outside [0, M] counts as
  * the nearest end of it, one smaller than an offset before it as that one.
