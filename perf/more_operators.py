@@ -408,22 +408,20 @@ def _adamw_own(st):
             return None if flat is None else [
                 flat[s // per:(s + n + per - 1) // per] for s, n in zip(st["starts"], st["sizes"])]
 
-        scales = {}
-        if bits8:
-            scales = {"m_scales": parts(st["m_scale"], 256), "v_scales": parts(st["v_scale"], 256)}
-        plan = ops.adamw_plan(parts(st["p"]), parts(st["g"]), parts(st["m"]), parts(st["v"]),
-                              copies=parts(st["copy"]), **scales)
-        values = None
+        values, states = None, {}
         if bits8:
             values = {n: torch.zeros(st["p"].shape, device="cuda") for n in ("m", "v")}
-            values["parts"] = (parts(values["m"]), parts(values["v"]))
+            states = {"m_scales": parts(st["m_scale"], 256), "v_scales": parts(st["v_scale"], 256),
+                      "m_values": parts(values["m"]), "v_values": parts(values["v"])}
+        plan = ops.adamw_plan(parts(st["p"]), parts(st["g"]), parts(st["m"]), parts(st["v"]),
+                              copies=parts(st["copy"]), **states)
         st["kept"] = (plan, values)
     plan, values = st["kept"]
     ops.adamw_step(plan, STEP, lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS, weight_decay=DECAY,
                    grad_scale=st["factor"])
     out = {"m": st["m"], "v": st["v"], "p": st["p"]}
     if bits8:
-        ops.adamw_state_values(plan, *values["parts"])
+        ops.adamw_state_values(plan)
         out["m"], out["v"] = values["m"], values["v"]
     if st["copy"] is not None:
         out["copy"] = st["copy"]
