@@ -477,6 +477,158 @@ moe_status moe_forward_few_int8(const moe_desc* desc, const void* x, const moe_w
                                 float* gates_or_null, void* ws, size_t ws_bytes,
                                 hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The gated half of a SwiGLU feed-forward block, with its gradients ("Under
+ * The Hood: Inkling", expert configuration), for training dense blocks, shared
+ * experts and experts whose rows are already grouped:
+ *
+ *   a = x W_gate^T,  u = x W_up^T,  h = silu(a) * u       (elementwise product)
+ *   s = 1 / (1 + exp(-a)),  da = dh u s (1 + a (1 - s)),  du = dh a s
+ *   dx = da W_gate + du W_up,  dW_gate = da^T x,  dW_up = du^T x
+ *
+ *   x, dx [M, d], w_gate, w_up and their gradients [E, F, d], h, dh [M, F], all
+ *   of `act` and aligned to their element; offsets int32 [E+1], non-decreasing:
+ *   the rows offsets[e] <= m < offsets[e+1] go through the matrices of group e;
+ *   NULL with E = 1: all M rows do.  An offset outside [0, M] counts as the
+ *   nearest end of it, one smaller than an offset before it as that one.
+ * Rows outside every group keep what h, pre and dx held and are in no gradient; a
+ * group without rows has gradients of zeros.  The gradients are written, not
+ * added to what was there.
+ * pre fp32 [M, 2F] takes a, then u, of each row where it is given; the backward
+ * pass reads it, or with NULL computes it again (a third of its work more).
+ * Sums are fp32; h, dx, dW_gate and dW_up are rounded once, and with bf16 da and
+ * du are rounded to bf16 before their products.  Results are bitwise
+ * reproducible.  dx may be NULL (not wanted), dW_gate and dW_up both may.
+ * 0 <= M <= 2^31 - 1024, 1 <= d, F <= 131072, 1 <= E <= 256, M max(d, 2F) and
+ * E F d < 2^40.  Any sizes and alignments are taken; rows of x and the matrices
+ * that start on 16 bytes (d and F multiples of 8 in bf16) are the fast ones.
+ * Outputs share no memory with inputs or each other.  The workspace (16-byte
+ * aligned; `saved`: pre will be given to the backward pass) is for one call at a
+ * time. */
+typedef struct {
+  int32_t M, d, F, E;
+  moe_dtype act;
+} moe_gated_ff_desc;
+
+moe_status moe_gated_ff_workspace_size(const moe_gated_ff_desc* desc, int32_t backward,
+                                       int32_t saved, size_t* bytes);
+moe_status moe_gated_ff(const moe_gated_ff_desc* desc, const void* x, const void* w_gate,
+                        const void* w_up, const int32_t* offsets_or_null, void* h,
+                        float* pre_or_null, void* ws, size_t ws_bytes, hipStream_t stream);
+moe_status moe_gated_ff_backward(const moe_gated_ff_desc* desc, const void* x, const void* w_gate,
+                                 const void* w_up, const int32_t* offsets_or_null, const void* dh,
+                                 const float* pre_or_null, void* dx_or_null,
+                                 void* dw_gate_or_null, void* dw_up_or_null, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Products of 8-bit floating point (OCP e4m3) with an fp32 scale for every 128
+ * values of an activation row and every 128 x 128 values of a weight matrix.
+ * Beside the 8-bit integers above, whose scale spans a row: a value far outside
+ * the others costs the precision of its block, not of its row.
+ *
+ * Codes: s = max|x| / 448 of the block, rounded to fp32 and at least 2^-126, and
+ * each value the e4m3 number nearest to the exact x / s, ties to the even code.  A
+ * block of zeros has scale 0 and codes 0; one that holds a NaN or an infinity has
+ * scale NaN and codes 0, which makes every product with it NaN.  Rows of codes
+ * are padded with zeros to Kp = K rounded up to 128.
+ *
+ * moe_quantize_fp8: x [rows, K] (MOE_F32 or MOE_BF16, dense, aligned to its
+ * element) -> codes [rows, Kp] (16-byte aligned), scales [rows, Kp/128].
+ * moe_quantize_fp8_weights: w [E, N, K] -> codes [E, N, Kp], scales
+ * [E, ceil(N/128), Kp/128].  1 <= K <= 131072, rows <= 2^31 - 1024, E <= 65535,
+ * N <= 8388480. */
+moe_status moe_quantize_fp8(int64_t rows, int32_t K, moe_dtype dtype, const void* x,
+                            uint8_t* codes, float* scales, hipStream_t stream);
+moe_status moe_quantize_fp8_weights(int32_t E, int32_t N, int32_t K, moe_dtype dtype,
+                                    const void* w, uint8_t* codes, float* scales,
+                                    hipStream_t stream);
+
+/* Grouped product: y[m, n] = sum_b a_scale[m, b] w_scale[e, n/128, b] sum_{k in b}
+ * a[m, k] w[e, n, k] over the blocks b of 128 values of K, for the rows m of group
+ * e (offsets as for moe_gated_ff; rows outside every group keep what y held).
+ * Sums are fp32, y is rounded once to `out` (MOE_F32 or MOE_BF16).  Codes are any
+ * e4m3 values; a NaN code (0x7f, 0xff) makes its products NaN.
+ *   a [M, Kp], a_scale [M, Kp/128], w [E, N, Kp], w_scale [E, ceil(N/128), Kp/128],
+ *   y [M, N]; y shares no memory with the inputs.
+ * 0 <= M, N <= 2^31 - 1024, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and
+ * M * max(N, Kp) < 2^40, a, w, y and the workspace 16-byte aligned. */
+typedef struct {
+  int32_t M, N, K, E;
+  moe_dtype out;
+} moe_gemm_fp8_desc;
+
+moe_status moe_gemm_fp8_workspace_size(const moe_gemm_fp8_desc* desc, size_t* bytes);
+moe_status moe_gemm_fp8(const moe_gemm_fp8_desc* desc, const uint8_t* a, const float* a_scale,
+                        const uint8_t* w, const float* w_scale, const int32_t* offsets_or_null,
+                        void* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * One AdamW step over many tensors in one launch:
+ *
+ *   g = gradient * grad_scale (1 where it is not given)
+ *   m' = beta1 m + (1 - beta1) g,  v' = beta2 v + (1 - beta2) g^2
+ *   p' = p (1 - lr weight_decay)
+ *        - lr (m' / (1 - beta1^step)) / (sqrt(v' / (1 - beta2^step)) + eps)
+ *
+ * p (`param`) and the gradients (`grad`) are MOE_F32 or MOE_BF16, p' is rounded
+ * once to p's type (bf16 parameters lose updates below 2^-9 of them); with fp32
+ * parameters `copy` (or NULL) takes p' rounded to bf16 as well.  States:
+ * state_bits 32: m and v fp32, updated in fp32.
+ * state_bits 8: m int8 codes, v uint8 codes, with fp32 scales m_scale, v_scale
+ *   [ceil(n/256)], the largest |m'| and v' of 256 consecutive values:
+ *     m = s sign(c) (c / 127)^2,  c = round(127 sqrt(|m'| / s))
+ *     v = z (c / 255)^4,          c = round(255 (v' / z)^(1/4)), 1 at least where v' > 0
+ *   Codes are those of exact arithmetic on the old states and g; p' is taken from
+ *   the unrounded m' and v'.  Zeros (codes and scales) are the states before the first step.  A
+ *   block whose m' or v' is not finite gets scales of NaN and codes 0.
+ *   m_values, v_values (both or neither): fp32 [n], where
+ *   moe_adamw_state_values writes the values that the codes stand for.
+ *
+ * moe_adamw_prepare checks `count` tensors (host array; n values each, dense,
+ * aligned to their element) and writes them into `table` (device memory of
+ * moe_adamw_table_size bytes, 16-byte aligned) on `stream`; *chunks goes to the
+ * calls that use the table.  The tensors must stay where they are while it is
+ * used, and no two of them share memory.
+ * moe_adamw: step counts from 1.  lr_dev, step_dev and grad_scale_dev (device
+ * memory, or NULL) are read when the kernel runs, for captured graphs; lr and step
+ * are not read where they are given.  A grad_scale that is NaN or infinite leaves
+ * everything as it was. */
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+  float* m_values;
+  float* v_values;
+  int64_t n;
+} moe_adamw_tensor;
+
+typedef struct {
+  int32_t count;
+  moe_dtype param, grad;
+  int32_t state_bits;
+} moe_adamw_desc;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale_dev;
+} moe_adamw_step;
+
+moe_status moe_adamw_table_size(const moe_adamw_desc* desc, size_t* bytes);
+moe_status moe_adamw_prepare(const moe_adamw_desc* desc, const moe_adamw_tensor* tensors,
+                             int64_t* chunks, void* table, size_t table_bytes, hipStream_t stream);
+moe_status moe_adamw(const moe_adamw_desc* desc, const moe_adamw_step* step, int64_t chunks,
+                     const void* table, hipStream_t stream);
+moe_status moe_adamw_state_values(const moe_adamw_desc* desc, int64_t chunks, const void* table,
+                                  hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

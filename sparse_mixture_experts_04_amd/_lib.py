@@ -31,7 +31,11 @@ SYMBOLS = ("moe_abi_version", "moe_status_string", "moe_workspace_size", "moe_ro
            "moe_dispatch_noalloc", "moe_router_planes_size", "moe_router_prepare",
            "moe_quantize_int8", "moe_gemm_int8_workspace_size", "moe_gemm_int8",
            "moe_expert_ffn_int8_workspace_size", "moe_expert_ffn_int8",
-           "moe_forward_few_workspace_size", "moe_forward_few", "moe_forward_few_int8")
+           "moe_forward_few_workspace_size", "moe_forward_few", "moe_forward_few_int8",
+           "moe_gated_ff_workspace_size", "moe_gated_ff", "moe_gated_ff_backward",
+           "moe_quantize_fp8", "moe_quantize_fp8_weights", "moe_gemm_fp8_workspace_size",
+           "moe_gemm_fp8", "moe_adamw_table_size", "moe_adamw_prepare", "moe_adamw",
+           "moe_adamw_state_values")
 
 
 class MoEError(RuntimeError):
@@ -65,6 +69,33 @@ class WeightsInt8(ctypes.Structure):
         for g in ("", "s") for p in ("_gate", "_up", "_down") for a in ("w", "t")]
 
 
+class GatedFfDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("d", ctypes.c_int32), ("F", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("act", ctypes.c_int)]
+
+
+class GemmFp8Desc(GemmInt8Desc):
+    pass
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("p", "g", "m", "v", "m_scale", "v_scale", "copy", "m_values", "v_values")] + [
+                    ("n", ctypes.c_int64)]
+
+
+class AdamwDesc(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("param", ctypes.c_int), ("grad", ctypes.c_int),
+                ("state_bits", ctypes.c_int32)]
+
+
+class AdamwStep(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in
+                ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+                    ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p),
+                    ("step_dev", ctypes.c_void_p), ("grad_scale_dev", ctypes.c_void_p)]
+
+
 class Routing(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("topk_idx", "gates", "margin", "counts", "offsets", "sorted_pair",
@@ -79,6 +110,7 @@ def _load(path=LIB_PATH):
     P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     D = ctypes.POINTER(Desc)
     W = ctypes.POINTER(Weights)
+    GF, AD = ctypes.POINTER(GatedFfDesc), ctypes.POINTER(AdamwDesc)
     sig = {
         "moe_abi_version": (I, []),
         "moe_status_string": (ctypes.c_char_p, [I]),
@@ -107,6 +139,20 @@ def _load(path=LIB_PATH):
         "moe_forward_few_workspace_size": (I, [D, ctypes.POINTER(Z)]),
         "moe_forward_few": (I, [D, P, W, P, P, P, P, P, Z, P]),
         "moe_forward_few_int8": (I, [D, P, ctypes.POINTER(WeightsInt8), P, P, P, P, P, Z, P]),
+        "moe_gated_ff_workspace_size": (I, [GF, ctypes.c_int32, ctypes.c_int32,
+                                            ctypes.POINTER(Z)]),
+        "moe_gated_ff": (I, [GF, P, P, P, P, P, P, P, Z, P]),
+        "moe_gated_ff_backward": (I, [GF, P, P, P, P, P, P, P, P, P, P, Z, P]),
+        "moe_quantize_fp8": (I, [ctypes.c_int64, ctypes.c_int32, I, P, P, P, P]),
+        "moe_quantize_fp8_weights": (I, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, I, P, P,
+                                         P, P]),
+        "moe_gemm_fp8_workspace_size": (I, [ctypes.POINTER(GemmFp8Desc), ctypes.POINTER(Z)]),
+        "moe_gemm_fp8": (I, [ctypes.POINTER(GemmFp8Desc), P, P, P, P, P, P, P, Z, P]),
+        "moe_adamw_table_size": (I, [AD, ctypes.POINTER(Z)]),
+        "moe_adamw_prepare": (I, [AD, ctypes.POINTER(AdamwTensor), ctypes.POINTER(ctypes.c_int64),
+                                  P, Z, P]),
+        "moe_adamw": (I, [AD, ctypes.POINTER(AdamwStep), ctypes.c_int64, P, P]),
+        "moe_adamw_state_values": (I, [AD, ctypes.c_int64, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -647,3 +693,244 @@ def forward_few(desc, x, weights, bias, y, topk_idx=None, gates=None, ws=None):
         None if topk_idx is None else _at(topk_idx, dev, torch.int32, (T, k), "topk_idx"),
         None if gates is None else _at(gates, dev, torch.float32, (T, k + S), "gates"),
         *_ws(ws, dev)))
+
+
+# ------------------------------------- gated block: forward and gradients
+
+def _opt(t, idx, dtype, shape, name):
+    """Address of a tensor that may be None."""
+    return None if t is None else _at(t, idx, dtype, shape, name)
+
+
+def gated_ff_workspace(M, d, F, E, dtype, device, backward=False, saved=True):
+    """A workspace for gated_ff, or with ``backward`` for both it and
+    gated_ff_backward (``saved``: which will be given ``pre``)."""
+    n = ctypes.c_size_t(0)
+    _check("moe_gated_ff_workspace_size", lib.moe_gated_ff_workspace_size(
+        ctypes.byref(GatedFfDesc(M, d, F, E, act_code(dtype))), int(backward), int(saved),
+        ctypes.byref(n)))
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
+
+
+def _gated_args(fn, x, w_gate, w_up):
+    dev = _on_gpu(x, "x")
+    if x.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 3:
+        raise ValueError(f"{fn} takes x [M, d] and w_gate, w_up [E, F, d]")
+    M, d = x.shape
+    E, F, _ = w_gate.shape
+    desc = GatedFfDesc(M, d, F, E, act_code(x.dtype))
+    return dev, desc, (_at(x, dev, x.dtype, (M, d), "x"),
+                       _at(w_gate, dev, x.dtype, (E, F, d), "w_gate"),
+                       _at(w_up, dev, x.dtype, (E, F, d), "w_up"))
+
+
+def gated_ff(x, w_gate, w_up, h, offsets=None, pre=None, ws=None):
+    """moe_gated_ff: h [M, F] = silu(x W_gate^T) * (x W_up^T) for x [M, d] and
+    matrices [E, F, d], all fp32 or all bf16.  ``offsets`` int32 [E+1] gives each
+    group's rows; without it E must be 1.  ``pre`` fp32 [M, 2F] takes the two
+    products for gated_ff_backward."""
+    dev, desc, args = _gated_args("gated_ff", x, w_gate, w_up)
+    M, F, E = desc.M, desc.F, desc.E
+    if ws is None:
+        ws = gated_ff_workspace(M, desc.d, F, E, x.dtype, x.device)
+    _check("moe_gated_ff", _call(
+        dev, lib.moe_gated_ff, ctypes.byref(desc), *args,
+        _opt(offsets, dev, torch.int32, (E + 1,), "offsets"), _at(h, dev, x.dtype, (M, F), "h"),
+        _opt(pre, dev, torch.float32, (M, 2 * F), "pre"), *_ws(ws, dev)))
+
+
+def gated_ff_backward(x, w_gate, w_up, dh, dx, dw_gate, dw_up, offsets=None, pre=None, ws=None):
+    """moe_gated_ff_backward: the gradients of gated_ff's x, w_gate and w_up from
+    that of h, written into dx (or None), dw_gate and dw_up (or both None).
+    Without ``pre`` (of gated_ff) the two products are computed again."""
+    dev, desc, args = _gated_args("gated_ff_backward", x, w_gate, w_up)
+    M, d, F, E, dt = desc.M, desc.d, desc.F, desc.E, x.dtype
+    if ws is None:
+        ws = gated_ff_workspace(M, d, F, E, dt, x.device, backward=True, saved=pre is not None)
+    _check("moe_gated_ff_backward", _call(
+        dev, lib.moe_gated_ff_backward, ctypes.byref(desc), *args,
+        _opt(offsets, dev, torch.int32, (E + 1,), "offsets"),
+        _at(dh, dev, dt, (M, F), "dh"), _opt(pre, dev, torch.float32, (M, 2 * F), "pre"),
+        _opt(dx, dev, dt, (M, d), "dx"), _opt(dw_gate, dev, dt, (E, F, d), "dw_gate"),
+        _opt(dw_up, dev, dt, (E, F, d), "dw_up"), *_ws(ws, dev)))
+
+
+# --------------------------------------- products of 8-bit floating point
+
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+
+
+def _blocks(n):
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def quantize_fp8(x, codes=None, scales=None):
+    """moe_quantize_fp8 of the rows of x [..., K] (fp32 or bf16): codes e4m3
+    [..., Kp], Kp = K rounded up to 128, and scales fp32 [..., Kp/128].  Allocates
+    the outputs that are not given."""
+    dev = _on_gpu(x, "x")
+    code = act_code(x.dtype)
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("x needs a last dimension of at least one value")
+    K, lead = shape[-1], shape[:-1]
+    out, sc = (*lead, _blocks(K) * FP8_BLOCK), (*lead, _blocks(K))
+    if codes is None:
+        codes = torch.empty(out, dtype=FP8, device=x.device)
+    if scales is None:
+        scales = torch.empty(sc, dtype=torch.float32, device=x.device)
+    _check("moe_quantize_fp8", _call(
+        dev, lib.moe_quantize_fp8, lead.numel(), K, code, _at(x, dev, x.dtype, shape, "x"),
+        _at(codes, dev, FP8, out, "codes"), _at(scales, dev, torch.float32, sc, "scales")))
+    return codes, scales
+
+
+def quantize_fp8_weights(w, codes=None, scales=None):
+    """moe_quantize_fp8_weights of matrices w [E, N, K] (fp32 or bf16): codes e4m3
+    [E, N, Kp] and scales fp32 [E, ceil(N/128), Kp/128]."""
+    dev = _on_gpu(w, "w")
+    code = act_code(w.dtype)
+    if w.dim() != 3 or w.shape[2] < 1:
+        raise ValueError("quantize_fp8_weights takes w [E, N, K]")
+    E, N, K = w.shape
+    out, sc = (E, N, _blocks(K) * FP8_BLOCK), (E, _blocks(N), _blocks(K))
+    if codes is None:
+        codes = torch.empty(out, dtype=FP8, device=w.device)
+    if scales is None:
+        scales = torch.empty(sc, dtype=torch.float32, device=w.device)
+    _check("moe_quantize_fp8_weights", _call(
+        dev, lib.moe_quantize_fp8_weights, E, N, K, code, _at(w, dev, w.dtype, (E, N, K), "w"),
+        _at(codes, dev, FP8, out, "codes"), _at(scales, dev, torch.float32, sc, "scales")))
+    return codes, scales
+
+
+def gemm_fp8_workspace(M, N, K, E=1, device="cuda"):
+    """A workspace for gemm_fp8 of these sizes (reusable by calls in turn)."""
+    n = ctypes.c_size_t(0)
+    _check("moe_gemm_fp8_workspace_size",
+           lib.moe_gemm_fp8_workspace_size(ctypes.byref(GemmFp8Desc(M, N, K, E, F32)),
+                                           ctypes.byref(n)))
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
+
+
+def gemm_fp8(a, a_scale, w, w_scale, y, offsets=None, ws=None):
+    """moe_gemm_fp8: y [M, N] (fp32 or bf16) = a [M, Kp] e4m3 times w [E, N, Kp]
+    e4m3, scaled by a_scale [M, Kp/128] and w_scale [E, ceil(N/128), Kp/128].
+    ``offsets`` int32 [E+1] gives each group's rows; without it E must be 1.  Rows
+    outside the groups keep what y held."""
+    dev = _on_gpu(a, "a")
+    if a.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("gemm_fp8 takes a [M, Kp] and w [E, N, Kp]")
+    _on_gpu(y, "y")
+    M, Kp = a.shape
+    E, N, _ = w.shape
+    if Kp == 0 or Kp % FP8_BLOCK:
+        raise ValueError(f"gemm_fp8: rows of codes are padded to a multiple of 128, got {Kp}")
+    desc = GemmFp8Desc(M, N, Kp, E, act_code(y.dtype))
+    if ws is None:
+        ws = gemm_fp8_workspace(M, N, Kp, E, a.device)
+    _check("moe_gemm_fp8", _call(
+        dev, lib.moe_gemm_fp8, ctypes.byref(desc), _at(a, dev, FP8, (M, Kp), "a"),
+        _at(a_scale, dev, torch.float32, (M, Kp // FP8_BLOCK), "a_scale"),
+        _at(w, dev, FP8, (E, N, Kp), "w"),
+        _at(w_scale, dev, torch.float32, (E, _blocks(N), Kp // FP8_BLOCK), "w_scale"),
+        _opt(offsets, dev, torch.int32, (E + 1,), "offsets"),
+        _at(y, dev, y.dtype, (M, N), "y"), *_ws(ws, dev)))
+
+
+# -------------------------------------------------------------- AdamW step
+
+ADAMW_BLOCK = 256
+
+
+class AdamwPlan:
+    """The tensors of a step in a device table (see adamw_plan)."""
+
+    def __init__(self, device, desc, chunks, table, tensors):
+        self.device, self.desc, self.chunks, self.table = device, desc, chunks, table
+        self.tensors = tensors  # keeps them alive
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v_scales=None,
+               m_values=None, v_values=None):
+    """A plan for adamw_step over lists of tensors on one GPU (moe_adamw_prepare).
+    ``params`` all fp32 or all bf16, ``grads`` likewise; states fp32, or int8 and
+    uint8 codes with ``m_scales`` and ``v_scales`` (fp32, one for every 256 values;
+    zeros to begin with).  ``copies``: bf16 tensors that take each fp32 parameter
+    too.  ``m_values``, ``v_values``: fp32 tensors for adamw_state_values.  The plan
+    holds the tensors; a gradient that moves needs a new plan."""
+    lists = {"params": params, "grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
+             "copies": copies, "m_scales": m_scales, "v_scales": v_scales, "m_values": m_values,
+             "v_values": v_values}
+    lists = {n: None if l is None else list(l) for n, l in lists.items()}
+    count = len(lists["params"])
+    for name, l in lists.items():
+        if l is not None and len(l) != count:
+            raise ValueError(f"adamw_plan: {len(l)} {name} for {count} params")
+    if count == 0:
+        raise ValueError("adamw_plan: no params")
+    dev = _on_gpu(lists["params"][0], "params[0]")
+    pt, gt = lists["params"][0].dtype, getattr(lists["grads"][0], "dtype", None)
+    bits8 = getattr(lists["exp_avg"][0], "dtype", None) is torch.int8
+    if bits8 != (m_scales is not None) or bits8 != (v_scales is not None):
+        raise ValueError("adamw_plan: m_scales and v_scales go with 8-bit states")
+    if (m_values is None) != (v_values is None) or (m_values is not None and not bits8):
+        raise ValueError("adamw_plan: m_values and v_values go together, with 8-bit states")
+    desc = AdamwDesc(count, act_code(pt), act_code(gt), 8 if bits8 else 32)
+    f32, mt, vt = torch.float32, *((torch.int8, torch.uint8) if bits8 else (torch.float32,) * 2)
+    rows = (AdamwTensor * count)()
+    for i, r in enumerate(rows):
+        p = lists["params"][i]
+        if not isinstance(p, torch.Tensor):
+            raise TypeError(f"params[{i}] must be a torch.Tensor")
+        shape, r.n = p.shape, p.numel()
+        blocks = ((r.n + ADAMW_BLOCK - 1) // ADAMW_BLOCK,)
+        for field, name, dt, shp in (
+                ("p", "params", pt, shape), ("g", "grads", gt, shape),
+                ("m", "exp_avg", mt, shape), ("v", "exp_avg_sq", vt, shape),
+                ("copy", "copies", torch.bfloat16, shape), ("m_scale", "m_scales", f32, blocks),
+                ("v_scale", "v_scales", f32, blocks), ("m_values", "m_values", f32, shape),
+                ("v_values", "v_values", f32, shape)):
+            if lists[name] is not None:
+                setattr(r, field, _at(lists[name][i], dev, dt, shp, f"{name}[{i}]"))
+    n = ctypes.c_size_t(0)
+    _check("moe_adamw_table_size", lib.moe_adamw_table_size(ctypes.byref(desc), ctypes.byref(n)))
+    device = lists["params"][0].device
+    table = torch.empty(n.value, dtype=torch.uint8, device=device)
+    chunks = ctypes.c_int64(0)
+    _check("moe_adamw_prepare", _call(dev, lib.moe_adamw_prepare, ctypes.byref(desc), rows,
+                                      ctypes.byref(chunks), table.data_ptr(), n.value))
+    return AdamwPlan(dev, desc, chunks.value, table, lists)
+
+
+def adamw_step(plan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+               grad_scale=None):
+    """moe_adamw: one step (the `step`-th, from 1) over the plan's tensors.  ``step``
+    may be an int64 tensor of one value on the GPU and ``lr`` an fp32 one, read when
+    the kernel runs (a captured graph then follows them); ``grad_scale``, an fp32
+    tensor of one value, multiplies every gradient, and where it is NaN or infinite
+    the step changes nothing."""
+    a = AdamwStep(0.0, beta1, beta2, eps, weight_decay, 0)
+    for name, v, dt in (("lr", lr, torch.float32), ("step", step, torch.int64),
+                        ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            if v.numel() != 1:
+                raise ValueError(f"{name} must hold one value")
+            setattr(a, name + "_dev", _at(v, plan.device, dt, v.shape, name))
+        elif name != "grad_scale":
+            setattr(a, name, v)
+        elif v is not None:
+            raise TypeError("grad_scale must be a torch.Tensor")
+    _check("moe_adamw", _call(plan.device, lib.moe_adamw, ctypes.byref(plan.desc),
+                              ctypes.byref(a), plan.chunks, plan.table.data_ptr()))
+
+
+def adamw_state_values(plan):
+    """moe_adamw_state_values: the fp32 values of the plan's 8-bit states, into the
+    plan's m_values and v_values."""
+    if plan.tensors["m_values"] is None:
+        raise ValueError("adamw_state_values: the plan has no m_values and v_values")
+    _check("moe_adamw_state_values", _call(plan.device, lib.moe_adamw_state_values,
+                                           ctypes.byref(plan.desc), plan.chunks,
+                                           plan.table.data_ptr()))

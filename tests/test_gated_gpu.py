@@ -1,0 +1,247 @@
+"""The gated block and its gradients against their formulas in 64 bits."""
+import pytest
+import torch
+
+from block_util import gated64, rand, spans, within
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def ops():
+    from sparse_mixture_experts_04_amd import ops
+    return ops
+
+
+def inputs(M, d, F, E, dt, seed=0, skew=0):
+    return (rand((M, d), dt, seed + 1, skew=skew), rand((E, F, d), dt, seed + 2, d ** -0.5, skew=skew),
+            rand((E, F, d), dt, seed + 3, d ** -0.5, skew=skew), rand((M, F), dt, seed + 4, 0.1, skew=skew))
+
+
+def both(x, wg, wu, dh, offsets, saved=True, want=("dx", "dw")):
+    """Forward and backward; outputs start as a marker value."""
+    L = ops()
+    M, d = x.shape
+    E, F, _ = wg.shape
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    new = lambda like: torch.full_like(like, 7.0)
+    h, dx, dwg, dwu = new(dh), new(x), new(wg), new(wu)
+    pre = torch.full((M, 2 * F), 7.0, device="cuda") if saved else None
+    ws = L.gated_ff_workspace(M, d, F, E, x.dtype, "cuda", backward=True, saved=saved)
+    ws.fill_(0xff)
+    L.gated_ff(x, wg, wu, h, offsets=off, pre=pre, ws=ws)
+    L.gated_ff_backward(x, wg, wu, dh, dx if "dx" in want else None,
+                        dwg if "dw" in want else None, dwu if "dw" in want else None,
+                        offsets=off, pre=pre, ws=ws)
+    torch.cuda.synchronize()
+    return {"h": h, "dx": dx, "dw_gate": dwg, "dw_up": dwu}
+
+
+def check(x, wg, wu, dh, offsets, got, names=("h", "dx", "dw_gate", "dw_up")):
+    ref, covered = gated64(x, wg, wu, offsets, dh)
+    for n in names:
+        value, bound = ref[n]
+        if n in ("h", "dx"):
+            within(got[n][covered.to("cuda")], value[covered], bound[covered], n)
+            assert (got[n].cpu()[~covered] == 7.0).all(), f"{n}: rows outside the groups"
+        else:
+            within(got[n], value, bound, n)
+    for e, (lo, hi) in enumerate(spans(offsets, x.shape[0], wg.shape[0])):
+        if lo == hi and "dw_gate" in names:
+            assert not got["dw_gate"][e].any() and not got["dw_up"][e].any()
+
+
+DENSE = [(1, 8, 8), (1, 256, 64), (2, 264, 24), (5, 512, 128), (16, 2048, 768), (17, 72, 200),
+         (33, 1000, 136), (64, 128, 1032), (127, 520, 264), (128, 256, 128), (129, 264, 136),
+         (256, 32, 16), (257, 1032, 256), (300, 16, 520), (700, 768, 384)]
+ODD = [(1, 1, 1), (3, 7, 5), (31, 33, 17), (65, 129, 63), (130, 301, 131)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,d,F", DENSE + ODD)
+def test_dense(M, d, F, dt):
+    x, wg, wu, dh = inputs(M, d, F, 1, dt, seed=M * 7 + d)
+    check(x, wg, wu, dh, None, both(x, wg, wu, dh, None))
+
+
+GROUPS = [
+    (40, 64, 32, [0, 40]),
+    (40, 64, 32, [0, 0, 13, 13, 40, 40]),                 # empty groups at every place
+    (64, 264, 72, [3, 20, 20, 50]),                       # rows before and behind the groups
+    (50, 128, 40, [0, 70, 60, -5, 50]),                   # outside [0, M], not increasing
+    (9, 40, 48, [0, 1, 2, 3, 4, 5, 6, 7, 8, 9]),          # one row each
+    (600, 512, 136, [0, 257, 258, 300, 555, 600]),
+    (1000, 256, 256, [0, 1, 129, 385, 386, 1000]),
+]
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,d,F,offsets", GROUPS)
+def test_groups(M, d, F, offsets, dt):
+    x, wg, wu, dh = inputs(M, d, F, len(offsets) - 1, dt, seed=M + d)
+    check(x, wg, wu, dh, offsets, both(x, wg, wu, dh, offsets))
+
+
+@pytest.mark.parametrize("per", [0, 1, 3, 40])
+def test_256_groups(per):
+    g = torch.Generator().manual_seed(per)
+    n = torch.randint(0, 2 * per + 1, (256,), generator=g)
+    off = [0] + torch.cumsum(n, 0).tolist()
+    x, wg, wu, dh = inputs(off[-1], 64, 24, 256, BF, seed=per)
+    check(x, wg, wu, dh, off, both(x, wg, wu, dh, off))
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("skew", [1, 3, 4])
+def test_alignment(skew, dt):
+    x, wg, wu, dh = inputs(70, 136, 72, 2, dt, skew=skew)
+    check(x, wg, wu, dh, [0, 30, 70], both(x, wg, wu, dh, [0, 30, 70]))
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_without_saved_products(dt):
+    """pre computed again gives the gradients of the saved one to the bit."""
+    x, wg, wu, dh = inputs(150, 264, 136, 3, dt)
+    off = [0, 60, 60, 150]
+    a, b = both(x, wg, wu, dh, off), both(x, wg, wu, dh, off, saved=False)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_parts_not_wanted():
+    x, wg, wu, dh = inputs(90, 128, 64, 1, BF)
+    full = both(x, wg, wu, dh, None)
+    no_dw, no_dx = both(x, wg, wu, dh, None, want=("dx",)), both(x, wg, wu, dh, None, want=("dw",))
+    assert torch.equal(full["dx"], no_dw["dx"]) and (no_dw["dw_up"] == 7.0).all()
+    assert torch.equal(full["dw_up"], no_dx["dw_up"]) and (no_dx["dx"] == 7.0).all()
+
+
+@pytest.mark.parametrize("E", [1, 4])
+def test_no_rows(E):
+    """Without rows the gradients of the matrices are zeros."""
+    x, wg, wu, dh = inputs(0, 128, 64, E, BF)
+    off = None if E == 1 else [0] * (E + 1)
+    got = both(x, wg, wu, dh, off)
+    assert not got["dw_gate"].any() and not got["dw_up"].any()
+
+
+def test_pre_values():
+    L = ops()
+    x, wg, wu, _ = inputs(77, 264, 40, 1, BF)
+    h = torch.empty((77, 40), dtype=BF, device="cuda")
+    pre = torch.empty((77, 80), device="cuda")
+    L.gated_ff(x, wg, wu, h, pre=pre)
+    X = x.cpu().double()
+    for i, w in enumerate((wg, wu)):
+        W = w[0].cpu().double()
+        within(pre[:, 40 * i:40 * i + 40], X @ W.T, 268 * 2.0 ** -24 * (X.abs() @ W.abs().T))
+
+
+def test_large_arguments():
+    """silu's two ends: exp overflows to the right result."""
+    L = ops()
+    x = torch.tensor([[200.0], [-200.0], [88.0], [-88.0], [0.0]], device="cuda")
+    one = torch.ones((1, 1, 1), device="cuda")
+    h, pre = torch.empty_like(x), torch.empty((5, 2), device="cuda")
+    L.gated_ff(x, one, one, h, pre=pre)
+    v = x.cpu().double()
+    within(h, v * v * torch.sigmoid(v), 16 * 2.0 ** -24 * (v * v * torch.sigmoid(v)).abs() + 1e-38)
+    dh, dx, dg, du = torch.ones_like(x), torch.empty_like(x), torch.empty_like(one), torch.empty_like(one)
+    L.gated_ff_backward(x, one, one, dh, dx, dg, du, pre=pre)
+    assert torch.isfinite(dx).all() and torch.isfinite(dg).all()
+
+
+def test_gradients_against_differences():
+    """dx, dWg and dWu against central differences of sum(h dh), taken in 64 bits from
+    the formula of h alone."""
+    x, wg, wu, dh = inputs(6, 12, 9, 1, F32, seed=5)
+    got = both(x, wg, wu, dh, None)
+    X, G, U, D = (t.cpu().double() for t in (x, wg[0], wu[0], dh))
+
+    def loss(a, b, c):
+        p, q = a @ b.T, a @ c.T
+        return float((p * torch.sigmoid(p) * q * D).sum())
+
+    step = 1e-5
+    for name, i in (("dx", 0), ("dw_gate", 1), ("dw_up", 2)):
+        args = [X, G, U]
+        num = torch.zeros_like(args[i])
+        for at in range(num.numel()):
+            hi, lo = ([t.clone() for t in args] for _ in range(2))
+            hi[i].view(-1)[at] += step
+            lo[i].view(-1)[at] -= step
+            num.view(-1)[at] = (loss(*hi) - loss(*lo)) / (2 * step)
+        g = got[name].cpu().double().view(num.shape)
+        # differences: step^2 / 6 of a third derivative of order 1, 1e-16 / step of rounding
+        assert (g - num).abs().max() < 1e-8 + 1e-5 * num.abs().max()
+
+
+def test_same_bits_again():
+    x, wg, wu, dh = inputs(513, 264, 136, 3, BF)
+    off = [0, 5, 260, 513]
+    a, b = both(x, wg, wu, dh, off), both(x, wg, wu, dh, off)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_rows_of_other_groups_do_not_leak():
+    """NaN rows of one group leave the others' results alone."""
+    x, wg, wu, dh = inputs(90, 64, 40, 3, BF)
+    off = [0, 31, 62, 90]
+    clean = both(x, wg, wu, dh, off)
+    x2, dh2 = x.clone(), dh.clone()
+    x2[31:62] = float("nan")
+    dh2[31:62] = float("inf")
+    dirty = both(x2, wg, wu, dh2, off)
+    keep = [r for r in range(90) if not 31 <= r < 62]
+    for n in ("h", "dx"):
+        assert torch.equal(clean[n][keep], dirty[n][keep]), n
+    for n in ("dw_gate", "dw_up"):
+        assert torch.equal(clean[n][[0, 2]], dirty[n][[0, 2]]), n
+
+
+def test_large_widths_bf16():
+    x, wg, wu, dh = inputs(600, 1536, 520, 1, BF, seed=9)
+    check(x, wg, wu, dh, None, both(x, wg, wu, dh, None))
+
+
+def test_long_batch():
+    x, wg, wu, dh = inputs(5000, 128, 72, 1, BF, seed=11)
+    check(x, wg, wu, dh, None, both(x, wg, wu, dh, None))
+
+
+def test_stream_and_graph():
+    """On another stream than the current one's tensors, and captured with replays
+    between eager work."""
+    L = ops()
+    x, wg, wu, dh = inputs(200, 256, 128, 2, BF)
+    off = torch.tensor([0, 90, 200], dtype=torch.int32, device="cuda")
+    want = both(x, wg, wu, dh, [0, 90, 200])
+    out = [torch.zeros_like(t) for t in (dh, x, wg, wu)]
+    pre = torch.zeros((200, 256), device="cuda")
+    ws = L.gated_ff_workspace(200, 256, 128, 2, BF, "cuda", backward=True)
+
+    def go():
+        L.gated_ff(x, wg, wu, out[0], offsets=off, pre=pre, ws=ws)
+        L.gated_ff_backward(x, wg, wu, dh, *out[1:], offsets=off, pre=pre, ws=ws)
+
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        go()
+    s.synchronize()
+    names = ("h", "dx", "dw_gate", "dw_up")
+    for n, t in zip(names, out):
+        assert torch.equal(t, want[n]), n
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for i in range(3):
+        for t in out:
+            t.fill_(3.0)
+        ws.fill_(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in zip(names, out):
+            assert torch.equal(t, want[n]), (i, n)
+        both(x, wg, wu, dh, [0, 90, 200])
