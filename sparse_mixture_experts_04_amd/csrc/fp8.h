@@ -31,5 +31,6 @@ struct Fp8Args {
   bool out_bf16;
 };
 hipError_t launch_gemm_fp8(const Fp8Args& a, hipStream_t st);
+hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st);
 
 }  // namespace moe

@@ -67,6 +67,7 @@ __global__ __launch_bounds__(kT32Threads) void gemm_fp8_tile_kernel(Fp8Args p) {
 }  // namespace
 
 hipError_t launch_gemm_fp8(const Fp8Args& a, hipStream_t st) {
+  if (a.M >= 64) return launch_gemm_fp8_big(a, st);
   gemm_fp8_tile_kernel<2><<<1024, kT32Threads, 0, st>>>(a);
   return hipGetLastError();
 }

@@ -1,0 +1,337 @@
+// e4m3 products for large batches.
+//
+// Tile, operand rings and the two wave groups in ping-pong are those of big_tile.h
+// (128 rows x 256 weight rows, K steps of 128 codes = 64 16-bit units, three slots
+// each), so a K step is one block of the scales.  The matrix instruction
+// (v_mfma_f32_32x32x64_f8f6f4, twice the bf16 rate) starts each block's sum at
+// zero, and the block joins the running sum by one fused multiply-add a value with
+// s_row s_column: 16 of them (64 cycles) beside two instructions of 64, on the
+// vector unit that the partner wave leaves idle.
+//
+// That instruction adds groups of 8 products with some 16 bits between the largest
+// and the last that counts: 1.4e-5 of a result (2-norm, measured at K = 128, 1024 and
+// 7168), 1/100 of the rounding of a bf16 y, which takes it.  An fp32 y takes the bf16
+// instruction on the codes as bf16 (exact; 1.4e-7 at K = 7168), at half the rate.
+//
+// The scales travel like the operands: each wave of the activation group loads, per
+// step, 32 row scales and the two weight scales of the tile into the stage's slot by
+// one 4-byte direct-to-LDS load, so that no load of theirs disturbs the count of
+// loads in flight.
+#include "big_tile.h"
+#include "fp8.h"
+
+namespace moe {
+
+namespace {
+
+using MidF8 = BigShape<128, 64, 3, 3>;
+typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kScaleSlot = 4 * 64;  // floats: 4 waves x (32 rows, 2 weight blocks, rest unused)
+
+// One direct global -> LDS load of 4 bytes a lane (dma16 has the why of the asm).
+__device__ __forceinline__ void dma4(const float* src, float* dst) {
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(dst))));
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(src), "s"(lds)
+               : "m0");
+}
+
+// 64 codes of K; the fragment's pieces of K are the same ones for both operands.
+__device__ __forceinline__ f32x16_t mul64(i32x8_t b, i32x8_t a, f32x16_t c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, 0, 0, 0);
+}
+
+// Eight codes of a fragment (words 2q and 2q + 1) as bf16, which holds every e4m3
+// value.
+__device__ __forceinline__ bf16x8_t wide8(i32x8_t f, int q) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  union {
+    bf16x2_t pair[4];
+    bf16x8_t all;
+  } u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    u.pair[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * q + i], 1.0f, false);
+    u.pair[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * q + i], 1.0f, true);
+  }
+  return u.all;
+}
+
+template <class C>
+struct ScaledCtx {
+  BigCtx<C> t;
+  const float* scale;  // this lane's scale of step 0 (activation group)
+};
+
+template <class C, bool FAST, int U, int GRP, int NV>
+__device__ __forceinline__ void f8_step(const ScaledCtx<C>& c, int kt, int nk,
+                                        bf16_t* const (&sA)[C::NSA], bf16_t* const (&sB)[C::NSB],
+                                        float* sS, int wig, int lane, const int (&off)[C::KK],
+                                        f32x16_t (&acc)[C::BM][C::BN]) {
+  constexpr int BLK = 32 * C::BK;
+  constexpr int NM = NV > 0 ? NV : 1;
+  constexpr int H = C::KK / 2;
+  i32x8_t a[H][NM], b[H][C::BN];
+  float s[NM];
+  const bf16_t* pa = sA[U % C::NSA];
+  const bf16_t* pb = sB[U % C::NSB];
+  const float* ps = sS + U % C::NSA * kScaleSlot;
+  auto frag = [&](const bf16_t* blk, int h) __attribute__((always_inline)) {
+    union {
+      bf16x8_t half[2];
+      i32x8_t all;
+    } u;
+    u.half[0] = *reinterpret_cast<const bf16x8_t*>(blk + off[2 * h]);
+    u.half[1] = *reinterpret_cast<const bf16x8_t*>(blk + off[2 * h + 1]);
+    return u.all;
+  };
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+#pragma unroll
+    for (int j = 0; j < C::BN; ++j) b[h][j] = frag(pb + (wig * 2 + j) * BLK, h);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) a[h][i] = frag(pa + (2 * i + GRP) * BLK, h);
+  }
+  // row block 2i + grp lies with wave 2i + grp's 32 scales; the two weight blocks
+  // (128 columns each) behind the first wave's
+  const float sw = ps[32 + (wig >> 1)];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) s[i] = ps[(2 * i + GRP) * 64 + (lane & 31)] * sw;
+  if constexpr (GRP == 0) {
+    const int ks = kt + C::NSB - 1 < nk ? kt + C::NSB - 1 : nk - 1;
+    c.t.template issue<C::LPW_B>(ks * C::BK, sB[(U + C::NSB - 1) % C::NSB], wig);
+  } else {
+    const int ks = kt + C::NSA - 1 < nk ? kt + C::NSA - 1 : nk - 1;
+    c.t.template issue<C::LPW_A>(ks * C::BK, sA[(U + C::NSA - 1) % C::NSA], wig);
+    dma4(c.scale + ks, sS + (U + C::NSA - 1) % C::NSA * kScaleSlot + wig * 64);
+  }
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): fragments in registers
+  if constexpr (GRP == 1) wait_vm<(C::NSA - 2) * (C::LPW_A + 1)>();
+  lds_barrier();
+  if constexpr (FAST) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < C::BN; ++j) {
+        f32x16_t p = {};
+#pragma unroll
+        for (int h = 0; h < H; ++h) p = mul64(b[h][j], a[h][i], p);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(p[r], s[i], acc[i][j][r]);
+      }
+  } else {
+    f32x16_t p[NM][C::BN] = {};
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x8_t wb[C::BN];
+#pragma unroll
+        for (int j = 0; j < C::BN; ++j) wb[j] = wide8(b[h][j], q);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const bf16x8_t wa = wide8(a[h][i], q);
+#pragma unroll
+          for (int j = 0; j < C::BN; ++j)
+            p[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa, p[i][j], 0, 0, 0);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < C::BN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(p[i][j][r], s[i], acc[i][j][r]);
+  }
+  if constexpr (GRP == 0) wait_vm<(C::NSB - 2) * C::LPW_B>();
+  lds_barrier();
+}
+
+template <class C, bool FAST, int GRP, int NV>
+__device__ __forceinline__ void f8_kloop(const ScaledCtx<C>& c, int nk,
+                                         bf16_t* const (&sA)[C::NSA],
+                                         bf16_t* const (&sB)[C::NSB], float* sS, int wave,
+                                         int lane, f32x16_t (&acc)[C::BM][C::BN]) {
+  static_assert(C::NSA == 3 && C::NSB == 3, "unrolled by 3");
+  const int wig = wave & 3, r32 = lane & 31;
+  int off[C::KK];
+#pragma unroll
+  for (int kk = 0; kk < C::KK; ++kk)
+    off[kk] = r32 * C::BK + (((2 * kk + (lane >> 5)) ^ row_swz<C>(r32)) << 3);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int ks = s < nk ? s : nk - 1;
+    if constexpr (GRP == 0) {
+      c.t.template issue<C::LPW_B>(ks * C::BK, sB[s], wig);
+    } else {
+      c.t.template issue<C::LPW_A>(ks * C::BK, sA[s], wig);
+      dma4(c.scale + ks, sS + s * kScaleSlot + wig * 64);
+    }
+  }
+  if constexpr (GRP == 0) wait_vm<C::LPW_B>();
+  else wait_vm<C::LPW_A + 1>();
+  lds_barrier();                // point 0: stage 0 complete
+  if (GRP == 1) lds_barrier();  // point 1 for group 1
+  for (int kt = 0; kt < nk; kt += 3) {
+    f8_step<C, FAST, 0, GRP, NV>(c, kt, nk, sA, sB, sS, wig, lane, off, acc);
+    if (kt + 1 < nk) f8_step<C, FAST, 1, GRP, NV>(c, kt + 1, nk, sA, sB, sS, wig, lane, off, acc);
+    if (kt + 2 < nk) f8_step<C, FAST, 2, GRP, NV>(c, kt + 2, nk, sA, sB, sS, wig, lane, off, acc);
+  }
+  if (GRP == 0) lds_barrier();
+}
+
+template <class C, bool FAST, int GRP, int NV>
+__device__ __forceinline__ void f8_kloop_nv(const ScaledCtx<C>& c, int nk,
+                                            bf16_t* const (&sA)[C::NSA],
+                                            bf16_t* const (&sB)[C::NSB], float* sS, int wave,
+                                            int lane, int nv, f32x16_t (&acc)[C::BM][C::BN]) {
+  if constexpr (NV == 0) {
+    f8_kloop<C, FAST, GRP, 0>(c, nk, sA, sB, sS, wave, lane, acc);
+  } else {
+    if (nv == NV) f8_kloop<C, FAST, GRP, NV>(c, nk, sA, sB, sS, wave, lane, acc);
+    else f8_kloop_nv<C, FAST, GRP, NV - 1>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+  }
+}
+
+template <class C, bool OUT_BF16>
+__global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
+  __shared__ __attribute__((aligned(1024))) bf16_t lds[C::LDS_ELEMS];
+  __shared__ __attribute__((aligned(256))) float sS[C::NSA * kScaleSlot];
+  __shared__ EntryPlan plan;
+  bf16_t* sA[C::NSA];
+  bf16_t* sB[C::NSB];
+#pragma unroll
+  for (int i = 0; i < C::NSA; ++i) sA[i] = lds + i * C::A_STAGE;
+#pragma unroll
+  for (int i = 0; i < C::NSB; ++i) sB[i] = lds + C::NSA * C::A_STAGE + i * C::B_STAGE;
+  constexpr int NOUT = C::NB;
+  constexpr int OB = OUT_BF16 ? 2 : 4;
+  static_assert(C::MT * NOUT * OB <= C::LDS_ELEMS * 2, "output tile");
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  make_entries<C::THREADS, C::MT>(p, plan);
+  const int n_tiles = (p.N + NOUT - 1) / NOUT, nb = (p.N + kFp8Block - 1) / kFp8Block;
+  const long long total = static_cast<long long>(plan.start[p.E]) * n_tiles;
+  const int xcd = blockIdx.x % kXcds;
+  const int kld = p.Kp / 2;  // row length in 16-bit units
+  const int nk = p.Kp / kFp8Block;
+  const int lrow = lane / C::CPR;
+  const bf16_t* A = reinterpret_cast<const bf16_t*>(p.a);
+  const bf16_t* W = reinterpret_cast<const bf16_t*>(p.w);
+
+  const long long chunk = (total + kXcds - 1) / kXcds;
+  for (long long mine = blockIdx.x / kXcds;; mine += gridDim.x / kXcds) {
+    const long long it = xcd * chunk + mine;
+    if (mine >= chunk || it >= total) break;
+    __syncthreads();  // the item before is done with the LDS
+    const int g = entry_group(plan, p.E, static_cast<int>(it / n_tiles));
+    const Item item = place_item(it, plan.start, g, n_tiles, C::MT, plan.rows[g], true);
+    const long long row0 = static_cast<long long>(plan.lo[g]) + item.m0;
+    auto source = [&](int r) { return row0 + (r < item.rows ? r : item.rows - 1); };
+    ScaledCtx<C> c;
+    if (wm == 1) {
+#pragma unroll
+      for (int q = 0; q < C::LPW_A; ++q) {
+        const int j = wn * C::LPW_A + q;
+        c.t.src[q] = A + source(j * C::RPL + lrow) * kld + src_chunk<C>(lane, j);
+      }
+      if (lane < 32) {
+        c.scale = p.a_scale + source(32 * wn + lane) * nk;
+      } else {
+        int blk = item.n * 2 + (lane & 1);
+        blk = blk < nb ? blk : nb - 1;
+        c.scale = p.w_scale + (static_cast<long long>(g) * nb + blk) * nk;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < C::LPW_B; ++q) {
+        const int j = wn * C::LPW_B + q;
+        int col = item.n * NOUT + j * C::RPL + lrow;
+        col = col < p.N ? col : p.N - 1;
+        c.t.src[q] = W + (static_cast<long long>(g) * p.N + col) * kld + src_chunk<C>(lane, j);
+      }
+      c.scale = nullptr;
+    }
+    f32x16_t acc[C::BM][C::BN];
+#pragma unroll
+    for (int i = 0; i < C::BM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::BN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    const int nblk = (item.rows + 31) >> 5;
+    const int nv = min((nblk - wm + 1) >> 1, C::BM);
+    if (wm == 0) f8_kloop_nv<C, OUT_BF16, 0, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+    else f8_kloop_nv<C, OUT_BF16, 1, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+    wait_vm<0>();
+    __syncthreads();
+
+    // ---- epilogue: block (i, j) holds the transposed product: lane l -> tile
+    // row (2i + wm) * 32 + l % 32, registers 4q..4q+3 -> output columns
+    // 8q + 4 (l / 32) + 0..3 of column block j.  Staged: 16-byte chunk c of row r in
+    // slot c ^ (r % CPR) of the LDS tile.
+    constexpr int CPR = NOUT * OB / 16;
+    char* tile = reinterpret_cast<char*>(lds);
+#pragma unroll
+    for (int i = 0; i < C::BM; ++i) {
+      const int row = (2 * i + wm) * 32 + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < C::BN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = wn * 64 + j * 32 + 8 * q + 4 * (lane >> 5);
+          const float* v = reinterpret_cast<const float*>(&acc[i][j]) + 4 * q;
+          if constexpr (OUT_BF16) {
+            const uint32_t w0 = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+            const uint32_t w1 = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+            *reinterpret_cast<uint2*>(tile + row * NOUT * OB +
+                                      (((col >> 3) ^ (row & (CPR - 1))) << 4) + (col & 4) * 2) =
+                make_uint2(w0, w1);
+          } else {
+            *reinterpret_cast<float4*>(tile + row * NOUT * OB +
+                                       (((col >> 2) ^ (row & (CPR - 1))) << 4)) =
+                make_float4(v[0], v[1], v[2], v[3]);
+          }
+        }
+    }
+    __syncthreads();
+    constexpr int PER = 16 / OB;  // values of a chunk
+    const int col0 = item.n * NOUT;
+    const bool whole = p.N % PER == 0;  // rows of y start on 16 bytes
+    char* out = static_cast<char*>(p.out);
+    for (int ch0 = tid; ch0 < item.rows * CPR; ch0 += C::THREADS) {
+      const int row = ch0 / CPR, ch = ch0 % CPR;
+      const uint4 v = *reinterpret_cast<const uint4*>(tile + row * NOUT * OB +
+                                                      ((ch ^ (row & (CPR - 1))) << 4));
+      const int col = col0 + ch * PER;
+      char* o = out + ((row0 + row) * p.N + col) * OB;
+      if (whole) {
+        if (col < p.N) *reinterpret_cast<uint4*>(o) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          if (col + e >= p.N) break;
+          if (OUT_BF16) reinterpret_cast<bf16_t*>(o)[e] = static_cast<bf16_t>(w[e / 2] >> (16 * (e & 1)));
+          else reinterpret_cast<uint32_t*>(o)[e] = w[e % 4];
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st) {
+  const int grid = (device_cus_big() + kXcds - 1) / kXcds * kXcds;
+  if (a.out_bf16) gemm_fp8_big_kernel<MidF8, true><<<grid, MidF8::THREADS, 0, st>>>(a);
+  else gemm_fp8_big_kernel<MidF8, false><<<grid, MidF8::THREADS, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace moe
