@@ -34,6 +34,8 @@ enum class GatedPart { kForward, kDx, kDw };
 
 __device__ __forceinline__ float sigmoid(float a) { return 1.0f / (1.0f + expf(-a)); }
 
+// The kernel of one of the block's products.
+hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st);
 // Any sizes, either type, on the fp32 matrix cores (gated_tile.hip).
 hipError_t launch_gated_tile(const GatedArgs& a, GatedPart part, hipStream_t st);
 // pre, dh -> dau.

@@ -82,7 +82,7 @@ moe_status moe_gated_ff(const moe_gated_ff_desc* desc, const void* x, const void
     return MOE_ERR_UNSUPPORTED;
   a.h = h;
   a.pre = pre;
-  return hip_status(launch_gated_tile(a, GatedPart::kForward, stream));
+  return hip_status(launch_gated(a, GatedPart::kForward, stream));
 }
 
 moe_status moe_gated_ff_backward(const moe_gated_ff_desc* desc, const void* x, const void* w_gate,
@@ -116,12 +116,12 @@ moe_status moe_gated_ff_backward(const moe_gated_ff_desc* desc, const void* x, c
       a.pre = const_cast<float*>(pre);
     } else {
       // h is not wanted: the product runs again for a and u alone
-      e = launch_gated_tile(a, GatedPart::kForward, stream);
+      e = launch_gated(a, GatedPart::kForward, stream);
     }
     if (e == hipSuccess) e = launch_gated_dau(a, stream);
-    if (e == hipSuccess && dx) e = launch_gated_tile(a, GatedPart::kDx, stream);
+    if (e == hipSuccess && dx) e = launch_gated(a, GatedPart::kDx, stream);
   }
-  if (e == hipSuccess && dw_gate) e = launch_gated_tile(a, GatedPart::kDw, stream);
+  if (e == hipSuccess && dw_gate) e = launch_gated(a, GatedPart::kDw, stream);
   return hip_status(e);
 }
 

@@ -111,18 +111,31 @@ __device__ __forceinline__ void f8_step(const ScaledCtx<C>& c, int kt, int nk,
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): fragments in registers
   if constexpr (GRP == 1) wait_vm<(C::NSA - 2) * (C::LPW_A + 1)>();
   lds_barrier();
-  if constexpr (FAST) {
+  if constexpr (FAST && NV > 0) {
+    // block n's instructions between the two halves of block n - 1's additions, so
+    // that the matrix unit does not wait for the vector unit
+    constexpr int NBLK = NV * C::BN;
+    static_assert(H == 2, "two instructions a block");
+    f32x16_t p[2];
+    auto join = [&](int n, int r0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int r = r0; r < r0 + 8; ++r)
+        acc[n / C::BN][n % C::BN][r] = fmaf(p[n & 1][r], s[n / C::BN], acc[n / C::BN][n % C::BN][r]);
+    };
 #pragma unroll
-      for (int j = 0; j < C::BN; ++j) {
-        f32x16_t p = {};
-#pragma unroll
-        for (int h = 0; h < H; ++h) p = mul64(b[h][j], a[h][i], p);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(p[r], s[i], acc[i][j][r]);
-      }
-  } else {
+    for (int n = 0; n < NBLK; ++n) {
+      p[n & 1] = mul64(b[0][n % C::BN], a[0][n / C::BN], f32x16_t{});
+      __builtin_amdgcn_sched_barrier(0);
+      if (n > 0) join(n - 1, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      p[n & 1] = mul64(b[1][n % C::BN], a[1][n / C::BN], p[n & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (n > 0) join(n - 1, 8);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    join(NBLK - 1, 0);
+    join(NBLK - 1, 8);
+  } else if constexpr (NV > 0) {
     f32x16_t p[NM][C::BN] = {};
 #pragma unroll
     for (int h = 0; h < H; ++h)

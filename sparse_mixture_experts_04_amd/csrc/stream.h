@@ -1,0 +1,28 @@
+// Internal declarations of the stream kernel (few rows a group).
+#pragma once
+
+#include "common.h"
+#include "groups.h"
+
+namespace moe {
+
+enum class StreamKind { kFp8, kGatedBf16, kGatedF32 };
+
+struct StreamArgs {
+  const void* a;          // activations [M, K]
+  const void* w0;         // weights [E, N, K]; gated: Wg and Wu
+  const void* w1;
+  const float* a_scale;   // kFp8: [M, K / 128]
+  const float* w_scale;   // kFp8: [E, ceil(N / 128), K / 128]
+  const int32_t* offsets;
+  void* out;              // [M, N], null: not wanted (gated)
+  float* pre;             // gated: [M, 2N], null: not kept
+  int M, N, K, E;
+  static constexpr int S = 0, T = 0;
+  bool out_bf16;          // kFp8
+};
+
+// Rows of a and the weights start on 16 bytes and are a multiple of it long.
+hipError_t launch_stream(const StreamArgs& a, StreamKind kind, hipStream_t st);
+
+}  // namespace moe
