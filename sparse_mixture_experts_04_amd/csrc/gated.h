@@ -38,6 +38,8 @@ __device__ __forceinline__ float sigmoid(float a) { return 1.0f / (1.0f + expf(-
 hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st);
 // Any sizes, either type, on the fp32 matrix cores (gated_tile.hip).
 hipError_t launch_gated_tile(const GatedArgs& a, GatedPart part, hipStream_t st);
+// bf16 rows of 16-byte pieces, in tiles of 128 or 256 rows (gated_big.hip).
+hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, int rows, hipStream_t st);
 // pre, dh -> dau.
 hipError_t launch_gated_dau(const GatedArgs& a, hipStream_t st);
 

@@ -24,6 +24,13 @@ hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st) {
     s.E = a.E;
     return launch_stream(s, a.bf16 ? StreamKind::kGatedBf16 : StreamKind::kGatedF32, st);
   }
+  const bool out16 = part == GatedPart::kForward ? on16(a.h) && on16(a.pre)
+                     : part == GatedPart::kDx    ? on16(a.dx)
+                                                 : on16(a.dw_gate) && on16(a.dw_up);
+  if (a.bf16 && wide && a.F % 8 == 0 && out16) {
+    const long long mean = part == GatedPart::kDw ? a.F : a.M / a.E;
+    return launch_gated_big(a, part, mean > 160 ? 256 : 128, st);
+  }
   return launch_gated_tile(a, part, st);
 }
 
