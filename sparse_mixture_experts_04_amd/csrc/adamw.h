@@ -28,7 +28,7 @@ static_assert(sizeof(AdamwBatch) <= 3584, "kernel arguments");
 
 struct AdamwStep {
   double lr, beta1, beta2, eps, weight_decay;
-  int64_t step;
+  double c1, c2;   // 1 - beta^step, where the step is known to the host
   const float* lr_dev;
   const int64_t* step_dev;
   const float* grad_scale;

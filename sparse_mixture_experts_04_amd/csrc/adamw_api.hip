@@ -115,8 +115,17 @@ moe_status moe_adamw(const moe_adamw_desc* desc, const moe_adamw_step* step, int
   if (!on(table, 16) || !on(step->lr_dev, 4) || !on(step->step_dev, 8) ||
       !on(step->grad_scale_dev, 4))
     return MOE_ERR_UNSUPPORTED;
-  const AdamwStep s{step->lr,   step->beta1,  step->beta2,    step->eps, step->weight_decay,
-                    step->step, step->lr_dev, step->step_dev, step->grad_scale_dev};
+  const double t = static_cast<double>(step->step);
+  const AdamwStep s{step->lr,
+                    step->beta1,
+                    step->beta2,
+                    step->eps,
+                    step->weight_decay,
+                    1.0 - std::pow(step->beta1, t),
+                    1.0 - std::pow(step->beta2, t),
+                    step->lr_dev,
+                    step->step_dev,
+                    step->grad_scale_dev};
   return hip_status(launch_adamw(table_at(const_cast<void*>(table), desc->count), s, chunks,
                                  desc->param == MOE_BF16, desc->grad == MOE_BF16,
                                  desc->state_bits == 8, stream));
