@@ -12,6 +12,7 @@
 // (one value in some 10^5) the two candidates' midpoint m decides: m has 5
 // significant bits, and x - m s in one fused multiply-add has the exact sign.
 #include <cmath>
+#include <type_traits>
 
 #include "fp8.h"
 #include "int8_quant.h"
@@ -59,38 +60,60 @@ __device__ __forceinline__ float fp8_scale(uint32_t top, bool& live) {
   return live ? s : finite ? 0.0f : NAN;
 }
 
-// 16 lanes hold a block of a row, 8 values each.
-template <typename T, bool VEC>
+// Largest over the 8 lanes around a lane, without the LDS that a shuffle takes.
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+  auto step = [&](auto ctrl) {
+    const uint32_t u = __builtin_amdgcn_update_dpp(0u, v, decltype(ctrl)::value, 0xf, 0xf, true);
+    v = u > v ? u : v;
+  };
+  step(std::integral_constant<int, 0xb1>{});   // lanes 1 apart
+  step(std::integral_constant<int, 0x4e>{});   // 2
+  step(std::integral_constant<int, 0x141>{});  // 4 (mirrored eights)
+  return v;
+}
+
+// 8 lanes hold a block of a row, 16 values each: 16 bytes of codes a store.
+// WHOLE: K is a multiple of 128, the blocks of all rows follow each other, and no
+// thread has to find its row by a division.
+// Memory-bound: MEASURED
+template <typename T, bool VEC, bool WHOLE>
 __global__ __launch_bounds__(256) void quantize_fp8_kernel(const T* __restrict__ x, long long rows,
                                                            int K, int blocks,
                                                            uint8_t* __restrict__ codes,
                                                            float* __restrict__ scales) {
   const long long total = rows * blocks;
-  const int in = threadIdx.x & 15;
+  const int in = threadIdx.x & 7;
   // every lane of a wave takes part in the exchange, also past the end
-  for (long long b0 = static_cast<long long>(blockIdx.x) * 16; b0 < total;
-       b0 += static_cast<long long>(gridDim.x) * 16) {
-    const long long b = b0 + (threadIdx.x >> 4);
+  for (long long b0 = static_cast<long long>(blockIdx.x) * 32; b0 < total;
+       b0 += static_cast<long long>(gridDim.x) * 32) {
+    const long long b = b0 + (threadIdx.x >> 3);
     const bool mine = b < total;
-    const long long row = mine ? b / blocks : 0;
-    const int k = static_cast<int>(mine ? b - row * blocks : 0) * kFp8Block + in * 8;
-    float v[8] = {};
-    if (mine && k < K) {
-      uint4 h[sizeof(T) / 2];
-      hold8<T, VEC>(x + row * K + k, K - k, h);
-      values(h, v);
-    }
-    uint32_t top = max_bits(v, 0);
+    const long long row = WHOLE || !mine ? 0 : b / blocks;
+    const int k = WHOLE ? in * 16 : static_cast<int>(mine ? b - row * blocks : 0) * kFp8Block + in * 16;
+    const T* from = x + (WHOLE ? b * kFp8Block : row * K) + k;
+    float v[2][8] = {};
+    uint32_t top = 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      const uint32_t u = __shfl_xor(top, o);
-      top = u > top ? u : top;
+    for (int h = 0; h < 2; ++h) {
+      if (mine && (WHOLE || k + 8 * h < K)) {
+        uint4 w[sizeof(T) / 2];
+        hold8<T, VEC>(from + 8 * h, WHOLE ? 8 : K - k - 8 * h, w);
+        values(w, v[h]);
+      }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) top = max_bits(v[h], top);
+    top = max8(top);
     bool live;
     const float s = fp8_scale(top, live);
     if (!mine) continue;
-    *reinterpret_cast<uint2*>(codes + b * kFp8Block + in * 8) =
-        live ? fp8_pack(v, s, 1.0f / s) : make_uint2(0u, 0u);
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (live) {
+      const float inv = 1.0f / s;
+      const uint2 a = fp8_pack(v[0], s, inv), c = fp8_pack(v[1], s, inv);
+      w = make_uint4(a.x, a.y, c.x, c.y);
+    }
+    *reinterpret_cast<uint4*>(codes + b * kFp8Block + in * 16) = w;
     if (in == 0) scales[b] = s;
   }
 }
@@ -140,10 +163,11 @@ hipError_t run_rows(long long rows, int K, const T* x, uint8_t* codes, float* sc
                     hipStream_t st) {
   const bool vec = K % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
   const int blocks = static_cast<int>(fp8_row(K) / kFp8Block);
-  const long long want = (rows * blocks + 15) / 16;
+  const long long want = (rows * blocks + 31) / 32;
   const unsigned grid = static_cast<unsigned>(want < (1 << 20) ? want : (1 << 20));
-  if (vec) quantize_fp8_kernel<T, true><<<grid, 256, 0, st>>>(x, rows, K, blocks, codes, scales);
-  else quantize_fp8_kernel<T, false><<<grid, 256, 0, st>>>(x, rows, K, blocks, codes, scales);
+  auto go = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(x, rows, K, blocks, codes, scales); };
+  if (vec) K % kFp8Block == 0 ? go(quantize_fp8_kernel<T, true, true>) : go(quantize_fp8_kernel<T, true, false>);
+  else K % kFp8Block == 0 ? go(quantize_fp8_kernel<T, false, true>) : go(quantize_fp8_kernel<T, false, false>);
   return hipGetLastError();
 }
 
