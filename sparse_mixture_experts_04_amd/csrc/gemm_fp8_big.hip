@@ -17,17 +17,18 @@
 // step, 32 row scales and the two weight scales of the tile into the stage's slot by
 // one 4-byte direct-to-LDS load, so that no load of theirs disturbs the count of
 // loads in flight.
-#include "big_tile.h"
 #include "fp8.h"
+#include "tile_kt.h"
 
 namespace moe {
 
 namespace {
 
 using MidF8 = BigShape<128, 64, 3, 3>;
+using BigF8 = BigShape<256, 64, 2, 2>;
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kScaleSlot = 4 * 64;  // floats: 4 waves x (32 rows, 2 weight blocks, rest unused)
+constexpr int kScaleSlot = 8 * 64;  // floats: waves x (32 rows, 2 weight blocks, rest unused)
 
 // One direct global -> LDS load of 4 bytes a lane (dma16 has the why of the asm).
 __device__ __forceinline__ void dma4(const float* src, float* dst) {
@@ -39,10 +40,24 @@ __device__ __forceinline__ void dma4(const float* src, float* dst) {
                : "m0");
 }
 
+// The same from a wave-uniform base and a lane's offset in bytes (dma16_at).
+__device__ __forceinline__ void dma4_at(const float* base, uint32_t off, float* dst) {
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(dst))));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "m0");
+}
+
 // 64 codes of K; the fragment's pieces of K are the same ones for both operands.
 __device__ __forceinline__ f32x16_t mul64(i32x8_t b, i32x8_t a, f32x16_t c) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, 0, 0, 0);
 }
+
+// Has the sums made here and now: the compiler would put the additions off to the end
+// of the loop and keep every block's p in registers until then.
+__device__ __forceinline__ void pin(f32x16_t& v) { asm volatile("" : "+v"(v)); }
 
 // Eight codes of a fragment (words 2q and 2q + 1) as bf16, which holds every e4m3
 // value.
@@ -130,11 +145,15 @@ __device__ __forceinline__ void f8_step(const ScaledCtx<C>& c, int kt, int nk,
       __builtin_amdgcn_sched_barrier(0);
       p[n & 1] = mul64(b[1][n % C::BN], a[1][n / C::BN], p[n & 1]);
       __builtin_amdgcn_sched_barrier(0);
-      if (n > 0) join(n - 1, 8);
+      if (n > 0) {
+        join(n - 1, 8);
+        pin(acc[(n - 1) / C::BN][(n - 1) % C::BN]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     join(NBLK - 1, 0);
     join(NBLK - 1, 8);
+    pin(acc[NV - 1][C::BN - 1]);
   } else if constexpr (NV > 0) {
     f32x16_t p[NM][C::BN] = {};
 #pragma unroll
@@ -209,6 +228,135 @@ __device__ __forceinline__ void f8_kloop_nv(const ScaledCtx<C>& c, int nk,
   }
 }
 
+// ------------------------------------------------------------- 256-row tiles
+//
+// Twice the products for 4/3 of the 128-row tile's bytes.  Each wave owns 128 rows x
+// 64 columns and walks its four row blocks with two sets of fragments of A in turn;
+// two slots an operand, one barrier a step: behind it stage j is there (each wave has
+// waited for its own loads) and nobody reads stage j - 1 any more, whose slot takes
+// stage j + 1 while this one is multiplied.
+struct F8Loads {
+  const bf16_t* a;       // (all wave-uniform) tile's first row, first weight row
+  const bf16_t* b;
+  const float* a_scale;  // scales of the tile's first row
+  const float* w_scale;  // of this wave's 64 weight rows
+  int last_a, last_b;    // last row there is
+  uint32_t ld;           // bytes of a row
+};
+
+__device__ __forceinline__ float sload_f32(const float* p, int i) {
+  typedef const float __attribute__((address_space(4)))* scalar_f32;
+  return ((scalar_f32)p)[__builtin_amdgcn_readfirstlane(i)];
+}
+
+template <class C, int NV>
+__device__ __forceinline__ void f8b_kloop(const F8Loads& t, int nk, bf16_t* const (&sA)[2],
+                                          bf16_t* const (&sB)[2], float* const (&sS)[2], int wave,
+                                          int lane, f32x16_t (&acc)[C::BM][C::BN]) {
+  constexpr int BLK = 32 * C::BK, H = C::KK / 2;
+  static_assert(H == 2 && C::BM == 4 && C::BN == 2, "256 x 256, 128 codes");
+  const int r32 = lane & 31, wm = wave >> 2, wn = wave & 3;
+  // LDS addresses of this lane's pieces in slot 0, row block wm of A and column block
+  // 2 wn of B: what else an address has is a constant that the load instruction adds
+  typedef const bf16x8_t __attribute__((address_space(3)))* lds_piece;
+  uint32_t at_a[C::KK], at_b[C::KK];
+#pragma unroll
+  for (int kk = 0; kk < C::KK; ++kk) {
+    const uint32_t o = 2 * (r32 * C::BK + (((2 * kk + (lane >> 5)) ^ row_swz<C>(r32)) << 3));
+    at_a[kk] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(sA[0]))) + wm * BLK * 2 + o;
+    at_b[kk] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(sB[0]))) + wn * BLK * 4 + o;
+  }
+  auto frag = [&](const uint32_t (&at)[C::KK], uint32_t more, int h) __attribute__((always_inline)) {
+    union {
+      bf16x8_t half[2];
+      i32x8_t all;
+    } u;
+    u.half[0] = *(lds_piece)(at[2 * h] + more);
+    u.half[1] = *(lds_piece)(at[2 * h + 1] + more);
+    return u.all;
+  };
+  // Load q (0 to 8) of a stage.  Offsets are made where they are used (two
+  // instructions; nine registers would not fit): row 64 w' + 8 q + lane / 8 of an
+  // operand, chunk as src_chunk has it.
+  int lrow = wave * 32 + (lane >> 3);
+  const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  auto load = [&](int ks, int slot, int q) __attribute__((always_inline)) {
+    ks = ks < nk ? ks : nk - 1;  // past the end: again, into a slot nobody reads
+    if (q < 8) {
+      const int r = min(lrow + 8 * (q & 3), q < 4 ? t.last_a : t.last_b);
+      const uint32_t at = __umul24(r, t.ld) + (chunk ^ ((q & 1) << 4));
+      dma16_at((q < 4 ? t.a : t.b) + ks * C::BK, at,
+               (q < 4 ? sA[slot] : sB[slot]) + (wave * 4 + (q & 3)) * 512);
+    } else {
+      dma4_at(t.a_scale + ks, 4u * __umul24(min(wave * 32 + r32, t.last_a), nk),
+              sS[slot] + wave * 64);
+    }
+  };
+  float sw = sload_f32(t.w_scale, 0);
+  auto step = [&](int kt, int slot) __attribute__((always_inline)) {
+    i32x8_t b[H][2], a[2][H];
+    float s[2];
+    asm volatile("" : "+v"(lrow));  // (keeps the offsets from being made, and kept, before the loop)
+    wait_vm<0>();
+    lds_barrier();
+    auto read_a = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) a[i & 1][h] = frag(at_a, slot * C::A_STAGE * 2 + i * BLK * 4, h);
+      s[i & 1] = sS[slot][(2 * i + wm) * 64 + r32] * sw;
+    };
+    if (NV > 0) {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) b[h][j] = frag(at_b, slot * C::B_STAGE * 2 + j * BLK * 2, h);
+      read_a(0);
+    }
+    if (NV > 1) read_a(1);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      // (the other wave of the SIMD has the matrix unit while this one adds)
+      if (n < 2 * NV) {
+        f32x16_t p = mul64(b[0][n % 2], a[n / 2 & 1][0], f32x16_t{});
+        p = mul64(b[1][n % 2], a[n / 2 & 1][1], p);
+        __builtin_amdgcn_sched_barrier(0);
+        if (n < 3)
+#pragma unroll
+          for (int q = 3 * n; q < 3 * n + 3; ++q) load(kt + 1, slot ^ 1, q);
+        // the fragments of the row block before are used up: those of the next one
+        if (n % 2 == 0 && n > 0 && n / 2 + 1 < NV) read_a(n / 2 + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[n / 2][n % 2][r] = fmaf(p[r], s[n / 2 & 1], acc[n / 2][n % 2][r]);
+        pin(acc[n / 2][n % 2]);
+        __builtin_amdgcn_sched_barrier(0);
+      } else if (n < 3) {
+#pragma unroll
+        for (int q = 3 * n; q < 3 * n + 3; ++q) load(kt + 1, slot ^ 1, q);
+      }
+    }
+    sw = sload_f32(t.w_scale, kt + 1 < nk ? kt + 1 : kt);
+  };
+#pragma unroll
+  for (int q = 0; q < 9; ++q) load(0, 0, q);
+  for (int kt = 0; kt < nk; kt += 2) {
+    step(kt, 0);
+    if (kt + 1 < nk) step(kt + 1, 1);
+  }
+}
+
+template <class C, int NV>
+__device__ __forceinline__ void f8b_kloop_nv(const F8Loads& t, int nk, bf16_t* const (&sA)[2],
+                                             bf16_t* const (&sB)[2], float* const (&sS)[2],
+                                             int wave, int lane, int nv,
+                                             f32x16_t (&acc)[C::BM][C::BN]) {
+  if constexpr (NV == 0) {
+    f8b_kloop<C, 0>(t, nk, sA, sB, sS, wave, lane, acc);
+  } else {
+    if (nv == NV) f8b_kloop<C, NV>(t, nk, sA, sB, sS, wave, lane, acc);
+    else f8b_kloop_nv<C, NV - 1>(t, nk, sA, sB, sS, wave, lane, nv, acc);
+  }
+}
+
 template <class C, bool OUT_BF16>
 __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
   __shared__ __attribute__((aligned(1024))) bf16_t lds[C::LDS_ELEMS];
@@ -242,34 +390,15 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
     const long long it = xcd * chunk + mine;
     if (mine >= chunk || it >= total) break;
     __syncthreads();  // the item before is done with the LDS
-    const int g = entry_group(plan, p.E, static_cast<int>(it / n_tiles));
-    const Item item = place_item(it, plan.start, g, n_tiles, C::MT, plan.rows[g], true);
-    const long long row0 = static_cast<long long>(plan.lo[g]) + item.m0;
+    // (uniform, but read from LDS: tell the compiler)
+    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    const int g = uni(entry_group(plan, p.E, static_cast<int>(it / n_tiles)));
+    Item item = place_item(it, plan.start, g, n_tiles, C::MT, plan.rows[g], true);
+    item.m0 = uni(item.m0);
+    item.rows = uni(item.rows);
+    item.n = uni(item.n);
+    const long long row0 = static_cast<long long>(uni(plan.lo[g])) + item.m0;
     auto source = [&](int r) { return row0 + (r < item.rows ? r : item.rows - 1); };
-    ScaledCtx<C> c;
-    if (wm == 1) {
-#pragma unroll
-      for (int q = 0; q < C::LPW_A; ++q) {
-        const int j = wn * C::LPW_A + q;
-        c.t.src[q] = A + source(j * C::RPL + lrow) * kld + src_chunk<C>(lane, j);
-      }
-      if (lane < 32) {
-        c.scale = p.a_scale + source(32 * wn + lane) * nk;
-      } else {
-        int blk = item.n * 2 + (lane & 1);
-        blk = blk < nb ? blk : nb - 1;
-        c.scale = p.w_scale + (static_cast<long long>(g) * nb + blk) * nk;
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < C::LPW_B; ++q) {
-        const int j = wn * C::LPW_B + q;
-        int col = item.n * NOUT + j * C::RPL + lrow;
-        col = col < p.N ? col : p.N - 1;
-        c.t.src[q] = W + (static_cast<long long>(g) * p.N + col) * kld + src_chunk<C>(lane, j);
-      }
-      c.scale = nullptr;
-    }
     f32x16_t acc[C::BM][C::BN];
 #pragma unroll
     for (int i = 0; i < C::BM; ++i)
@@ -279,8 +408,41 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     const int nblk = (item.rows + 31) >> 5;
     const int nv = min((nblk - wm + 1) >> 1, C::BM);
-    if (wm == 0) f8_kloop_nv<C, OUT_BF16, 0, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
-    else f8_kloop_nv<C, OUT_BF16, 1, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+    const float* wscale = p.w_scale + static_cast<long long>(g) * nb * nk;
+    if constexpr (C::MT == 256) {
+      F8Loads t;
+      t.a = A + row0 * kld;
+      t.b = W + (static_cast<long long>(g) * p.N + item.n * NOUT) * kld;
+      t.a_scale = p.a_scale + row0 * nk;
+      t.w_scale = wscale + static_cast<long long>(min(item.n * 2 + (wn >> 1), nb - 1)) * nk;
+      t.last_a = item.rows - 1;
+      t.last_b = p.N - 1 - item.n * NOUT;
+      t.ld = p.Kp;
+      float* const scales[2] = {sS, sS + kScaleSlot};
+      f8b_kloop_nv<C, C::BM>(t, nk, sA, sB, scales, wave, lane, nv, acc);
+    } else {
+      ScaledCtx<C> c;
+      if (wm == 1) {
+#pragma unroll
+        for (int q = 0; q < C::LPW_A; ++q) {
+          const int j = wn * C::LPW_A + q;
+          c.t.src[q] = A + source(j * C::RPL + lrow) * kld + src_chunk<C>(lane, j);
+        }
+        c.scale = lane < 32 ? p.a_scale + source(32 * wn + lane) * nk
+                            : wscale + static_cast<long long>(min(item.n * 2 + (lane & 1), nb - 1)) * nk;
+      } else {
+#pragma unroll
+        for (int q = 0; q < C::LPW_B; ++q) {
+          const int j = wn * C::LPW_B + q;
+          int col = item.n * NOUT + j * C::RPL + lrow;
+          col = col < p.N ? col : p.N - 1;
+          c.t.src[q] = W + (static_cast<long long>(g) * p.N + col) * kld + src_chunk<C>(lane, j);
+        }
+        c.scale = nullptr;
+      }
+      if (wm == 0) f8_kloop_nv<C, OUT_BF16, 0, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+      else f8_kloop_nv<C, OUT_BF16, 1, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+    }
     wait_vm<0>();
     __syncthreads();
 
@@ -342,8 +504,9 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
 
 hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st) {
   const int grid = (device_cus_big() + kXcds - 1) / kXcds * kXcds;
-  if (a.out_bf16) gemm_fp8_big_kernel<MidF8, true><<<grid, MidF8::THREADS, 0, st>>>(a);
-  else gemm_fp8_big_kernel<MidF8, false><<<grid, MidF8::THREADS, 0, st>>>(a);
+  if (!a.out_bf16) gemm_fp8_big_kernel<MidF8, false><<<grid, MidF8::THREADS, 0, st>>>(a);
+  else if (a.M / a.E >= 160) gemm_fp8_big_kernel<BigF8, true><<<grid, BigF8::THREADS, 0, st>>>(a);
+  else gemm_fp8_big_kernel<MidF8, true><<<grid, MidF8::THREADS, 0, st>>>(a);
   return hipGetLastError();
 }
 
