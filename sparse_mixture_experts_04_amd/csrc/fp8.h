@@ -26,10 +26,15 @@ struct Fp8Args {
   const float* w_scale;   // [E, ceil(N / 128), Kp / 128]
   const int32_t* offsets;
   void* out;              // [M, N]
+  float* part;            // [splits, M, N]
   int M, N, Kp, E;
   static constexpr int S = 0, T = 0;
+  int splits;             // slices of K (fp8_splits)
   bool out_bf16;
 };
+// Whether a product goes through the stream of its weights (stream.hip).
+bool fp8_streams(int M, int N, int Kp, int E);
+int fp8_splits(int M, int N, int Kp, int E);
 hipError_t launch_gemm_fp8(const Fp8Args& a, hipStream_t st);
 hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st);
 

@@ -29,6 +29,18 @@ moe_status check_gemm(const moe_gemm_fp8_desc* d) {
   return MOE_OK;
 }
 
+// Slices of K whose sums the workspace holds (1: none).
+int slices(const moe_gemm_fp8_desc* d) {
+  const int kp = static_cast<int>(fp8_row(d->K));
+  return d->M == 0 || d->N == 0 || fp8_streams(d->M, d->N, kp, d->E)
+             ? 1
+             : fp8_splits(d->M, d->N, kp, d->E);
+}
+size_t ws_bytes_of(const moe_gemm_fp8_desc* d) {
+  const int s = slices(d);
+  return s > 1 ? static_cast<size_t>(s) * d->M * d->N * sizeof(float) : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -63,7 +75,7 @@ moe_status moe_gemm_fp8_workspace_size(const moe_gemm_fp8_desc* desc, size_t* by
   if (!bytes) return MOE_ERR_NULL;
   const moe_status st = check_gemm(desc);
   if (st != MOE_OK) return st;
-  *bytes = 0;
+  *bytes = ws_bytes_of(desc);
   return MOE_OK;
 }
 
@@ -77,7 +89,12 @@ moe_status moe_gemm_fp8(const moe_gemm_fp8_desc* desc, const uint8_t* a, const f
   if (!aligned16(a) || !aligned16(w) || !aligned16(y) || !aligned4(a_scale) ||
       !aligned4(w_scale) || !aligned4(offsets))
     return MOE_ERR_UNSUPPORTED;
+  const size_t need = ws_bytes_of(desc);
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
   Fp8Args g{};
+  g.part = static_cast<float*>(ws);
+  g.splits = slices(desc);
   g.a = a;
   g.a_scale = a_scale;
   g.w = w;

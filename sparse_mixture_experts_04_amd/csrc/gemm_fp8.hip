@@ -4,8 +4,10 @@
 
 namespace moe {
 
+bool fp8_streams(int M, int N, int Kp, int E) { return E == 1 ? M <= 16 : M / E < 1; }
+
 hipError_t launch_gemm_fp8(const Fp8Args& a, hipStream_t st) {
-  if (a.M / a.E >= 24) return launch_gemm_fp8_big(a, st);
+  if (!fp8_streams(a.M, a.N, a.Kp, a.E)) return launch_gemm_fp8_big(a, st);
   StreamArgs s{};
   s.a = a.a;
   s.w0 = a.w;

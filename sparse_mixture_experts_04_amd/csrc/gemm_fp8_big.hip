@@ -17,6 +17,8 @@
 // step, 32 row scales and the two weight scales of the tile into the stage's slot by
 // one 4-byte direct-to-LDS load, so that no load of theirs disturbs the count of
 // loads in flight.
+#include <cmath>
+
 #include "fp8.h"
 #include "tile_kt.h"
 
@@ -30,26 +32,6 @@ typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kScaleSlot = 8 * 64;  // floats: waves x (32 rows, 2 weight blocks, rest unused)
 
-// One direct global -> LDS load of 4 bytes a lane (dma16 has the why of the asm).
-__device__ __forceinline__ void dma4(const float* src, float* dst) {
-  const uint32_t lds = __builtin_amdgcn_readfirstlane(
-      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(dst))));
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
-               :
-               : "v"(src), "s"(lds)
-               : "m0");
-}
-
-// The same from a wave-uniform base and a lane's offset in bytes (dma16_at).
-__device__ __forceinline__ void dma4_at(const float* base, uint32_t off, float* dst) {
-  const uint32_t lds = __builtin_amdgcn_readfirstlane(
-      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(dst))));
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-               :
-               : "v"(off), "s"(base), "s"(lds)
-               : "m0");
-}
-
 // 64 codes of K; the fragment's pieces of K are the same ones for both operands.
 __device__ __forceinline__ f32x16_t mul64(i32x8_t b, i32x8_t a, f32x16_t c) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, 0, 0, 0);
@@ -57,7 +39,14 @@ __device__ __forceinline__ f32x16_t mul64(i32x8_t b, i32x8_t a, f32x16_t c) {
 
 // Has the sums made here and now: the compiler would put the additions off to the end
 // of the loop and keep every block's p in registers until then.
-__device__ __forceinline__ void pin(f32x16_t& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void pin(f32x16_t& v) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float x = v[r];
+    asm volatile("" : "+v"(x));
+    v[r] = x;
+  }
+}
 
 // Eight codes of a fragment (words 2q and 2q + 1) as bf16, which holds every e4m3
 // value.
@@ -75,14 +64,24 @@ __device__ __forceinline__ bf16x8_t wide8(i32x8_t f, int q) {
   return u.all;
 }
 
+// The loads of a wave of the 128-row tiles: B's for group 0, A's and the scales' for
+// group 1, from a wave-uniform base.
 template <class C>
-struct ScaledCtx {
-  BigCtx<C> t;
-  const float* scale;  // this lane's scale of step 0 (activation group)
+struct MidLoads {
+  const bf16_t* base;
+  uint32_t off[C::LPW_MAX];  // bytes from it to this lane's source of each load
+  const float* scale;        // this lane's scale of step 0 (activation group)
+
+  template <int L>
+  __device__ __forceinline__ void issue(int ks, uint32_t slot, int wig) const {
+#pragma unroll
+    for (int q = 0; q < L; ++q)
+      dma16_at(base + ks * C::BK, off[q], slot + (wig * L + q) * 1024);
+  }
 };
 
 template <class C, bool FAST, int U, int GRP, int NV>
-__device__ __forceinline__ void f8_step(const ScaledCtx<C>& c, int kt, int nk,
+__device__ __forceinline__ void f8_step(const MidLoads<C>& c, uint32_t lds, uint32_t scales, int kt, int nk,
                                         bf16_t* const (&sA)[C::NSA], bf16_t* const (&sB)[C::NSB],
                                         float* sS, int wig, int lane, const int (&off)[C::KK],
                                         f32x16_t (&acc)[C::BM][C::BN]) {
@@ -117,11 +116,11 @@ __device__ __forceinline__ void f8_step(const ScaledCtx<C>& c, int kt, int nk,
   for (int i = 0; i < NV; ++i) s[i] = ps[(2 * i + GRP) * 64 + (lane & 31)] * sw;
   if constexpr (GRP == 0) {
     const int ks = kt + C::NSB - 1 < nk ? kt + C::NSB - 1 : nk - 1;
-    c.t.template issue<C::LPW_B>(ks * C::BK, sB[(U + C::NSB - 1) % C::NSB], wig);
+    c.template issue<C::LPW_B>(ks, slot_b<C>(lds, (U + C::NSB - 1) % C::NSB), wig);
   } else {
     const int ks = kt + C::NSA - 1 < nk ? kt + C::NSA - 1 : nk - 1;
-    c.t.template issue<C::LPW_A>(ks * C::BK, sA[(U + C::NSA - 1) % C::NSA], wig);
-    dma4(c.scale + ks, sS + (U + C::NSA - 1) % C::NSA * kScaleSlot + wig * 64);
+    c.template issue<C::LPW_A>(ks, slot_a<C>(lds, (U + C::NSA - 1) % C::NSA), wig);
+    dma4_to(c.scale + ks, scales + ((U + C::NSA - 1) % C::NSA * kScaleSlot + wig * 64) * 4);
   }
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): fragments in registers
   if constexpr (GRP == 1) wait_vm<(C::NSA - 2) * (C::LPW_A + 1)>();
@@ -155,35 +154,34 @@ __device__ __forceinline__ void f8_step(const ScaledCtx<C>& c, int kt, int nk,
     join(NBLK - 1, 8);
     pin(acc[NV - 1][C::BN - 1]);
   } else if constexpr (NV > 0) {
-    f32x16_t p[NM][C::BN] = {};
+    // a column block at a time (both at once do not fit in the registers)
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+    for (int j = 0; j < C::BN; ++j) {
+      f32x16_t p[NM] = {};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bf16x8_t wb[C::BN];
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int j = 0; j < C::BN; ++j) wb[j] = wide8(b[h][j], q);
+        for (int q = 0; q < 4; ++q) {
+          const bf16x8_t wb = wide8(b[h][j], q);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const bf16x8_t wa = wide8(a[h][i], q);
-#pragma unroll
-          for (int j = 0; j < C::BN; ++j)
-            p[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa, p[i][j], 0, 0, 0);
+          for (int i = 0; i < NV; ++i)
+            p[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb, wide8(a[h][i], q), p[i], 0, 0, 0);
         }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(p[i][r], s[i], acc[i][j][r]);
+        pin(acc[i][j]);
       }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < C::BN; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(p[i][j][r], s[i], acc[i][j][r]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   if constexpr (GRP == 0) wait_vm<(C::NSB - 2) * C::LPW_B>();
   lds_barrier();
 }
 
 template <class C, bool FAST, int GRP, int NV>
-__device__ __forceinline__ void f8_kloop(const ScaledCtx<C>& c, int nk,
+__device__ __forceinline__ void f8_kloop(const MidLoads<C>& c, uint32_t lds, uint32_t scales, int nk,
                                          bf16_t* const (&sA)[C::NSA],
                                          bf16_t* const (&sB)[C::NSB], float* sS, int wave,
                                          int lane, f32x16_t (&acc)[C::BM][C::BN]) {
@@ -197,10 +195,10 @@ __device__ __forceinline__ void f8_kloop(const ScaledCtx<C>& c, int nk,
   for (int s = 0; s < 2; ++s) {
     const int ks = s < nk ? s : nk - 1;
     if constexpr (GRP == 0) {
-      c.t.template issue<C::LPW_B>(ks * C::BK, sB[s], wig);
+      c.template issue<C::LPW_B>(ks, slot_b<C>(lds, s), wig);
     } else {
-      c.t.template issue<C::LPW_A>(ks * C::BK, sA[s], wig);
-      dma4(c.scale + ks, sS + s * kScaleSlot + wig * 64);
+      c.template issue<C::LPW_A>(ks, slot_a<C>(lds, s), wig);
+      dma4_to(c.scale + ks, scales + (s * kScaleSlot + wig * 64) * 4);
     }
   }
   if constexpr (GRP == 0) wait_vm<C::LPW_B>();
@@ -208,23 +206,23 @@ __device__ __forceinline__ void f8_kloop(const ScaledCtx<C>& c, int nk,
   lds_barrier();                // point 0: stage 0 complete
   if (GRP == 1) lds_barrier();  // point 1 for group 1
   for (int kt = 0; kt < nk; kt += 3) {
-    f8_step<C, FAST, 0, GRP, NV>(c, kt, nk, sA, sB, sS, wig, lane, off, acc);
-    if (kt + 1 < nk) f8_step<C, FAST, 1, GRP, NV>(c, kt + 1, nk, sA, sB, sS, wig, lane, off, acc);
-    if (kt + 2 < nk) f8_step<C, FAST, 2, GRP, NV>(c, kt + 2, nk, sA, sB, sS, wig, lane, off, acc);
+    f8_step<C, FAST, 0, GRP, NV>(c, lds, scales, kt, nk, sA, sB, sS, wig, lane, off, acc);
+    if (kt + 1 < nk) f8_step<C, FAST, 1, GRP, NV>(c, lds, scales, kt + 1, nk, sA, sB, sS, wig, lane, off, acc);
+    if (kt + 2 < nk) f8_step<C, FAST, 2, GRP, NV>(c, lds, scales, kt + 2, nk, sA, sB, sS, wig, lane, off, acc);
   }
   if (GRP == 0) lds_barrier();
 }
 
 template <class C, bool FAST, int GRP, int NV>
-__device__ __forceinline__ void f8_kloop_nv(const ScaledCtx<C>& c, int nk,
+__device__ __forceinline__ void f8_kloop_nv(const MidLoads<C>& c, uint32_t lds, uint32_t scales, int nk,
                                             bf16_t* const (&sA)[C::NSA],
                                             bf16_t* const (&sB)[C::NSB], float* sS, int wave,
                                             int lane, int nv, f32x16_t (&acc)[C::BM][C::BN]) {
   if constexpr (NV == 0) {
-    f8_kloop<C, FAST, GRP, 0>(c, nk, sA, sB, sS, wave, lane, acc);
+    f8_kloop<C, FAST, GRP, 0>(c, lds, scales, nk, sA, sB, sS, wave, lane, acc);
   } else {
-    if (nv == NV) f8_kloop<C, FAST, GRP, NV>(c, nk, sA, sB, sS, wave, lane, acc);
-    else f8_kloop_nv<C, FAST, GRP, NV - 1>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+    if (nv == NV) f8_kloop<C, FAST, GRP, NV>(c, lds, scales, nk, sA, sB, sS, wave, lane, acc);
+    else f8_kloop_nv<C, FAST, GRP, NV - 1>(c, lds, scales, nk, sA, sB, sS, wave, lane, nv, acc);
   }
 }
 
@@ -250,9 +248,9 @@ __device__ __forceinline__ float sload_f32(const float* p, int i) {
 }
 
 template <class C, int NV>
-__device__ __forceinline__ void f8b_kloop(const F8Loads& t, int nk, bf16_t* const (&sA)[2],
-                                          bf16_t* const (&sB)[2], float* const (&sS)[2], int wave,
-                                          int lane, f32x16_t (&acc)[C::BM][C::BN]) {
+__device__ __forceinline__ void f8b_kloop(const F8Loads& t, int nk, uint32_t lds,
+                                          uint32_t scales, const float* sS, int wave, int lane,
+                                          f32x16_t (&acc)[C::BM][C::BN]) {
   constexpr int BLK = 32 * C::BK, H = C::KK / 2;
   static_assert(H == 2 && C::BM == 4 && C::BN == 2, "256 x 256, 128 codes");
   const int r32 = lane & 31, wm = wave >> 2, wn = wave & 3;
@@ -263,8 +261,8 @@ __device__ __forceinline__ void f8b_kloop(const F8Loads& t, int nk, bf16_t* cons
 #pragma unroll
   for (int kk = 0; kk < C::KK; ++kk) {
     const uint32_t o = 2 * (r32 * C::BK + (((2 * kk + (lane >> 5)) ^ row_swz<C>(r32)) << 3));
-    at_a[kk] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(sA[0]))) + wm * BLK * 2 + o;
-    at_b[kk] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(sB[0]))) + wn * BLK * 4 + o;
+    at_a[kk] = slot_a<C>(lds, 0) + wm * BLK * 2 + o;
+    at_b[kk] = slot_b<C>(lds, 0) + wn * BLK * 4 + o;
   }
   auto frag = [&](const uint32_t (&at)[C::KK], uint32_t more, int h) __attribute__((always_inline)) {
     union {
@@ -286,10 +284,10 @@ __device__ __forceinline__ void f8b_kloop(const F8Loads& t, int nk, bf16_t* cons
       const int r = min(lrow + 8 * (q & 3), q < 4 ? t.last_a : t.last_b);
       const uint32_t at = __umul24(r, t.ld) + (chunk ^ ((q & 1) << 4));
       dma16_at((q < 4 ? t.a : t.b) + ks * C::BK, at,
-               (q < 4 ? sA[slot] : sB[slot]) + (wave * 4 + (q & 3)) * 512);
+               (q < 4 ? slot_a<C>(lds, slot) : slot_b<C>(lds, slot)) + (wave * 4 + (q & 3)) * 1024);
     } else {
       dma4_at(t.a_scale + ks, 4u * __umul24(min(wave * 32 + r32, t.last_a), nk),
-              sS[slot] + wave * 64);
+              scales + (slot * kScaleSlot + wave * 64) * 4);
     }
   };
   float sw = sload_f32(t.w_scale, 0);
@@ -302,7 +300,7 @@ __device__ __forceinline__ void f8b_kloop(const F8Loads& t, int nk, bf16_t* cons
     auto read_a = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int h = 0; h < H; ++h) a[i & 1][h] = frag(at_a, slot * C::A_STAGE * 2 + i * BLK * 4, h);
-      s[i & 1] = sS[slot][(2 * i + wm) * 64 + r32] * sw;
+      s[i & 1] = sS[slot * kScaleSlot + (2 * i + wm) * 64 + r32] * sw;
     };
     if (NV > 0) {
 #pragma unroll
@@ -345,19 +343,20 @@ __device__ __forceinline__ void f8b_kloop(const F8Loads& t, int nk, bf16_t* cons
 }
 
 template <class C, int NV>
-__device__ __forceinline__ void f8b_kloop_nv(const F8Loads& t, int nk, bf16_t* const (&sA)[2],
-                                             bf16_t* const (&sB)[2], float* const (&sS)[2],
-                                             int wave, int lane, int nv,
-                                             f32x16_t (&acc)[C::BM][C::BN]) {
+__device__ __forceinline__ void f8b_kloop_nv(const F8Loads& t, int nk, uint32_t lds,
+                                             uint32_t scales, const float* sS, int wave, int lane,
+                                             int nv, f32x16_t (&acc)[C::BM][C::BN]) {
   if constexpr (NV == 0) {
-    f8b_kloop<C, 0>(t, nk, sA, sB, sS, wave, lane, acc);
+    f8b_kloop<C, 0>(t, nk, lds, scales, sS, wave, lane, acc);
   } else {
-    if (nv == NV) f8b_kloop<C, NV>(t, nk, sA, sB, sS, wave, lane, acc);
-    else f8b_kloop_nv<C, NV - 1>(t, nk, sA, sB, sS, wave, lane, nv, acc);
+    if (nv == NV) f8b_kloop<C, NV>(t, nk, lds, scales, sS, wave, lane, acc);
+    else f8b_kloop_nv<C, NV - 1>(t, nk, lds, scales, sS, wave, lane, nv, acc);
   }
 }
 
-template <class C, bool OUT_BF16>
+// FAST: the e4m3 instruction (see above).  SPLIT: K is cut into p.splits slices, each
+// an item of its own, whose fp32 sums go to slice s of p.part [splits, M, N].
+template <class C, bool FAST, bool OUT_BF16, bool SPLIT = false>
 __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
   __shared__ __attribute__((aligned(1024))) bf16_t lds[C::LDS_ELEMS];
   __shared__ __attribute__((aligned(256))) float sS[C::NSA * kScaleSlot];
@@ -377,19 +376,24 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
   const int wm = wave >> 2, wn = wave & 3;
   make_entries<C::THREADS, C::MT>(p, plan);
   const int n_tiles = (p.N + NOUT - 1) / NOUT, nb = (p.N + kFp8Block - 1) / kFp8Block;
-  const long long total = static_cast<long long>(plan.start[p.E]) * n_tiles;
+  const int splits = SPLIT ? p.splits : 1;
+  const long long total = static_cast<long long>(plan.start[p.E]) * n_tiles * splits;
   const int xcd = blockIdx.x % kXcds;
   const int kld = p.Kp / 2;  // row length in 16-bit units
-  const int nk = p.Kp / kFp8Block;
+  const int kb = p.Kp / kFp8Block;
   const int lrow = lane / C::CPR;
   const bf16_t* A = reinterpret_cast<const bf16_t*>(p.a);
   const bf16_t* W = reinterpret_cast<const bf16_t*>(p.w);
 
   const long long chunk = (total + kXcds - 1) / kXcds;
   for (long long mine = blockIdx.x / kXcds;; mine += gridDim.x / kXcds) {
-    const long long it = xcd * chunk + mine;
-    if (mine >= chunk || it >= total) break;
+    const long long turn = xcd * chunk + mine;
+    if (mine >= chunk || turn >= total) break;
     __syncthreads();  // the item before is done with the LDS
+    const long long it = SPLIT ? turn / splits : turn;
+    const int slice = SPLIT ? static_cast<int>(turn % splits) : 0;
+    const int k0 = SPLIT ? kb * slice / splits : 0;                // first step
+    const int nk = SPLIT ? kb * (slice + 1) / splits - k0 : kb;    // and how many
     // (uniform, but read from LDS: tell the compiler)
     auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     const int g = uni(entry_group(plan, p.E, static_cast<int>(it / n_tiles)));
@@ -408,40 +412,33 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     const int nblk = (item.rows + 31) >> 5;
     const int nv = min((nblk - wm + 1) >> 1, C::BM);
-    const float* wscale = p.w_scale + static_cast<long long>(g) * nb * nk;
+    const float* wscale = p.w_scale + static_cast<long long>(g) * nb * kb + k0;
     if constexpr (C::MT == 256) {
+      static_assert(!SPLIT, "128-row tiles");
       F8Loads t;
       t.a = A + row0 * kld;
       t.b = W + (static_cast<long long>(g) * p.N + item.n * NOUT) * kld;
-      t.a_scale = p.a_scale + row0 * nk;
-      t.w_scale = wscale + static_cast<long long>(min(item.n * 2 + (wn >> 1), nb - 1)) * nk;
+      t.a_scale = p.a_scale + row0 * kb;
+      t.w_scale = wscale + static_cast<long long>(min(item.n * 2 + (wn >> 1), nb - 1)) * kb;
       t.last_a = item.rows - 1;
       t.last_b = p.N - 1 - item.n * NOUT;
       t.ld = p.Kp;
-      float* const scales[2] = {sS, sS + kScaleSlot};
-      f8b_kloop_nv<C, C::BM>(t, nk, sA, sB, scales, wave, lane, nv, acc);
+      f8b_kloop_nv<C, C::BM>(t, nk, lds_address(lds), lds_address(sS), sS, wave, lane, nv, acc);
     } else {
-      ScaledCtx<C> c;
-      if (wm == 1) {
+      MidLoads<C> c;
+      c.base = (wm == 1 ? A + row0 * kld
+                        : W + (static_cast<long long>(g) * p.N + item.n * NOUT) * kld) + k0 * C::BK;
+      const int last = wm == 1 ? item.rows - 1 : p.N - 1 - item.n * NOUT;
 #pragma unroll
-        for (int q = 0; q < C::LPW_A; ++q) {
-          const int j = wn * C::LPW_A + q;
-          c.t.src[q] = A + source(j * C::RPL + lrow) * kld + src_chunk<C>(lane, j);
-        }
-        c.scale = lane < 32 ? p.a_scale + source(32 * wn + lane) * nk
-                            : wscale + static_cast<long long>(min(item.n * 2 + (lane & 1), nb - 1)) * nk;
-      } else {
-#pragma unroll
-        for (int q = 0; q < C::LPW_B; ++q) {
-          const int j = wn * C::LPW_B + q;
-          int col = item.n * NOUT + j * C::RPL + lrow;
-          col = col < p.N ? col : p.N - 1;
-          c.t.src[q] = W + (static_cast<long long>(g) * p.N + col) * kld + src_chunk<C>(lane, j);
-        }
-        c.scale = nullptr;
+      for (int q = 0; q < C::LPW_MAX; ++q) {
+        const int j = wn * (wm == 1 ? C::LPW_A : C::LPW_B) + q;
+        c.off[q] = 2u * (static_cast<uint32_t>(min(j * C::RPL + lrow, last)) * kld +
+                         src_chunk<C>(lane, j));
       }
-      if (wm == 0) f8_kloop_nv<C, OUT_BF16, 0, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
-      else f8_kloop_nv<C, OUT_BF16, 1, C::BM>(c, nk, sA, sB, sS, wave, lane, nv, acc);
+      c.scale = lane < 32 ? p.a_scale + source(32 * wn + lane) * kb + k0
+                          : wscale + static_cast<long long>(min(item.n * 2 + (lane & 1), nb - 1)) * kb;
+      if (wm == 0) f8_kloop_nv<C, FAST, 0, C::BM>(c, lds_address(lds), lds_address(sS), nk, sA, sB, sS, wave, lane, nv, acc);
+      else f8_kloop_nv<C, FAST, 1, C::BM>(c, lds_address(lds), lds_address(sS), nk, sA, sB, sS, wave, lane, nv, acc);
     }
     wait_vm<0>();
     __syncthreads();
@@ -478,7 +475,8 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
     constexpr int PER = 16 / OB;  // values of a chunk
     const int col0 = item.n * NOUT;
     const bool whole = p.N % PER == 0;  // rows of y start on 16 bytes
-    char* out = static_cast<char*>(p.out);
+    char* out = SPLIT ? reinterpret_cast<char*>(p.part + static_cast<size_t>(slice) * p.M * p.N)
+                      : static_cast<char*>(p.out);
     for (int ch0 = tid; ch0 < item.rows * CPR; ch0 += C::THREADS) {
       const int row = ch0 / CPR, ch = ch0 % CPR;
       const uint4 v = *reinterpret_cast<const uint4*>(tile + row * NOUT * OB +
@@ -500,13 +498,77 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
   }
 }
 
+// y from the slices' sums, in order; a thread per 4 values (VEC: N a multiple of 4).
+// Rows outside the one group keep what y held.
+template <bool VEC>
+__global__ __launch_bounds__(256) void gemm_fp8_reduce_kernel(Fp8Args p) {
+  long long first = 0, last = p.M;
+  if (p.offsets) {
+    first = clampi(p.offsets[0], 0, p.M);
+    last = clampi(p.offsets[1], 0, p.M);
+  }
+  const long long n = static_cast<long long>(p.M) * p.N, end = last * p.N;
+  constexpr int PER = VEC ? 4 : 1;
+  for (long long i = first * p.N + (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * PER;
+       i < end; i += static_cast<long long>(gridDim.x) * 256 * PER) {
+    float v[PER] = {};
+    for (int s = 0; s < p.splits; ++s) {
+      if constexpr (VEC) {
+        const float4 f = *reinterpret_cast<const float4*>(p.part + s * n + i);
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+      } else {
+        v[0] += p.part[s * n + i];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      if (p.out_bf16) static_cast<bf16_t*>(p.out)[i + e] = f32_to_bf16(v[e]);
+      else static_cast<float*>(p.out)[i + e] = v[e];
+    }
+  }
+}
+
 }  // namespace
+
+// Slices of K of a product of one group on 128-row tiles: where there are few tiles a
+// workgroup walks all of K alone (a step of 128 takes 0.75 us of it), while others
+// have none.  Estimated (us): the walk, and for slices 6 and their sums written and
+// read at 4 TB/s.  Measured: MEASURED_SPLIT
+int fp8_splits(int M, int N, int Kp, int E) {
+  if (E != 1) return 1;
+  const double items = std::ceil(M / 128.0) * std::ceil(N / 256.0), nk = Kp / kFp8Block;
+  int best = 1;
+  double time = nk * 0.75 * std::ceil(items / 256.0);
+  for (int s = 2; s <= 16 && s * 2 <= nk; ++s) {
+    const double t = 6.0 + std::ceil(nk / s) * 0.75 * std::ceil(items * s / 256.0) +
+                     8.0 * s * M * N / 4e6;
+    if (t < 0.9 * time) {
+      time = t;
+      best = s;
+    }
+  }
+  return best;
+}
 
 hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st) {
   const int grid = (device_cus_big() + kXcds - 1) / kXcds * kXcds;
-  if (!a.out_bf16) gemm_fp8_big_kernel<MidF8, false><<<grid, MidF8::THREADS, 0, st>>>(a);
-  else if (a.M / a.E >= 160) gemm_fp8_big_kernel<BigF8, true><<<grid, BigF8::THREADS, 0, st>>>(a);
-  else gemm_fp8_big_kernel<MidF8, true><<<grid, MidF8::THREADS, 0, st>>>(a);
+  auto go = [&](auto kernel) { kernel<<<grid, MidF8::THREADS, 0, st>>>(a); };
+  if (a.splits > 1) {
+    a.out_bf16 ? go(gemm_fp8_big_kernel<MidF8, true, false, true>)
+               : go(gemm_fp8_big_kernel<MidF8, false, false, true>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const long long blocks = (static_cast<long long>(a.M) * a.N + 1023) / 1024;
+    const unsigned g = static_cast<unsigned>(blocks < 4096 ? blocks : 4096);
+    if (a.N % 4 == 0) gemm_fp8_reduce_kernel<true><<<g, 256, 0, st>>>(a);
+    else gemm_fp8_reduce_kernel<false><<<g, 256, 0, st>>>(a);
+  } else if (!a.out_bf16) {
+    go(gemm_fp8_big_kernel<MidF8, false, false>);
+  } else if (a.M / a.E >= 160 && static_cast<long long>(a.M) * a.N >= 6291456LL * 2) {
+    go(gemm_fp8_big_kernel<BigF8, true, true>);
+  } else {
+    go(gemm_fp8_big_kernel<MidF8, true, true>);
+  }
   return hipGetLastError();
 }
 

@@ -56,6 +56,16 @@ __device__ __forceinline__ void make_entries(const Args& p, EntryPlan& s) {
   static_assert(NT >= GROUPS && GROUPS <= kPlanGroups, "a thread per group");
   __shared__ int wsum[NT / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, G = p.E + p.S;
+  if (!p.offsets && G == 1) {  // nothing to read or to add up
+    if (tid == 0) {
+      s.start[0] = 0;
+      s.start[1] = static_cast<int>((static_cast<long long>(p.M) + MR - 1) / MR);
+      s.lo[0] = 0;
+      s.rows[0] = p.M;
+    }
+    __syncthreads();
+    return;
+  }
   int lo = 0, n = 0;
   group_rows<NT>(p, lo, n);
   const int t = (n + MR - 1) / MR;

@@ -25,15 +25,45 @@ __device__ const uint4 kTileZeros = {0, 0, 0, 0};
 
 __device__ __forceinline__ int lines_swz(int k) { return ((k & 3) << 2) | (((k >> 3) & 1) << 1); }
 
-// dma16 (ffn_common.h) from a wave-uniform base and a lane's offset in bytes: one
-// register a load instead of two, and the base moves along K for all of them.
-__device__ __forceinline__ void dma16_at(const bf16_t* base, uint32_t off, bf16_t* dst) {
-  const uint32_t lds = __builtin_amdgcn_readfirstlane(
-      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(dst))));
+// Direct global -> LDS loads to an LDS address (as dma16 in ffn_common.h, which takes
+// a pointer: turning one into an address costs a comparison with null each time).
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(LDS_PTR(p)));
+}
+__device__ __forceinline__ void dma16_to(const bf16_t* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "m0");
+}
+// From a wave-uniform base and a lane's offset in bytes: one register a load instead
+// of two, and the base moves along K for all of them.
+__device__ __forceinline__ void dma16_at(const bf16_t* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
-               : "v"(off), "s"(base), "s"(lds)
+               : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                : "m0");
+}
+// 4 bytes a lane.
+__device__ __forceinline__ void dma4_to(const float* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "m0");
+}
+__device__ __forceinline__ void dma4_at(const float* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "m0");
+}
+
+// LDS addresses of the slots of rings that start at lds (operand A's slots first).
+template <class C>
+__device__ __forceinline__ uint32_t slot_a(uint32_t lds, int i) { return lds + i * C::A_STAGE * 2; }
+template <class C>
+__device__ __forceinline__ uint32_t slot_b(uint32_t lds, int i) {
+  return lds + (C::NSA * C::A_STAGE + i * C::B_STAGE) * 2;
 }
 
 // One operand's loads of a wave: up to L of 1 KiB a stage.  kpos: the K value that
@@ -53,7 +83,7 @@ struct KtLoads {
                           // loads to that of the second
 
   template <int BK, int LW, int LINES, bool TWO>
-  __device__ __forceinline__ void issue(int ks, bf16_t* slot, int wig) const {
+  __device__ __forceinline__ void issue(int ks, uint32_t slot, int wig) const {
     static_assert(LW <= L && LW % 2 == 0, "loads of a stage");
     const bool second = ks >= nseg;
     const int k0 = (second ? ks - nseg : ks) * BK;
@@ -61,7 +91,7 @@ struct KtLoads {
     if (k0 + BK <= kend) {
 #pragma unroll
       for (int q = 0; q < LW; ++q)
-        dma16_at(TWO && q >= LW / 2 ? at + upper : at, off[q], slot + (wig * LW + q) * 512);
+        dma16_at(TWO && q >= LW / 2 ? at + upper : at, off[q], slot + (wig * LW + q) * 1024);
     } else {
 #pragma unroll
       for (int q = 0; q < LW; ++q) {
@@ -71,7 +101,7 @@ struct KtLoads {
                                     reinterpret_cast<const char*>(TWO && q >= LW / 2 ? at + upper : at) +
                                     off[q])
                               : reinterpret_cast<const bf16_t*>(&kTileZeros);
-        dma16(p, slot + (wig * LW + q) * 512);
+        dma16_to(p, slot + (wig * LW + q) * 1024);
       }
     }
   }
@@ -156,16 +186,16 @@ struct KtFrags {
 template <class C, bool TA, bool TB, int U, int GRP, int NV, class Loads>
 __device__ __forceinline__ void kt_step(const Loads& t, const KtFrags<C, TA, TB>& fr, int kt,
                                         int nk, bf16_t* const (&sA)[C::NSA],
-                                        bf16_t* const (&sB)[C::NSB], int wig,
+                                        bf16_t* const (&sB)[C::NSB], uint32_t lds, int wig,
                                         f32x16_t (&acc)[C::BM][C::BN]) {
   BigFrags<C> f;
   fr.template read<GRP, NV>(sA[U % C::NSA], sB[U % C::NSB], wig, f);
   if constexpr (GRP == 0) {
     const int ks = kt + C::NSB - 1 < nk ? kt + C::NSB - 1 : nk - 1;
-    t.template issue<C::BK, C::LPW_B, TB ? kLinesOfLoad<C::NB> : 0, !TB>(ks, sB[(U + C::NSB - 1) % C::NSB], wig);
+    t.template issue<C::BK, C::LPW_B, TB ? kLinesOfLoad<C::NB> : 0, !TB>(ks, slot_b<C>(lds, (U + C::NSB - 1) % C::NSB), wig);
   } else {
     const int ks = kt + C::NSA - 1 < nk ? kt + C::NSA - 1 : nk - 1;
-    t.template issue<C::BK, C::LPW_A, TA ? kLinesOfLoad<C::MT> : 0, false>(ks, sA[(U + C::NSA - 1) % C::NSA], wig);
+    t.template issue<C::BK, C::LPW_A, TA ? kLinesOfLoad<C::MT> : 0, false>(ks, slot_a<C>(lds, (U + C::NSA - 1) % C::NSA), wig);
   }
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): fragments in registers
   if constexpr (GRP == 1) wait_vm<(C::NSA - 2) * C::LPW_A>();
@@ -181,28 +211,29 @@ __device__ __forceinline__ void kt_kloop(const Loads& t, int nk, bf16_t* const (
                                          bf16_t* const (&sB)[C::NSB], int wave, int lane,
                                          f32x16_t (&acc)[C::BM][C::BN]) {
   const int wig = wave & 3;
+  const uint32_t lds = lds_address(sA[0]);
   KtFrags<C, TA, TB> fr;
   fr.template init<GRP>(lane, wig);
   if constexpr (GRP == 0) {
 #pragma unroll
     for (int s = 0; s < C::NSB - 1; ++s)
-      t.template issue<C::BK, C::LPW_B, TB ? kLinesOfLoad<C::NB> : 0, !TB>(s < nk ? s : nk - 1, sB[s], wig);
+      t.template issue<C::BK, C::LPW_B, TB ? kLinesOfLoad<C::NB> : 0, !TB>(s < nk ? s : nk - 1, slot_b<C>(lds, s), wig);
     wait_vm<(C::NSB - 2) * C::LPW_B>();
   } else {
 #pragma unroll
     for (int s = 0; s < C::NSA - 1; ++s)
-      t.template issue<C::BK, C::LPW_A, TA ? kLinesOfLoad<C::MT> : 0, false>(s < nk ? s : nk - 1, sA[s], wig);
+      t.template issue<C::BK, C::LPW_A, TA ? kLinesOfLoad<C::MT> : 0, false>(s < nk ? s : nk - 1, slot_a<C>(lds, s), wig);
     wait_vm<(C::NSA - 2) * C::LPW_A>();
   }
   lds_barrier();                // point 0: stage 0 complete
   if (GRP == 1) lds_barrier();  // point 1 for group 1
   for (int kt = 0; kt < nk; kt += 6) {
-    kt_step<C, TA, TB, 0, GRP, NV>(t, fr, kt, nk, sA, sB, wig, acc);
-    if (kt + 1 < nk) kt_step<C, TA, TB, 1, GRP, NV>(t, fr, kt + 1, nk, sA, sB, wig, acc);
-    if (kt + 2 < nk) kt_step<C, TA, TB, 2, GRP, NV>(t, fr, kt + 2, nk, sA, sB, wig, acc);
-    if (kt + 3 < nk) kt_step<C, TA, TB, 3, GRP, NV>(t, fr, kt + 3, nk, sA, sB, wig, acc);
-    if (kt + 4 < nk) kt_step<C, TA, TB, 4, GRP, NV>(t, fr, kt + 4, nk, sA, sB, wig, acc);
-    if (kt + 5 < nk) kt_step<C, TA, TB, 5, GRP, NV>(t, fr, kt + 5, nk, sA, sB, wig, acc);
+    kt_step<C, TA, TB, 0, GRP, NV>(t, fr, kt, nk, sA, sB, lds, wig, acc);
+    if (kt + 1 < nk) kt_step<C, TA, TB, 1, GRP, NV>(t, fr, kt + 1, nk, sA, sB, lds, wig, acc);
+    if (kt + 2 < nk) kt_step<C, TA, TB, 2, GRP, NV>(t, fr, kt + 2, nk, sA, sB, lds, wig, acc);
+    if (kt + 3 < nk) kt_step<C, TA, TB, 3, GRP, NV>(t, fr, kt + 3, nk, sA, sB, lds, wig, acc);
+    if (kt + 4 < nk) kt_step<C, TA, TB, 4, GRP, NV>(t, fr, kt + 4, nk, sA, sB, lds, wig, acc);
+    if (kt + 5 < nk) kt_step<C, TA, TB, 5, GRP, NV>(t, fr, kt + 5, nk, sA, sB, lds, wig, acc);
   }
   if (GRP == 0) lds_barrier();
 }
