@@ -23,9 +23,10 @@ struct GatedArgs {
   void* dx;               // [M, d], null: not wanted
   void* dw_gate;          // [E, F, d], null: not wanted
   void* dw_up;
-  float* part;            // partial sums of the weight gradients
+  float* part;            // sums of slices of K
   int M, d, F, E;
   static constexpr int S = 0, T = 0;
+  int splits;             // slices of K (gated_splits; set by launch_gated)
   bool bf16;
 };
 
@@ -39,7 +40,10 @@ hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st);
 // Any sizes, either type, on the fp32 matrix cores (gated_tile.hip).
 hipError_t launch_gated_tile(const GatedArgs& a, GatedPart part, hipStream_t st);
 // bf16 rows of 16-byte pieces, in tiles of 128 or 256 rows (gated_big.hip).
-hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, int rows, hipStream_t st);
+hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, hipStream_t st);
+int gated_splits(int M, int d, int F, int E, GatedPart part);
+// Floats of GatedArgs::part that a product may need (0: none).
+size_t gated_part_floats(int M, int d, int F, int E, bool bf16, GatedPart part);
 // pre, dh -> dau.
 hipError_t launch_gated_dau(const GatedArgs& a, hipStream_t st);
 

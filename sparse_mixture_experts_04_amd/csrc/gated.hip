@@ -6,11 +6,24 @@ namespace moe {
 
 static bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// Few rows a group: the stream of the weights.
+static bool streams(int M, int E, GatedPart part) {
+  return part == GatedPart::kForward && (E == 1 ? M <= 16 : M / E < 24);
+}
+
+size_t gated_part_floats(int M, int d, int F, int E, bool bf16, GatedPart part) {
+  if (!bf16 || d % 8 != 0 || F % 8 != 0 || M == 0 || streams(M, E, part)) return 0;
+  const int s = gated_splits(M, d, F, E, part);
+  if (s == 1) return 0;
+  const size_t rows = part == GatedPart::kDw ? 2 * static_cast<size_t>(F) : M;
+  return s * rows * (part == GatedPart::kForward ? 2 * static_cast<size_t>(F) : d);
+}
+
 hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st) {
   // rows of x and of the matrices that start on 16 bytes
   const bool wide = static_cast<long long>(a.d) * (a.bf16 ? 2 : 4) % 16 == 0 && on16(a.x) &&
                     on16(a.w_gate) && on16(a.w_up);
-  if (part == GatedPart::kForward && wide && a.M / a.E < 24) {
+  if (streams(a.M, a.E, part) && wide) {
     StreamArgs s{};
     s.a = a.x;
     s.w0 = a.w_gate;
@@ -28,8 +41,11 @@ hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st) {
                      : part == GatedPart::kDx    ? on16(a.dx)
                                                  : on16(a.dw_gate) && on16(a.dw_up);
   if (a.bf16 && wide && a.F % 8 == 0 && out16) {
-    const long long mean = part == GatedPart::kDw ? a.F : a.M / a.E;
-    return launch_gated_big(a, part, mean > 160 ? 256 : 128, st);
+    GatedArgs b = a;
+    b.splits = gated_part_floats(a.M, a.d, a.F, a.E, true, part) > 0
+                   ? gated_splits(a.M, a.d, a.F, a.E, part)
+                   : 1;
+    return launch_gated_big(b, part, st);
   }
   return launch_gated_tile(a, part, st);
 }

@@ -1,5 +1,7 @@
 // C ABI of the gated feed-forward block: host-side validation, workspace layout
 // and the order of launches (include/moe.h has the meaning of every argument).
+#include <initializer_list>
+
 #include "../../include/moe.h"
 #include "api.h"
 #include "gated.h"
@@ -45,12 +47,21 @@ bool on_value(const void* p, const GatedArgs& a) {
 }
 bool on4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
-// Carves the workspace into a.  Only the backward pass needs one.
+// Carves the workspace into a: dau of the backward pass, the products where they are
+// not saved, and the sums of the slices of one product after another.
 void carve_gated(Carver& c, GatedArgs& a, bool backward, bool saved) {
-  if (!backward) return;
-  const size_t cols = static_cast<size_t>(a.M) * 2 * a.F;
-  a.dau = a.bf16 ? static_cast<void*>(c.take<bf16_t>(cols)) : c.take<float>(cols);
-  if (!saved) a.pre = c.take<float>(cols);
+  if (backward) {
+    const size_t cols = static_cast<size_t>(a.M) * 2 * a.F;
+    a.dau = a.bf16 ? static_cast<void*>(c.take<bf16_t>(cols)) : c.take<float>(cols);
+    if (!saved) a.pre = c.take<float>(cols);
+  }
+  size_t part = 0;
+  for (GatedPart k : {GatedPart::kForward, GatedPart::kDx, GatedPart::kDw}) {
+    if (!backward && k != GatedPart::kForward) continue;
+    const size_t n = gated_part_floats(a.M, a.d, a.F, a.E, a.bf16, k);
+    part = n > part ? n : part;
+  }
+  a.part = c.take<float>(part);
 }
 
 }  // namespace
@@ -80,6 +91,13 @@ moe_status moe_gated_ff(const moe_gated_ff_desc* desc, const void* x, const void
   if (!on_value(x, a) || !on_value(w_gate, a) || !on_value(w_up, a) || !on_value(h, a) ||
       !on4(offsets) || !on4(pre))
     return MOE_ERR_UNSUPPORTED;
+  size_t need = 0;
+  st = moe_gated_ff_workspace_size(desc, 0, 1, &need);
+  if (st != MOE_OK) return st;
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  Carver c{static_cast<char*>(ws)};
+  carve_gated(c, a, false, true);
   a.h = h;
   a.pre = pre;
   return hip_status(launch_gated(a, GatedPart::kForward, stream));

@@ -8,6 +8,8 @@
 // contiguous along their rows.
 // Rows of x, the matrices, dau and the results start on 16 bytes (d and F are
 // multiples of 8).
+#include <cmath>
+
 #include "gated.h"
 #include "tile_kt.h"
 
@@ -18,7 +20,24 @@ namespace {
 using Big = BigShape<256, 32, 3, 6>;
 using Mid = BigShape<128, 64, 3, 3>;
 
-template <class C, GatedPart PART>
+// Whether a gradient's product takes 256-row tiles: they use what they load twice as
+// often, and need as many of them as there are compute units to keep busy.  (The
+// forward pass is faster in 128-row tiles at every size measured, M=8192 d=7168
+// F=2048 393 against 406 us, 24576 rows over 128 experts 244 against 274.)
+// Measured (us, 256 / 128 rows):
+//   dx  M=8192 d=7168 F=2048  424 / 451   dW  383 / 479
+//       1024                   70 / 56         63 / 80
+//       24576 rows, 128 experts, d=2048 F=768  243 / 255   dW  366 / 424
+//       M=4096 d=2048 F=768    35 / 30         64 / 48
+bool large_tiles(const GatedArgs& a, GatedPart part) {
+  const double rows = part == GatedPart::kDw ? 2.0 * a.F * a.E : a.M;
+  const long long mean = part == GatedPart::kDw ? a.F : a.M / a.E;
+  return mean >= 160 && rows * a.d / 65536.0 >= 224.0;
+}
+
+// SPLIT: K is cut into p.splits slices, each an item of its own, whose fp32 sums go to
+// slice s of p.part [splits, rows, columns] (forward [M, 2F], dx [M, d], dW [2F, d]).
+template <class C, GatedPart PART, bool SPLIT = false>
 __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
   constexpr bool FWD = PART == GatedPart::kForward, DW = PART == GatedPart::kDw;
   constexpr bool TA = DW, TB = !FWD;
@@ -32,6 +51,7 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
 #pragma unroll
   for (int i = 0; i < C::NSB; ++i) sB[i] = lds + C::NSA * C::A_STAGE + i * C::B_STAGE;
   static_assert(C::MT * NOUT <= C::LDS_ELEMS, "output tile");
+  static_assert(!SPLIT || C::MT * C::NB * 2 <= C::LDS_ELEMS, "fp32 tile");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -41,8 +61,9 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
   const int ncols = FWD ? F : d;  // columns of the result
   const int n_tiles = (ncols + NOUT - 1) / NOUT;
   const int m_tiles = (F + C::MT - 1) / C::MT;  // kDw: row tiles of a matrix
+  const int splits = SPLIT ? p.splits : 1;
   const long long total = (DW ? static_cast<long long>(p.E) * 2 * m_tiles
-                              : static_cast<long long>(plan.start[p.E])) * n_tiles;
+                              : static_cast<long long>(plan.start[p.E])) * n_tiles * splits;
   const int xcd = blockIdx.x % kXcds;
   const bf16_t* x = static_cast<const bf16_t*>(p.x);
   const bf16_t* dau = static_cast<const bf16_t*>(p.dau);
@@ -50,9 +71,11 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
 
   const long long chunk = (total + kXcds - 1) / kXcds;
   for (long long mine = blockIdx.x / kXcds;; mine += gridDim.x / kXcds) {
-    const long long it = xcd * chunk + mine;
-    if (mine >= chunk || it >= total) break;
+    const long long turn = xcd * chunk + mine;
+    if (mine >= chunk || turn >= total) break;
     __syncthreads();  // the item before is done with the LDS
+    const long long it = SPLIT ? turn / splits : turn;
+    const int slice = SPLIT ? static_cast<int>(turn % splits) : 0;
     int g, m0, rows, nt;
     bool half = false;
     if constexpr (DW) {
@@ -82,11 +105,15 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
     const bf16_t* wu = static_cast<const bf16_t*>(p.w_up) + wat;
     const int kend = FWD ? d : DW ? uni(plan.rows[g]) : F;
     const int nseg = (kend + C::BK - 1) / C::BK;
-    const int nk = PART == GatedPart::kDx ? 2 * nseg : nseg;
+    const int steps = PART == GatedPart::kDx ? 2 * nseg : nseg;
+    const int first = SPLIT ? static_cast<int>(static_cast<long long>(steps) * slice / splits) : 0;
+    const int nk = SPLIT ? static_cast<int>(static_cast<long long>(steps) * (slice + 1) / splits) - first
+                         : steps;
 
     KtLoads<C::LPW_MAX> t;
     t.kend = kend;
     t.nseg = nseg;
+    t.first = first;
     t.jump = 0;
     // offsets inside a tile stay below 2^32: 256 rows of up to 2 * 131072 values
     if (wm == 1) {
@@ -138,7 +165,7 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
       for (int j = 0; j < C::BN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    if (!DW || nk > 0) {  // a group without rows: zeros
+    if ((!DW && !SPLIT) || nk > 0) {  // a group without rows: zeros
       const int nblk = (rows + 31) >> 5;
       const int nv = min((nblk - wm + 1) >> 1, C::BM);
       if (wm == 0) kt_kloop_nv<C, TA, TB, 0, C::BM>(t, nk, sA, sB, wave, lane, nv, acc);
@@ -149,8 +176,40 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
 
     // ---- epilogue: block (i, j) holds the transposed product: lane l -> tile
     // row (2i + wm) * 32 + l % 32, registers 4q..4q+3 -> columns 8q + 4 (l / 32) +
-    // 0..3 of column block j (forward: block 0 a, 1 u).  Through the LDS tile, 16-byte
+    // 0..3 of column block j (forward: block 0 a, 1 u).  Through an LDS tile, 16-byte
     // chunk c of row r in slot c ^ (r % CPR), to coalesced stores.
+    if constexpr (SPLIT) {
+      // the columns of dx or dW, or forward a and u of a row [2F]
+      const size_t ld = FWD ? F2 : d;
+      float* to = p.part + (static_cast<size_t>(slice) * (DW ? F2 : p.M) +
+                            (DW ? (half ? F : 0) : row0) + m0) * ld;
+      constexpr int CPR = C::NB / 4;
+      float* tile = reinterpret_cast<float*>(lds);
+#pragma unroll
+      for (int i = 0; i < C::BM; ++i) {
+        const int row = (2 * i + wm) * 32 + (lane & 31);
+#pragma unroll
+        for (int j = 0; j < C::BN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int ch = wn * 16 + j * 8 + 2 * q + (lane >> 5);
+            *reinterpret_cast<float4*>(tile + (row * CPR + (ch ^ (row & (CPR - 1)))) * 4) =
+                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]);
+          }
+      }
+      __syncthreads();
+      for (int c = tid; c < rows * CPR; c += C::THREADS) {
+        const int row = c / CPR, ch = c % CPR;
+        // forward: of 64 columns of the tile, 32 are a's and 32 u's
+        const int col = n0 + (FWD ? ch / 16 * 32 + ch % 8 * 4 : ch * 4);
+        if (col < ncols)
+          *reinterpret_cast<float4*>(to + row * ld + (FWD && (ch & 8) ? F : 0) + col) =
+              *reinterpret_cast<const float4*>(tile + (row * CPR + (ch ^ (row & (CPR - 1)))) * 4);
+      }
+      continue;
+    }
+    if (FWD && !p.h && !p.pre) continue;
     constexpr int CPR = NOUT / 8;
     bf16_t* tile = lds;
 #pragma unroll
@@ -168,16 +227,16 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
             v[e] = acc[i][j][4 * q + e];
             if (FWD) v[e] = v[e] * sigmoid(v[e]) * acc[i][1][4 * q + e];
           }
-          if (FWD && p.pre && row < rows) {
-            const int c = n0 + wn * 32 + 8 * q + 4 * (lane >> 5);
-            if (c < F) {
-              float* o = p.pre + (row0 + m0 + row) * F2 + c;
-              *reinterpret_cast<float4*>(o) = make_float4(acc[i][0][4 * q], acc[i][0][4 * q + 1],
-                                                          acc[i][0][4 * q + 2], acc[i][0][4 * q + 3]);
-              *reinterpret_cast<float4*>(o + F) =
-                  make_float4(acc[i][1][4 * q], acc[i][1][4 * q + 1], acc[i][1][4 * q + 2],
-                              acc[i][1][4 * q + 3]);
-            }
+          // (a and u straight from the registers, 32 bytes of a row at a time; through
+          // an LDS tile the forward pass of 24576 rows over 128 experts took 313 us
+          // against 275)
+          const int c = n0 + wn * 32 + 8 * q + 4 * (lane >> 5);
+          if (FWD && p.pre && row < rows && c < F) {
+            float* o = p.pre + (row0 + m0 + row) * F2 + c;
+            *reinterpret_cast<float4*>(o) = make_float4(acc[i][0][4 * q], acc[i][0][4 * q + 1],
+                                                        acc[i][0][4 * q + 2], acc[i][0][4 * q + 3]);
+            *reinterpret_cast<float4*>(o + F) = make_float4(acc[i][1][4 * q], acc[i][1][4 * q + 1],
+                                                            acc[i][1][4 * q + 2], acc[i][1][4 * q + 3]);
           }
           const uint32_t w0 = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
           const uint32_t w1 = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
@@ -200,22 +259,97 @@ __global__ __launch_bounds__(512, 1) void gated_big_kernel(GatedArgs p) {
   }
 }
 
-template <class C>
-hipError_t run(const GatedArgs& a, GatedPart part, hipStream_t st) {
+// The result from the slices' sums, in order, 4 values of a row a thread.  Forward:
+// h from a and u, and pre.  Rows outside the one group keep what they held.
+template <GatedPart PART>
+__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
+  constexpr bool FWD = PART == GatedPart::kForward, DW = PART == GatedPart::kDw;
+  long long first = 0, last = DW ? 2 * p.F : p.M;
+  if (!DW && p.offsets) {
+    first = clampi(p.offsets[0], 0, p.M);
+    last = clampi(p.offsets[1], 0, p.M);
+  }
+  const int cols = FWD ? p.F : p.d, ld = FWD ? 2 * p.F : p.d, quads = cols / 4;
+  const size_t slice = static_cast<size_t>(DW ? 2 * p.F : p.M) * ld;
+  for (long long i = first * quads + static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+       i < last * quads; i += static_cast<long long>(gridDim.x) * 256) {
+    const long long row = i / quads;
+    const int c = static_cast<int>(i - row * quads) * 4;
+    const float* from = p.part + row * ld + c;
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f}, u = v;
+    for (int s = 0; s < p.splits; ++s) {
+      v += *reinterpret_cast<const f32x4_t*>(from + s * slice);
+      if (FWD) u += *reinterpret_cast<const f32x4_t*>(from + s * slice + p.F);
+    }
+    if (FWD && p.pre) {
+      *reinterpret_cast<f32x4_t*>(p.pre + row * ld + c) = v;
+      *reinterpret_cast<f32x4_t*>(p.pre + row * ld + p.F + c) = u;
+    }
+    if (FWD && !p.h) continue;
+    if (FWD)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = v[e] * sigmoid(v[e]) * u[e];
+    bf16_t* out = FWD ? static_cast<bf16_t*>(p.h) + row * p.F
+                  : DW ? (row < p.F ? static_cast<bf16_t*>(p.dw_gate) + row * p.d
+                                    : static_cast<bf16_t*>(p.dw_up) + (row - p.F) * p.d)
+                       : static_cast<bf16_t*>(p.dx) + row * p.d;
+    *reinterpret_cast<uint2*>(out + c) =
+        make_uint2(f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
+                   f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16));
+  }
+}
+
+template <GatedPart PART>
+hipError_t run(const GatedArgs& a, hipStream_t st) {
   const int grid = (device_cus_big() + kXcds - 1) / kXcds * kXcds;
-  if (part == GatedPart::kForward)
-    gated_big_kernel<C, GatedPart::kForward><<<grid, C::THREADS, 0, st>>>(a);
-  else if (part == GatedPart::kDx)
-    gated_big_kernel<C, GatedPart::kDx><<<grid, C::THREADS, 0, st>>>(a);
-  else
-    gated_big_kernel<C, GatedPart::kDw><<<grid, C::THREADS, 0, st>>>(a);
+  auto go = [&](auto kernel) { kernel<<<grid, Mid::THREADS, 0, st>>>(a); };
+  if (a.splits > 1) {
+    go(gated_big_kernel<Mid, PART, true>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const long long rows = PART == GatedPart::kDw ? 2LL * a.F : a.M;
+    const long long blocks = (rows * (PART == GatedPart::kForward ? a.F : a.d) / 4 + 255) / 256;
+    gated_reduce_kernel<PART><<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(a);
+  } else if constexpr (PART == GatedPart::kForward) {
+    go(gated_big_kernel<Mid, PART>);
+  } else {
+    if (large_tiles(a, PART)) go(gated_big_kernel<Big, PART>);
+    else go(gated_big_kernel<Mid, PART>);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, int rows, hipStream_t st) {
-  return rows == Big::MT ? run<Big>(a, part, st) : run<Mid>(a, part, st);
+// Slices of K of a product of one group on 128-row tiles: where there are few tiles a
+// workgroup walks all of K alone (a step of 64 takes 0.6 us of it), while others have
+// none.  Estimated (us): the walk, and for slices 6 and their sums written and read
+// at 4 TB/s.  MEASURED_SPLIT
+int gated_splits(int M, int d, int F, int E, GatedPart part) {
+  if (E != 1) return 1;
+  const bool fwd = part == GatedPart::kForward, dw = part == GatedPart::kDw;
+  const double rows = dw ? 2.0 * F : M, cols = fwd ? 2.0 * F : d;
+  const double items = std::ceil(rows / 128.0) * std::ceil(cols / 256.0);
+  const double nk = fwd ? std::ceil(d / 64.0) : dw ? std::ceil(M / 64.0) : 2.0 * std::ceil(F / 64.0);
+  int best = 1;
+  double time = nk * 0.6 * std::ceil(items / 256.0);
+  for (int s = 2; s <= 16 && s * 2 <= nk; ++s) {
+    const double t = 6.0 + std::ceil(nk / s) * 0.6 * std::ceil(items * s / 256.0) +
+                     8.0 * s * rows * cols / 4e6;
+    if (t < 0.9 * time) {
+      time = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, hipStream_t st) {
+  switch (part) {
+    case GatedPart::kForward: return run<GatedPart::kForward>(a, st);
+    case GatedPart::kDx: return run<GatedPart::kDx>(a, st);
+    default: return run<GatedPart::kDw>(a, st);
+  }
 }
 
 }  // namespace moe

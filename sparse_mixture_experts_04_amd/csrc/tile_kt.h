@@ -79,12 +79,14 @@ struct KtLoads {
   long long jump;         // elements from the first segment to the second
   int kend;               // K values of a segment
   int nseg;               // steps of a segment
+  int first;              // step that the loop begins at
   long long upper;        // TWO: elements from the base of the first half of the
                           // loads to that of the second
 
   template <int BK, int LW, int LINES, bool TWO>
   __device__ __forceinline__ void issue(int ks, uint32_t slot, int wig) const {
     static_assert(LW <= L && LW % 2 == 0, "loads of a stage");
+    ks += first;
     const bool second = ks >= nseg;
     const int k0 = (second ? ks - nseg : ks) * BK;
     const bf16_t* at = base + k0 * kstride + (second ? jump : 0);
