@@ -120,6 +120,125 @@ __global__ __launch_bounds__(kT32Threads) void gated_tile_kernel(GatedArgs p) {
   }
 }
 
+// The same for results of few tiles, where one step after another of a large tile is
+// waiting for memory: a workgroup's 8 waves share K of one 32 x 32 block (forward: 32
+// rows x 16 columns), each from global memory straight into registers, and add their
+// sums through LDS in order.  An instruction's two k are 4 apart (lane / 32), so that
+// an operand contiguous along K is read 4 values a lane.
+constexpr int kSmallWaves = 8;
+template <typename T, GatedPart PART>
+__global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(GatedArgs p) {
+  __shared__ float red[kSmallWaves][16][64];
+  __shared__ EntryPlan plan;
+  constexpr bool FWD = PART == GatedPart::kForward, DW = PART == GatedPart::kDw;
+  constexpr int NOUT = FWD ? 16 : 32;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r32 = lane & 31, half = lane >> 5;
+  make_entries<64 * kSmallWaves, 32, kMaxGroups>(p, plan);
+  const int d = p.d, F = p.F, F2 = 2 * F;
+  const int n_tiles = ((FWD ? F : d) + NOUT - 1) / NOUT, m_tiles = (F2 + 31) / 32;
+  const long long total = (DW ? static_cast<long long>(p.E) * m_tiles
+                              : static_cast<long long>(plan.start[p.E])) * n_tiles;
+  const T* x = static_cast<const T*>(p.x);
+  const T* dau = static_cast<const T*>(p.dau);
+  const bool vx = d % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0;
+  const bool vw = d % 4 == 0 && (reinterpret_cast<uintptr_t>(p.w_gate) |
+                                 reinterpret_cast<uintptr_t>(p.w_up)) % (4 * sizeof(T)) == 0;
+  const bool vd = F % 2 == 0;
+
+  for (long long it = blockIdx.x; it < total; it += gridDim.x) {
+    const int ent = static_cast<int>(it / n_tiles), n0 = static_cast<int>(it % n_tiles) * NOUT;
+    const int g = DW ? ent / m_tiles : entry_group(plan, p.E, ent);
+    const int m0 = (DW ? ent % m_tiles : ent - plan.start[g]) * 32;
+    const int rows = DW ? min(F2 - m0, 32) : min(plan.rows[g] - m0, 32);
+    const long long row0 = plan.lo[g];
+    const size_t wat = static_cast<size_t>(g) * F * d;
+    const T* wg = static_cast<const T*>(p.w_gate) + wat;
+    const T* wu = static_cast<const T*>(p.w_up) + wat;
+    const int K = FWD ? d : DW ? plan.rows[g] : F2;
+    const int chunks = (K + 7) / 8;
+    const int c0 = chunks * wave / kSmallWaves, c1 = chunks * (wave + 1) / kSmallWaves;
+    // this lane's row and column of the operands
+    const long long row = row0 + m0 + min(r32, rows - 1);
+    const T* xr = x + row * d;
+    const T* dr = dau + row * F2;
+    const T* wr = (r32 & 16 ? wu : wg) + static_cast<size_t>(min(n0 + (r32 & 15), F - 1)) * d;
+    const int mc = min(m0 + r32, F2 - 1), nc = min(n0 + r32, d - 1);
+    f32x16_t acc;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) {
+      const int k = c * 8 + 4 * half;
+      float a[4], b[4];
+      if constexpr (FWD) {
+        load4(xr + k, d - k, vx, a);
+        load4(wr + k, d - k, vw, b);
+      } else if constexpr (!DW) {
+        load4(dr + k, F2 - k, vd, a);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int f = k + e;
+          const T* w = f < F ? wg + static_cast<size_t>(f) * d : wu + static_cast<size_t>(f - F) * d;
+          b[e] = f < F2 ? ActTraits<T>::load(w + nc) : 0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a[e] = k + e < K ? ActTraits<T>::load(dau + (row0 + k + e) * F2 + mc) : 0.0f;
+          b[e] = k + e < K ? ActTraits<T>::load(x + (row0 + k + e) * d + nc) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b[e], a[e], acc, 0, 0, 0);
+    }
+    __syncthreads();  // the block before is done with red
+#pragma unroll
+    for (int r = 0; r < 16; ++r) red[wave][r][lane] = acc[r];
+    __syncthreads();
+    // thread: lane l's registers r and r + 8 of all waves
+    const int r = wave;
+    float v[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; ++w) {
+      v[0] += red[w][r][lane];
+      v[1] += red[w][r + 8][lane];
+    }
+    if (r32 >= rows) continue;
+    if constexpr (FWD) {
+      const int c = n0 + 8 * (r / 4) + 4 * half + r % 4;
+      if (c >= F) continue;
+      const size_t at = static_cast<size_t>(row0 + m0 + r32);
+      if (p.h) ActTraits<T>::store(static_cast<T*>(p.h) + at * F + c, v[0] * sigmoid(v[0]) * v[1]);
+      if (p.pre) {
+        p.pre[at * F2 + c] = v[0];
+        p.pre[at * F2 + F + c] = v[1];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = n0 + 8 * (r / 4 + 2 * i) + 4 * half + r % 4;
+        if (c >= d) continue;
+        const int n = m0 + r32;
+        T* out = !DW ? static_cast<T*>(p.dx) + static_cast<size_t>(row0 + m0 + r32) * d
+                 : n < F ? static_cast<T*>(p.dw_gate) + wat + static_cast<size_t>(n) * d
+                         : static_cast<T*>(p.dw_up) + wat + static_cast<size_t>(n - F) * d;
+        ActTraits<T>::store(out + c, v[i]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(bf16_t* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
+                 f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16));
+}
+
 // dau from pre and dh, in fp32, rounded once to T (the products that read dau take
 // T).  A thread per 4 columns of a row.
 template <typename T>
@@ -145,40 +264,45 @@ __global__ __launch_bounds__(256) void gated_dau_kernel(GatedArgs p, int quads) 
       du[e] = g[e] * a[e] * s;
     }
     T* o = dau + row * 2 * F + c;
+    if (vec) {
+      store4(o, da);
+      store4(o + F, du);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e >= n) break;
-      ActTraits<T>::store(o + e, da[e]);
-      ActTraits<T>::store(o + F + e, du[e]);
+      for (int e = 0; e < 4; ++e) {
+        if (e >= n) break;
+        ActTraits<T>::store(o + e, da[e]);
+        ActTraits<T>::store(o + F + e, du[e]);
+      }
     }
   }
 }
 
-template <int R, typename T>
-void run(const GatedArgs& a, GatedPart part, int grid, hipStream_t st) {
-  if (part == GatedPart::kForward)
-    gated_tile_kernel<R, T, GatedPart::kForward><<<grid, kT32Threads, 0, st>>>(a);
-  else if (part == GatedPart::kDx)
-    gated_tile_kernel<R, T, GatedPart::kDx><<<grid, kT32Threads, 0, st>>>(a);
-  else
-    gated_tile_kernel<R, T, GatedPart::kDw><<<grid, kT32Threads, 0, st>>>(a);
+template <typename T, GatedPart PART>
+void run(const GatedArgs& a, hipStream_t st) {
+  const int cols = PART == GatedPart::kForward ? 2 * a.F : a.d;
+  const long long rows = PART == GatedPart::kDw ? 2LL * a.F * a.E : a.M;
+  // tiles of 64 while 128 would leave compute units without one; blocks of 32 whose K
+  // eight waves share while tiles of 64 would.  MEASURED_SMALL
+  const long long of64 = (rows + 63) / 64 * ((cols + 63) / 64);
+  const long long of128 = (rows + 127) / 128 * ((cols + 127) / 128);
+  if (of64 < 256) gated_small_kernel<T, PART><<<1024, 64 * kSmallWaves, 0, st>>>(a);
+  else if (of128 < 256) gated_tile_kernel<1, T, PART><<<1024, kT32Threads, 0, st>>>(a);
+  else gated_tile_kernel<2, T, PART><<<1024, kT32Threads, 0, st>>>(a);
+}
+
+template <typename T>
+void run(const GatedArgs& a, GatedPart part, hipStream_t st) {
+  if (part == GatedPart::kForward) run<T, GatedPart::kForward>(a, st);
+  else if (part == GatedPart::kDx) run<T, GatedPart::kDx>(a, st);
+  else run<T, GatedPart::kDw>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_gated_tile(const GatedArgs& a, GatedPart part, hipStream_t st) {
-  // tiles of 64 while 128 would leave compute units without one
-  const int cols = part == GatedPart::kForward ? 2 * a.F : a.d;
-  const long long rows = part == GatedPart::kDw ? 2LL * a.F * a.E : a.M;
-  const long long large = (rows + 127) / 128 * ((cols + 127) / 128);
-  const int grid = 1024;
-  if (large >= 256) {
-    if (a.bf16) run<2, bf16_t>(a, part, grid, st);
-    else run<2, float>(a, part, grid, st);
-  } else {
-    if (a.bf16) run<1, bf16_t>(a, part, grid, st);
-    else run<1, float>(a, part, grid, st);
-  }
+  if (a.bf16) run<bf16_t>(a, part, st);
+  else run<float>(a, part, st);
   return hipGetLastError();
 }
 
