@@ -24,7 +24,7 @@ namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kThreads = 1024, kWaves = kThreads / 64, kLogWaves = 4;
 constexpr int kEntryRows = 16;
 constexpr int kStep = 128;  // bytes of a row per step
 
@@ -93,7 +93,7 @@ __device__ __forceinline__ void multiply(const Piece& a, const Piece (&w)[TILES]
 // GROUPED: rows of groups by the offsets; otherwise one group of all M rows, and no
 // plan of entries to make first.  RING: steps in registers.
 template <StreamKind KIND, bool GROUPED, int TILES, int RING>
-__global__ __launch_bounds__(kThreads, 4) void stream_kernel(StreamArgs p, int split) {
+__global__ __launch_bounds__(kThreads, 4) void stream_kernel(StreamArgs p, int log_split) {
   constexpr bool GATED = KIND != StreamKind::kFp8;
   constexpr int SIZE = KIND == StreamKind::kFp8 ? 1 : KIND == StreamKind::kGatedBf16 ? 2 : 4;
   constexpr int NOUT = GATED ? 8 * TILES : 16 * TILES;
@@ -108,26 +108,29 @@ __global__ __launch_bounds__(kThreads, 4) void stream_kernel(StreamArgs p, int s
   const int per = (p.N + NOUT - 1) / NOUT;
   const int nb = (p.N + 127) / 128;
   const int entries = GROUPED ? plan.start[p.E] : (p.M + kEntryRows - 1) / kEntryRows;
-  const long long units = static_cast<long long>(entries) * per;
-  const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  // (32 bits hold the units: E N K < 2^40, and no more than 2.5 E entries come here)
+  const int units = entries * per, share = units / gridDim.x, rest = units % gridDim.x;
+  const int u0 = blockIdx.x * share + min(static_cast<int>(blockIdx.x), rest);
+  const int u1 = u0 + share + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
   // this wave's units: a run of the workgroup's, or every teams-th of them
-  const int teams = kWaves / split, team = wave / split, part = wave % split;
-  const long long first = split == 1 ? u0 + (u1 - u0) * wave / kWaves : u0 + team;
-  const long long last = split == 1 ? u0 + (u1 - u0) * (wave + 1) / kWaves : u1;
-  const int stride = split == 1 ? 1 : teams;
-  const int count = last > first ? static_cast<int>((last - first + stride - 1) / stride) : 0;
-  const int rounds = split == 1 ? 0 : static_cast<int>((u1 - u0 + teams - 1) / teams);
-  const int s0 = static_cast<int>(static_cast<long long>(nk) * part / split);
-  const int ns = static_cast<int>(static_cast<long long>(nk) * (part + 1) / split) - s0;
+  const int split = 1 << log_split, teams = kWaves >> log_split;
+  const int team = wave >> log_split, part = wave & (split - 1);
+  const int first = split == 1 ? u0 + (u1 - u0) * wave / kWaves : u0 + team;
+  const int last = split == 1 ? u0 + (u1 - u0) * (wave + 1) / kWaves : u1;
+  const int log_stride = split == 1 ? 0 : kLogWaves - log_split, stride = 1 << log_stride;
+  const int count = last > first ? (last - first + stride - 1) >> log_stride : 0;
+  const int rounds = split == 1 ? 0 : (u1 - u0 + teams - 1) >> log_stride;
+  const int s0 = (nk * part) >> log_split;
+  const int ns = ((nk * (part + 1)) >> log_split) - s0;
 
   struct Place {
     int g, tile, rows;
     long long row0;
   };
-  auto place = [&](long long u) __attribute__((always_inline)) {
+  auto place = [&](int u) __attribute__((always_inline)) {
     Place q;
-    const int ent = static_cast<int>(u / per);
-    q.tile = static_cast<int>(u - static_cast<long long>(ent) * per);
+    const int ent = entries == 1 ? 0 : u / per;
+    q.tile = u - ent * per;
     if constexpr (GROUPED) {
       q.g = entry_group(plan, p.E, ent);
       const int m0 = (ent - plan.start[q.g]) * kEntryRows;
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(kThreads, 4) void stream_kernel(StreamArgs p, int s
 
   if (count > 0) {
     // ---- load side
-    long long lu = first;
+    int lu = first;
     int ls = 0, lleft = count;
     const char* ap;
     const char* wp[TILES];
@@ -205,7 +208,7 @@ __global__ __launch_bounds__(kThreads, 4) void stream_kernel(StreamArgs p, int s
     for (int i = 0; i < RING - 1; ++i) load(i);
 
     // ---- compute side
-    long long cu = first;
+    int cu = first;
     int cs = 0;
     f32x4_t acc[TILES] = {};
     const long long total = static_cast<long long>(count) * ns;
@@ -292,13 +295,13 @@ hipError_t run(const StreamArgs& a, hipStream_t st) {
   const long long units = entries * ((a.N + (two ? 2 : 1) * cols - 1) / ((two ? 2 : 1) * cols));
   // waves that share a unit: as many as leave no more than a unit a team, with two
   // steps each at least
-  int split = 1;
-  while (split < kWaves && units * split * 2 <= static_cast<long long>(kGrid) * kWaves &&
-         nk >= split * 4)
-    split *= 2;
-  const long long teams = kWaves / split;
+  int split = 0;  // as a power of two
+  while (split < kLogWaves && (units << (split + 1)) <= static_cast<long long>(kGrid) * kWaves &&
+         nk >= 4LL << split)
+    ++split;
+  const long long teams = kWaves >> split;
   const long long want = (units + teams - 1) / teams;
-  const int grid = split == 1 || want > kGrid ? kGrid : static_cast<int>(want);
+  const int grid = split == 0 || want > kGrid ? kGrid : static_cast<int>(want);
   if (a.offsets) {
     if (two) stream_kernel<KIND, true, 2, 3><<<grid, kThreads, 0, st>>>(a, split);
     else stream_kernel<KIND, true, 1, 4><<<grid, kThreads, 0, st>>>(a, split);
