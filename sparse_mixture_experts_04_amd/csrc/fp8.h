@@ -33,7 +33,7 @@ struct Fp8Args {
   bool out_bf16;
 };
 // Whether a product goes through the stream of its weights (stream.hip).
-bool fp8_streams(int M, int N, int Kp, int E);
+bool fp8_streams(int M);
 int fp8_splits(int M, int N, int Kp, int E);
 hipError_t launch_gemm_fp8(const Fp8Args& a, hipStream_t st);
 hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st);

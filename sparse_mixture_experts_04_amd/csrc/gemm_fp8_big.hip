@@ -474,25 +474,25 @@ __global__ __launch_bounds__(512, 1) void gemm_fp8_big_kernel(Fp8Args p) {
     __syncthreads();
     constexpr int PER = 16 / OB;  // values of a chunk
     const int col0 = item.n * NOUT;
-    const bool whole = p.N % PER == 0;  // rows of y start on 16 bytes
     char* out = SPLIT ? reinterpret_cast<char*>(p.part + static_cast<size_t>(slice) * p.M * p.N)
                       : static_cast<char*>(p.out);
-    for (int ch0 = tid; ch0 < item.rows * CPR; ch0 += C::THREADS) {
-      const int row = ch0 / CPR, ch = ch0 % CPR;
-      const uint4 v = *reinterpret_cast<const uint4*>(tile + row * NOUT * OB +
-                                                      ((ch ^ (row & (CPR - 1))) << 4));
-      const int col = col0 + ch * PER;
-      char* o = out + ((row0 + row) * p.N + col) * OB;
-      if (whole) {
-        if (col < p.N) *reinterpret_cast<uint4*>(o) = v;
-      } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          if (col + e >= p.N) break;
-          if (OUT_BF16) reinterpret_cast<bf16_t*>(o)[e] = static_cast<bf16_t>(w[e / 2] >> (16 * (e & 1)));
-          else reinterpret_cast<uint32_t*>(o)[e] = w[e % 4];
-        }
+    out += (row0 * p.N + col0) * OB;
+    if (p.N % PER == 0) {  // rows of y start on 16 bytes
+      for (int c = tid; c < item.rows * CPR; c += C::THREADS) {
+        const int row = c / CPR, ch = c % CPR;
+        if (col0 + ch * PER < p.N)
+          *reinterpret_cast<uint4*>(out + (static_cast<size_t>(row) * p.N + ch * PER) * OB) =
+              *reinterpret_cast<const uint4*>(tile + row * NOUT * OB + ((ch ^ (row & (CPR - 1))) << 4));
+      }
+    } else {  // a value a thread
+      const int cols = min(NOUT, p.N - col0);
+      for (int c = tid; c < item.rows * NOUT; c += C::THREADS) {
+        const int row = c / NOUT, col = c % NOUT;
+        if (col >= cols) continue;
+        const char* from = tile + row * NOUT * OB + (((col / PER) ^ (row & (CPR - 1))) << 4) + col % PER * OB;
+        const size_t to = static_cast<size_t>(row) * p.N + col;
+        if (OB == 2) reinterpret_cast<uint16_t*>(out)[to] = *reinterpret_cast<const uint16_t*>(from);
+        else reinterpret_cast<uint32_t*>(out)[to] = *reinterpret_cast<const uint32_t*>(from);
       }
     }
   }
