@@ -588,8 +588,8 @@ moe_status moe_gemm_fp8(const moe_gemm_fp8_desc* desc, const uint8_t* a, const f
  *     m = s sign(c) (c / 127)^2,  c = round(127 sqrt(|m'| / s))
  *     v = z (c / 255)^4,          c = round(255 (v' / z)^(1/4)), 1 at least where v' > 0
  *   Codes are those of exact arithmetic on the old states and g; p' is taken from
- *   the unrounded m' and v'.  Zeros (codes and scales) are the states before the first step.  A
- *   block whose m' or v' is not finite gets scales of NaN and codes 0.
+ *   m' and v' in fp32, not from their codes.  Zeros (codes and scales) are the
+ *   states before the first step.  A block whose m' or v' is not finite gets scales of NaN and codes 0.
  *   m_values, v_values (both or neither): fp32 [n], where
  *   moe_adamw_state_values writes the values that the codes stand for; it passes
  *   over tensors without them.
@@ -597,8 +597,9 @@ moe_status moe_gemm_fp8(const moe_gemm_fp8_desc* desc, const uint8_t* a, const f
  * moe_adamw_prepare checks `count` tensors (host array; n values each, dense,
  * aligned to their element) and writes them into `table` (device memory of
  * moe_adamw_table_size bytes, 16-byte aligned) on `stream`; *chunks goes to the
- * calls that use the table.  The tensors must stay where they are while it is
- * used, and no two of them share memory.
+ * calls that use the table, which come after it in stream order.  The tensors must
+ * stay where they are while it is used, and no two of them share memory (for
+ * parameters MOE_ERR_UNSUPPORTED).
  * moe_adamw: step counts from 1.  lr_dev, step_dev and grad_scale_dev (device
  * memory, or NULL) are read when the kernel runs, for captured graphs; lr and step
  * are not read where they are given.  A grad_scale that is NaN or infinite leaves

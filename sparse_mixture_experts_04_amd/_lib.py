@@ -859,7 +859,8 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v
     uint8 codes with ``m_scales`` and ``v_scales`` (fp32, one for every 256 values;
     zeros to begin with).  ``copies``: bf16 tensors that take each fp32 parameter
     too.  ``m_values``, ``v_values``: fp32 tensors for adamw_state_values.  The plan
-    holds the tensors; a gradient that moves needs a new plan."""
+    holds the tensors; a gradient that moves needs a new plan.  Waits for the current
+    stream; not for use inside a capture (a step with the plan is)."""
     lists = {"params": params, "grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
              "copies": copies, "m_scales": m_scales, "v_scales": v_scales, "m_values": m_values,
              "v_values": v_values}
@@ -871,6 +872,8 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v
     if count == 0:
         raise ValueError("adamw_plan: no params")
     dev = _on_gpu(lists["params"][0], "params[0]")
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("adamw_plan: make the plan before the capture that uses it")
     pt, gt = lists["params"][0].dtype, getattr(lists["grads"][0], "dtype", None)
     bits8 = getattr(lists["exp_avg"][0], "dtype", None) is torch.int8
     if bits8 != (m_scales is not None) or bits8 != (v_scales is not None):
@@ -901,6 +904,7 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v
     chunks = ctypes.c_int64(0)
     _check("moe_adamw_prepare", _call(dev, lib.moe_adamw_prepare, ctypes.byref(desc), rows,
                                       ctypes.byref(chunks), table.data_ptr(), n.value))
+    torch.cuda.current_stream(device).synchronize()  # steps may run on any stream
     return AdamwPlan(dev, desc, chunks.value, table, lists)
 
 

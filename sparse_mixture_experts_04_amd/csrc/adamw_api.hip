@@ -1,6 +1,10 @@
 // C ABI of the AdamW step: host-side validation, the table of tensors and launches
 // (include/moe.h has the meaning of every argument).
+#include <algorithm>
 #include <cmath>
+#include <new>
+#include <utility>
+#include <vector>
 
 #include "../../include/moe.h"
 #include "adamw.h"
@@ -53,6 +57,21 @@ moe_status check_tensor(const moe_adamw_desc* d, const moe_adamw_tensor& t) {
   return MOE_OK;
 }
 
+// Whether two tensors share parameters: both would take the step.
+bool shared(const moe_adamw_desc* d, const moe_adamw_tensor* t) {
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;  // first byte, one past the last
+  const uintptr_t size = d->param == MOE_F32 ? 4 : 2;
+  for (int i = 0; i < d->count; ++i)
+    if (t[i].n > 0) {
+      const uintptr_t p = reinterpret_cast<uintptr_t>(t[i].p);
+      spans.emplace_back(p, p + size * static_cast<uintptr_t>(t[i].n));
+    }
+  std::sort(spans.begin(), spans.end());
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i].first < spans[i - 1].second) return true;
+  return false;
+}
+
 long long chunks_of(int64_t n) { return (n + kAdamwChunk - 1) / kAdamwChunk; }
 
 }  // namespace
@@ -82,6 +101,11 @@ moe_status moe_adamw_prepare(const moe_adamw_desc* desc, const moe_adamw_tensor*
   }
   if (!table || bytes < table_bytes(desc->count)) return MOE_ERR_WORKSPACE;
   if (!on(table, 16)) return MOE_ERR_UNSUPPORTED;
+  try {
+    if (shared(desc, tensors)) return MOE_ERR_UNSUPPORTED;
+  } catch (const std::bad_alloc&) {
+    return MOE_ERR_WORKSPACE;
+  }
   *chunks = total;
   const AdamwTable t = table_at(table, desc->count);
   long long at = 0;

@@ -1,5 +1,6 @@
 """64-bit forms of the gated block, the e4m3 products and the AdamW step, with
 bounds of what fp32 sums and the stated roundings may differ from them."""
+import numpy as np
 import torch
 
 U32 = 2.0 ** -24                # half a step of fp32, relative
@@ -173,8 +174,13 @@ def adamw64(p, g, m, v, step, lr, b1, b2, eps, wd, factor, ms=None, vs=None):
         bv = torch.nn.functional.pad(new_v.flatten(), (0, pad)).view(-1, 256)
         s, z = bm.abs().amax(1).float(), bv.amax(1).float()
         safe = lambda t: torch.where(t > 0, t, torch.ones_like(t)).double()[:, None]
-        cm = torch.sign(bm) * torch.round(127 * (bm.abs() / safe(s)).sqrt()).clamp(max=127)
-        cv = torch.round(255 * (bv / safe(z)).sqrt().sqrt()).clamp(max=255)
+        # roots in 64-bit mantissas: a quarter of the largest lies on a border (127 / 2 =
+        # 63.5), and bf16 gradients meet it, often one step of 64 bits (2^-52) below.
+        # The root halves that to 2^-53, which a root in 53 bits rounds away.
+        wide = lambda t: t.numpy().astype(np.longdouble)
+        narrow = lambda a: torch.from_numpy(np.rint(a).astype(np.float64))
+        cm = torch.sign(bm) * narrow(127 * np.sqrt(wide(bm.abs()) / wide(safe(s)))).clamp(max=127)
+        cv = narrow(255 * np.sqrt(np.sqrt(wide(bv) / wide(safe(z))))).clamp(max=255)
         cv = torch.where(bv > 0, cv.clamp(min=1), cv)
         out.update(cm=cm.flatten()[:n].view(M.shape).to(torch.int8),
                    cv=cv.flatten()[:n].view(M.shape).to(torch.uint8), s=s, z=z)

@@ -275,3 +275,101 @@ def test_shapes_and_a_second_plan():
     old = clone(t)
     L.adamw_step(L.adamw_plan(**t), 2, **HYPER)
     check(t, old, 2)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("size,eps", [(1e-17, 0.0), (1e-20, 1e-8), (1e-30, 1e-8), (1e18, 1e-8)])
+def test_sizes_of_gradients(size, eps, bits):
+    """Scales far from 1: roots beyond the reach of the short forms, values below the
+    smallest normal fp32, squares near its largest."""
+    L = ops()
+    t = tensors([3000, 77], F32, F32, bits)
+    for k in ("exp_avg", "exp_avg_sq", "m_scales", "v_scales"):
+        for x in t.get(k, []):
+            x.zero_()
+    plan = L.adamw_plan(**t)
+    for step in (1, 2):
+        for i, g in enumerate(t["grads"]):
+            z = rand(g.shape, F32, 7 * step + i)      # half of `size` to some 4 of it
+            g.copy_((torch.sign(z) * 0.5 + z) * size)
+        old = clone(t)
+        L.adamw_step(plan, step, **{**HYPER, "eps": eps})
+        check(t, old, step, eps=eps)
+
+
+def test_values_without_a_place_for_them():
+    """The table's tensors without m_values are passed over, their neighbours not."""
+    import ctypes
+    L = ops()
+    from sparse_mixture_experts_04_amd import _lib
+    t = tensors([3000], F32, F32, 8)
+    plan = L.adamw_plan(**t)
+    before = clone(t)
+    with pytest.raises(ValueError):
+        L.adamw_state_values(plan)
+    status = _lib.lib.moe_adamw_state_values(ctypes.byref(plan.desc), plan.chunks,
+                                             plan.table.data_ptr(), None)
+    torch.cuda.synchronize()
+    assert status == 0
+    for k in t:
+        assert torch.equal(t[k][0], before[k][0]), k
+
+
+def test_step_on_another_stream():
+    """A plan made on one stream, its steps on another at once."""
+    L = ops()
+    t = tensors([70000, 5], F32, BF, 8)
+    old = clone(t)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan = L.adamw_plan(**t)
+    with torch.cuda.stream(s):
+        L.adamw_step(plan, 4, **HYPER)
+    s.synchronize()
+    check(t, old, 4)
+
+
+def test_same_bits_again():
+    L = ops()
+    for bits in (32, 8):
+        t = tensors([100000], BF, F32, bits)
+        u = clone(t)
+        for x in (t, u):
+            L.adamw_step(L.adamw_plan(**x), 6, **HYPER)
+        for k in t:
+            assert torch.equal(t[k][0], u[k][0]), (bits, k)
+
+
+def test_refusals_of_the_binding():
+    L = ops()
+    t = tensors([300, 20], F32, F32, 32)
+    e = tensors([300, 20], F32, F32, 8)
+    bad = [{**t, "params": [t["params"][0]] * 2}, {**t, "grads": t["grads"][:1]},
+           {**t, "grads": [t["grads"][0], t["grads"][1].to(BF)]},
+           {**t, "params": [t["params"][0], t["params"][1].half()]},
+           {**t, "exp_avg": [t["exp_avg"][0], t["exp_avg"][1][:10]]},
+           {**t, "exp_avg_sq": [x.double() for x in t["exp_avg_sq"]]},
+           {**t, "m_scales": e["m_scales"], "v_scales": e["v_scales"]},
+           {**t, "copies": [x.clone() for x in t["params"]]},
+           {**e, "m_scales": None}, {**e, "v_scales": [x[:1] for x in e["v_scales"]]},
+           {**e, "exp_avg_sq": e["exp_avg"]}, {**e, "m_values": [x.clone() for x in e["params"]]},
+           {**t, "params": [x.cpu() for x in t["params"]]},
+           {**t, "params": [t["params"][0], t["params"][0][5:25]]}]
+    for kw in bad:
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            L.adamw_plan(**kw)
+    bf = tensors([300], BF, F32, 32)
+    with pytest.raises(RuntimeError):                               # copies of bf16 parameters
+        L.adamw_plan(**bf, copies=[x.clone() for x in bf["params"]])
+    plan, old = L.adamw_plan(**t), clone(t)
+    for kw in (dict(step=0), dict(step=1, beta1=1.0), dict(step=1, beta2=-0.5), dict(step=1, eps=-1.0),
+               dict(step=1, lr=float("nan")), dict(step=torch.ones(2, dtype=torch.int64, device="cuda")),
+               dict(step=torch.ones(1, dtype=torch.int32, device="cuda")),
+               dict(step=1, lr=torch.ones(1)), dict(step=1, grad_scale=2.0)):
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            L.adamw_step(plan, **{**HYPER, **kw})
+    with pytest.raises(ValueError):
+        L.adamw_state_values(plan)
+    torch.cuda.synchronize()
+    for k in t:
+        assert all(torch.equal(a, b) for a, b in zip(t[k], old[k]))

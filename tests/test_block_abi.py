@@ -225,6 +225,16 @@ def test_adamw_prepare_checks():
     assert f(ref(adamw(count=0)), None, ref(n), P, 1 << 20, None) == 0 and n.value == 0
 
 
+@pytest.mark.parametrize("first,second", [
+    (dict(p=0x1000, n=100), dict(p=0x1000, n=100)), (dict(p=0x1000, n=100), dict(p=0x118c, n=1)),
+    (dict(p=0x2000, n=10), dict(p=0x1000, n=1025)),
+])
+def test_parameters_that_overlap_are_refused(first, second):
+    n = ctypes.c_int64(0)
+    t = (L.AdamwTensor * 3)(tensor(**first), tensor(n=0), tensor(**second))
+    assert lib.moe_adamw_prepare(ref(adamw(count=3)), t, ref(n), P, 1 << 20, None) == 5
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(step=0), 2), (dict(beta1=1.0), 2), (dict(beta1=-0.1), 2), (dict(beta2=1.0), 2),
     (dict(beta2=float("nan")), 2), (dict(eps=-1e-8), 2), (dict(eps=float("inf")), 2),

@@ -223,3 +223,77 @@ def test_no_rows():
     L.gemm_fp8(a[:0], sa[:0], w, sw, y)
     c, s = L.quantize_fp8(torch.empty((0, 40), device="cuda"))
     assert c.shape == (0, 128) and s.shape == (0, 1)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,offsets", [(256, 520, [3, 200]), (256, 333, [0, 256]), (9, 130, [1, 9]),
+                                         (8, 130, [2, 7]), (100, 2048, [50, 50]), (130, 258, None)])
+def test_slices_of_k(M, N, offsets, dt):
+    """One group of part of the rows, a product cut along K, columns of any number."""
+    assert M < 100 or ops().gemm_fp8_workspace(M, N, 3500).numel() > 1
+    check_product(M, N, 3500, offsets, dt=dt, seed=M + N)
+
+
+@pytest.mark.parametrize("M,N,K,offsets", [
+    (4200, 3104, 256, None), (4100, 3100, 300, [2, 4099]),
+    (6000, 2200, 640, [0, 1, 1, 2048, 2305, 5990]), (25000, 600, 128, None)])
+def test_large_tiles(M, N, K, offsets):
+    """256 x 256 tiles: last tiles that are not whole, groups that end inside one."""
+    check_product(M, N, K, offsets, dt=BF, seed=M)
+
+
+def test_two_products_at_once():
+    L = ops()
+    sets = [operands(256, 2048, 3584, 1, seed=s) for s in (1, 5)]
+    want = [torch.empty((256, 2048), dtype=BF, device="cuda") for _ in sets]
+    got = [torch.zeros_like(t) for t in want]
+    for s, y in zip(sets, want):
+        L.gemm_fp8(*s, y)
+    wss = [L.gemm_fp8_workspace(256, 2048, 3584) for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, y, ws, st in zip(sets, got, wss, streams):
+            with torch.cuda.stream(st):
+                L.gemm_fp8(*s, y, ws=ws)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_a_row_does_not_depend_on_the_batch_of_its_tile():
+    """Rows of one group beside others of any values: same bits."""
+    a, sa, w, sw = operands(300, 520, 640, 1)
+    y = check_product(300, 520, 640, ops_=(a, sa, w, sw), dt=BF)
+    a2, sa2 = a.clone(), sa.clone()
+    a2.view(torch.uint8)[100:] = 0x7f          # NaN
+    y2 = torch.empty_like(y)
+    ops().gemm_fp8(a2, sa2, w, sw, y2)
+    assert torch.equal(y[:100], y2[:100]) and torch.isnan(y2[100:]).all()
+
+
+def test_refusals_of_the_binding():
+    L = ops()
+    a, sa, w, sw = operands(20, 40, 200, 2)
+    off = torch.tensor([0, 9, 20], dtype=torch.int32, device="cuda")
+    y = torch.zeros((20, 40), device="cuda")
+    with pytest.raises(RuntimeError):
+        L.gemm_fp8(a, sa, w, sw, y)                                # offsets missing
+    for args in ((a.view(torch.uint8), sa, w, sw, y), (a[:, :128], sa, w, sw, y),
+                 (a[:, :200], sa, w, sw, y), (a, sa[:, :1], w, sw, y), (a, sa.to(BF), w, sw, y),
+                 (a, sa, w[:, :30], sw, y), (a, sa, w, sw[:, :, :1], y), (a, sa, w[0], sw, y),
+                 (a, sa, w, sw, y[:10]), (a, sa, w, sw, y.half()), (a, sa, w, sw, y.t())):
+        with pytest.raises((TypeError, ValueError)):
+            L.gemm_fp8(*args, offsets=off)
+    for x in (y.half(), y.long(), y.t(), torch.zeros((), device="cuda"), y[:, :0]):
+        with pytest.raises((TypeError, ValueError)):
+            L.quantize_fp8(x)
+    with pytest.raises((TypeError, ValueError)):
+        L.quantize_fp8(y, codes=torch.empty((20, 40), dtype=FP8, device="cuda"))
+    with pytest.raises((TypeError, ValueError)):
+        L.quantize_fp8_weights(y)
+    flat = torch.zeros(20 * 128 + 8, dtype=torch.uint8, device="cuda")
+    with pytest.raises(RuntimeError):                              # codes not on 16 bytes
+        L.quantize_fp8(y, codes=flat[8:].view(20, 128).view(FP8))
+    torch.cuda.synchronize()
+    assert not y.any() and not flat.any()

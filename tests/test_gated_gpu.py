@@ -245,3 +245,100 @@ def test_stream_and_graph():
         for n, t in zip(names, out):
             assert torch.equal(t, want[n]), (i, n)
         both(x, wg, wu, dh, [0, 90, 200])
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M", [15, 16, 17, 18, 31, 32, 33, 48])
+def test_row_counts_where_the_kernel_changes(M, dt):
+    x, wg, wu, dh = inputs(M, 1032, 200, 1, dt, seed=M)
+    check(x, wg, wu, dh, None, both(x, wg, wu, dh, None))
+
+
+@pytest.mark.parametrize("M,offsets", [(200, [5, 190]), (200, [0, 200]), (200, [7, 7]), (70, [69, 70])])
+def test_slices_of_k_with_rows_outside(M, offsets):
+    """One group of part of the rows, where a product is cut along K."""
+    from sparse_mixture_experts_04_amd import ops
+    assert ops.gated_ff_workspace(M, 2000, 504, 1, BF, "cuda").numel() > 1
+    x, wg, wu, dh = inputs(M, 2000, 504, 1, BF, seed=M)
+    check(x, wg, wu, dh, offsets, both(x, wg, wu, dh, offsets))
+
+
+def test_many_large_tiles():
+    """Gradients in 256 x 256 tiles: ragged groups, one without and one of a single row,
+    rows that no step of 64 divides, columns past the last whole tile."""
+    n = [300, 0, 1, 777, 512, 255, 257, 1111, 640, 900, 333, 1024, 700, 463]
+    off = [9]
+    for k in n:
+        off.append(off[-1] + k)
+    M = off[-1] + 18
+    x, wg, wu, dh = inputs(M, 2056, 264, len(n), BF, seed=3)
+    check(x, wg, wu, dh, off, both(x, wg, wu, dh, off))
+
+
+def test_one_group_in_large_tiles():
+    x, wg, wu, dh = inputs(7400, 2056, 168, 1, BF, seed=4)
+    check(x, wg, wu, dh, [3, 7390], both(x, wg, wu, dh, [3, 7390]))
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each: neither disturbs the other."""
+    L = ops()
+    sets = [inputs(256, 2048, 512, 1, BF, seed=s) for s in (1, 2)]
+    want = [both(*s, None) for s in sets]
+    outs = [[torch.zeros_like(t) for t in (s[3], s[0], s[1], s[2])] for s in sets]
+    pres = [torch.zeros((256, 1024), device="cuda") for _ in sets]
+    wss = [L.gated_ff_workspace(256, 2048, 512, 1, BF, "cuda", backward=True) for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (x, wg, wu, dh), o, pre, ws, st in zip(sets, outs, pres, wss, streams):
+            with torch.cuda.stream(st):
+                L.gated_ff(x, wg, wu, o[0], pre=pre, ws=ws)
+                L.gated_ff_backward(x, wg, wu, dh, *o[1:], pre=pre, ws=ws)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for t, n in zip(o, ("h", "dx", "dw_gate", "dw_up")):
+            assert torch.equal(t, w[n]), n
+
+
+def test_masked_rows():
+    """Rows of zeros with gradients of zeros (padding inside a group) add nothing; an
+    infinite x makes its own row NaN or infinite, no other."""
+    x, wg, wu, dh = inputs(120, 264, 72, 1, BF, seed=8)
+    x[40:80] = 0
+    dh[40:80] = 0
+    got = both(x, wg, wu, dh, None)
+    check(x, wg, wu, dh, None, got)
+    assert not got["h"][40:80].any() and not got["dx"][40:80].any()
+    bad = x.clone()
+    bad[3, 5] = float("inf")
+    h = both(bad, wg, wu, dh, None)["h"]
+    keep = [r for r in range(120) if r != 3]
+    assert torch.equal(h[keep], got["h"][keep]) and not torch.isfinite(h[3].float()).any()
+
+
+def test_refusals_of_the_binding():
+    L = ops()
+    x, wg, wu, dh = inputs(20, 64, 32, 2, BF)
+    off = torch.tensor([0, 9, 20], dtype=torch.int32, device="cuda")
+    h = torch.zeros_like(dh)
+    with pytest.raises(RuntimeError):                              # offsets for two groups
+        L.gated_ff(x, wg, wu, h)
+    for kw in (dict(offsets=off[:2]), dict(offsets=off.long()), dict(offsets=off.cpu()),
+               dict(offsets=off, pre=torch.zeros((20, 32), device="cuda")),
+               dict(offsets=off, pre=torch.zeros((20, 64), dtype=BF, device="cuda")),
+               dict(offsets=off, ws=torch.zeros(100, device="cuda"))):
+        with pytest.raises((TypeError, ValueError)):
+            L.gated_ff(x, wg, wu, h, **kw)
+    for args in ((x.float(), wg, wu, h), (x, wg, wu.float(), h), (x, wg[:, :, :32], wu, h),
+                 (x, wg, wu[:1], h), (x, wg, wu, h.float()), (x, wg, wu, h[:, :16]),
+                 (x.t().contiguous().t(), wg, wu, h), (x, wg.half(), wu, h), (x[0], wg, wu, h)):
+        with pytest.raises((TypeError, ValueError)):
+            L.gated_ff(*args, offsets=off)
+    with pytest.raises(RuntimeError):                              # one gradient of two
+        L.gated_ff_backward(x, wg, wu, dh, None, torch.zeros_like(wg), None, offsets=off)
+    with pytest.raises(RuntimeError):
+        L.gated_ff_backward(x, wg, wu, dh, torch.zeros_like(x), None, None, offsets=off,
+                            ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert not h.any()
