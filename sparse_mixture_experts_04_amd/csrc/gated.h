@@ -37,8 +37,14 @@ __device__ __forceinline__ float sigmoid(float a) { return 1.0f / (1.0f + expf(-
 
 // The kernel of one of the block's products.
 hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st);
-// Any sizes, either type, on the fp32 matrix cores (gated_tile.hip).
+// The gradients that are wanted, from pre and dh.
+hipError_t launch_gated_gradients(const GatedArgs& a, hipStream_t st);
+// Any sizes, either type, on the fp32 matrix cores (gated_tile.hip): in tiles; in blocks
+// of 32 x 32 whose K the waves share; all gradients in one launch of such blocks
+// (from_pre: da and du made where they are used, otherwise they lie in dau).
 hipError_t launch_gated_tile(const GatedArgs& a, GatedPart part, hipStream_t st);
+hipError_t launch_gated_small(const GatedArgs& a, GatedPart part, hipStream_t st);
+hipError_t launch_gated_small_grads(const GatedArgs& a, bool from_pre, hipStream_t st);
 // bf16 rows of 16-byte pieces, in tiles of 128 or 256 rows (gated_big.hip).
 hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, hipStream_t st);
 int gated_splits(int M, int d, int F, int E, GatedPart part);

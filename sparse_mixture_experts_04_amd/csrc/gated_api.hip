@@ -136,10 +136,10 @@ moe_status moe_gated_ff_backward(const moe_gated_ff_desc* desc, const void* x, c
       // h is not wanted: the product runs again for a and u alone
       e = launch_gated(a, GatedPart::kForward, stream);
     }
-    if (e == hipSuccess) e = launch_gated_dau(a, stream);
-    if (e == hipSuccess && dx) e = launch_gated(a, GatedPart::kDx, stream);
+    if (e == hipSuccess) e = launch_gated_gradients(a, stream);
+  } else if (dw_gate) {
+    e = launch_gated(a, GatedPart::kDw, stream);
   }
-  if (e == hipSuccess && dw_gate) e = launch_gated(a, GatedPart::kDw, stream);
   return hip_status(e);
 }
 

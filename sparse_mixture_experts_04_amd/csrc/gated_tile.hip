@@ -120,113 +120,182 @@ __global__ __launch_bounds__(kT32Threads) void gated_tile_kernel(GatedArgs p) {
   }
 }
 
+// da and du of a value of a, u and dh, rounded to T (the products that take them take
+// T).
+template <typename T>
+__device__ __forceinline__ void gate_grad(float a, float u, float g, float& da, float& du) {
+  const float s = sigmoid(a);
+  da = g * u * s * (1.0f + a * (1.0f - s));
+  du = g * a * s;
+  if constexpr (sizeof(T) == 2) {
+    da = __uint_as_float(static_cast<uint32_t>(f32_to_bf16(da)) << 16);
+    du = __uint_as_float(static_cast<uint32_t>(f32_to_bf16(du)) << 16);
+  }
+}
+
 // The same for results of few tiles, where one step after another of a large tile is
 // waiting for memory: a workgroup's 8 waves share K of one 32 x 32 block (forward: 32
 // rows x 16 columns), each from global memory straight into registers, and add their
 // sums through LDS in order.  An instruction's two k are 4 apart (lane / 32), so that
 // an operand contiguous along K is read 4 values a lane.
+// FROM_PRE: dau is not there, its values are made of pre's and dh's where they are
+// used.
 constexpr int kSmallWaves = 8;
-template <typename T, GatedPart PART>
-__global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(GatedArgs p) {
-  __shared__ float red[kSmallWaves][16][64];
-  __shared__ EntryPlan plan;
+typedef float SmallSums[kSmallWaves][16][64];
+
+template <GatedPart PART>
+__device__ __forceinline__ long long small_items(const GatedArgs& p, const EntryPlan& plan) {
+  constexpr int NOUT = PART == GatedPart::kForward ? 16 : 32;
+  const int n_tiles = ((PART == GatedPart::kForward ? p.F : p.d) + NOUT - 1) / NOUT;
+  return (PART == GatedPart::kDw ? static_cast<long long>(p.E) * ((2 * p.F + 31) / 32)
+                                 : static_cast<long long>(plan.start[p.E])) * n_tiles;
+}
+
+template <typename T, GatedPart PART, bool FROM_PRE>
+__device__ __forceinline__ void small_item(const GatedArgs& p, const EntryPlan& plan, long long it,
+                                           SmallSums& red) {
   constexpr bool FWD = PART == GatedPart::kForward, DW = PART == GatedPart::kDw;
   constexpr int NOUT = FWD ? 16 : 32;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r32 = lane & 31, half = lane >> 5;
-  make_entries<64 * kSmallWaves, 32, kMaxGroups>(p, plan);
   const int d = p.d, F = p.F, F2 = 2 * F;
   const int n_tiles = ((FWD ? F : d) + NOUT - 1) / NOUT, m_tiles = (F2 + 31) / 32;
-  const long long total = (DW ? static_cast<long long>(p.E) * m_tiles
-                              : static_cast<long long>(plan.start[p.E])) * n_tiles;
   const T* x = static_cast<const T*>(p.x);
   const T* dau = static_cast<const T*>(p.dau);
-  const bool vx = d % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T)) == 0;
-  const bool vw = d % 4 == 0 && (reinterpret_cast<uintptr_t>(p.w_gate) |
-                                 reinterpret_cast<uintptr_t>(p.w_up)) % (4 * sizeof(T)) == 0;
+  const T* dh = static_cast<const T*>(p.dh);
+  auto on4 = [](const void* b) { return reinterpret_cast<uintptr_t>(b) % (4 * sizeof(T)) == 0; };
+  const bool vx = d % 4 == 0 && on4(x), vw = d % 4 == 0 && on4(p.w_gate) && on4(p.w_up);
   const bool vd = F % 2 == 0;
+  const bool vp = F % 4 == 0 && on4(dh) && reinterpret_cast<uintptr_t>(p.pre) % 16 == 0;
 
-  for (long long it = blockIdx.x; it < total; it += gridDim.x) {
-    const int ent = static_cast<int>(it / n_tiles), n0 = static_cast<int>(it % n_tiles) * NOUT;
-    const int g = DW ? ent / m_tiles : entry_group(plan, p.E, ent);
-    const int m0 = (DW ? ent % m_tiles : ent - plan.start[g]) * 32;
-    const int rows = DW ? min(F2 - m0, 32) : min(plan.rows[g] - m0, 32);
-    const long long row0 = plan.lo[g];
-    const size_t wat = static_cast<size_t>(g) * F * d;
-    const T* wg = static_cast<const T*>(p.w_gate) + wat;
-    const T* wu = static_cast<const T*>(p.w_up) + wat;
-    const int K = FWD ? d : DW ? plan.rows[g] : F2;
-    const int chunks = (K + 7) / 8;
-    const int c0 = chunks * wave / kSmallWaves, c1 = chunks * (wave + 1) / kSmallWaves;
-    // this lane's row and column of the operands
-    const long long row = row0 + m0 + min(r32, rows - 1);
-    const T* xr = x + row * d;
-    const T* dr = dau + row * F2;
-    const T* wr = (r32 & 16 ? wu : wg) + static_cast<size_t>(min(n0 + (r32 & 15), F - 1)) * d;
-    const int mc = min(m0 + r32, F2 - 1), nc = min(n0 + r32, d - 1);
-    f32x16_t acc;
+  const int ent = static_cast<int>(it / n_tiles), n0 = static_cast<int>(it % n_tiles) * NOUT;
+  const int g = DW ? ent / m_tiles : entry_group(plan, p.E, ent);
+  const int m0 = (DW ? ent % m_tiles : ent - plan.start[g]) * 32;
+  const int rows = DW ? min(F2 - m0, 32) : min(plan.rows[g] - m0, 32);
+  const long long row0 = plan.lo[g];
+  const size_t wat = static_cast<size_t>(g) * F * d;
+  const T* wg = static_cast<const T*>(p.w_gate) + wat;
+  const T* wu = static_cast<const T*>(p.w_up) + wat;
+  const int K = FWD ? d : DW ? plan.rows[g] : F2;
+  const int chunks = (K + 7) / 8;
+  const int c0 = chunks * wave / kSmallWaves, c1 = chunks * (wave + 1) / kSmallWaves;
+  // this lane's row and column of the operands
+  const long long row = row0 + m0 + min(r32, rows - 1);
+  const T* xr = x + row * d;
+  const T* wr = (r32 & 16 ? wu : wg) + static_cast<size_t>(min(n0 + (r32 & 15), F - 1)) * d;
+  const int mc = min(m0 + r32, F2 - 1), nc = min(n0 + r32, d - 1);
+  // value f of [da | du] of a row
+  auto grad = [&](long long r, int f) __attribute__((always_inline)) {
+    const int c = f < F ? f : f - F;
+    float da, du;
+    gate_grad<T>(p.pre[r * F2 + c], p.pre[r * F2 + F + c], ActTraits<T>::load(dh + r * F + c), da, du);
+    return f < F ? da : du;
+  };
+  f32x16_t acc;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+  for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
 #pragma unroll 4
-    for (int c = c0; c < c1; ++c) {
-      const int k = c * 8 + 4 * half;
-      float a[4], b[4];
-      if constexpr (FWD) {
-        load4(xr + k, d - k, vx, a);
-        load4(wr + k, d - k, vw, b);
-      } else if constexpr (!DW) {
-        load4(dr + k, F2 - k, vd, a);
+  for (int c = c0; c < c1; ++c) {
+    const int k = c * 8 + 4 * half;
+    float a[4], b[4];
+    if constexpr (FWD) {
+      load4(xr + k, d - k, vx, a);
+      load4(wr + k, d - k, vw, b);
+    } else if constexpr (!DW) {
+      if constexpr (!FROM_PRE) {
+        load4(dau + row * F2 + k, F2 - k, vd, a);
+      } else if (vp) {
+        const int at = k < F ? k : k - F;
+        float ga[4], gu[4], gh[4];
+        load4(p.pre + row * F2 + at, F - at, true, ga);
+        load4(p.pre + row * F2 + F + at, F - at, true, gu);
+        load4(dh + row * F + at, F - at, true, gh);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int f = k + e;
-          const T* w = f < F ? wg + static_cast<size_t>(f) * d : wu + static_cast<size_t>(f - F) * d;
-          b[e] = f < F2 ? ActTraits<T>::load(w + nc) : 0.0f;
+          float da, du;
+          gate_grad<T>(ga[e], gu[e], gh[e], da, du);
+          a[e] = k < F ? da : du;
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] = k + e < K ? ActTraits<T>::load(dau + (row0 + k + e) * F2 + mc) : 0.0f;
-          b[e] = k + e < K ? ActTraits<T>::load(x + (row0 + k + e) * d + nc) : 0.0f;
-        }
+        for (int e = 0; e < 4; ++e) a[e] = k + e < F2 ? grad(row, k + e) : 0.0f;
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b[e], a[e], acc, 0, 0, 0);
-    }
-    __syncthreads();  // the block before is done with red
-#pragma unroll
-    for (int r = 0; r < 16; ++r) red[wave][r][lane] = acc[r];
-    __syncthreads();
-    // thread: lane l's registers r and r + 8 of all waves
-    const int r = wave;
-    float v[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kSmallWaves; ++w) {
-      v[0] += red[w][r][lane];
-      v[1] += red[w][r + 8][lane];
-    }
-    if (r32 >= rows) continue;
-    if constexpr (FWD) {
-      const int c = n0 + 8 * (r / 4) + 4 * half + r % 4;
-      if (c >= F) continue;
-      const size_t at = static_cast<size_t>(row0 + m0 + r32);
-      if (p.h) ActTraits<T>::store(static_cast<T*>(p.h) + at * F + c, v[0] * sigmoid(v[0]) * v[1]);
-      if (p.pre) {
-        p.pre[at * F2 + c] = v[0];
-        p.pre[at * F2 + F + c] = v[1];
+      for (int e = 0; e < 4; ++e) {
+        const int f = k + e;
+        const T* w = f < F ? wg + static_cast<size_t>(f) * d : wu + static_cast<size_t>(f - F) * d;
+        b[e] = f < F2 ? ActTraits<T>::load(w + nc) : 0.0f;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = n0 + 8 * (r / 4 + 2 * i) + 4 * half + r % 4;
-        if (c >= d) continue;
-        const int n = m0 + r32;
-        T* out = !DW ? static_cast<T*>(p.dx) + static_cast<size_t>(row0 + m0 + r32) * d
-                 : n < F ? static_cast<T*>(p.dw_gate) + wat + static_cast<size_t>(n) * d
-                         : static_cast<T*>(p.dw_up) + wat + static_cast<size_t>(n - F) * d;
-        ActTraits<T>::store(out + c, v[i]);
+      for (int e = 0; e < 4; ++e) {
+        a[e] = k + e >= K ? 0.0f
+               : FROM_PRE ? grad(row0 + k + e, mc)
+                          : ActTraits<T>::load(dau + (row0 + k + e) * F2 + mc);
+        b[e] = k + e < K ? ActTraits<T>::load(x + (row0 + k + e) * d + nc) : 0.0f;
       }
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b[e], a[e], acc, 0, 0, 0);
+  }
+  __syncthreads();  // the block before is done with red
+#pragma unroll
+  for (int r = 0; r < 16; ++r) red[wave][r][lane] = acc[r];
+  __syncthreads();
+  // thread: lane l's registers r and r + 8 of all waves
+  const int r = wave;
+  float v[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int w = 0; w < kSmallWaves; ++w) {
+    v[0] += red[w][r][lane];
+    v[1] += red[w][r + 8][lane];
+  }
+  if (r32 >= rows) return;
+  if constexpr (FWD) {
+    const int c = n0 + 8 * (r / 4) + 4 * half + r % 4;
+    if (c >= F) return;
+    const size_t at = static_cast<size_t>(row0 + m0 + r32);
+    if (p.h) ActTraits<T>::store(static_cast<T*>(p.h) + at * F + c, v[0] * sigmoid(v[0]) * v[1]);
+    if (p.pre) {
+      p.pre[at * F2 + c] = v[0];
+      p.pre[at * F2 + F + c] = v[1];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = n0 + 8 * (r / 4 + 2 * i) + 4 * half + r % 4;
+      if (c >= d) continue;
+      const int n = m0 + r32;
+      T* out = !DW ? static_cast<T*>(p.dx) + static_cast<size_t>(row0 + m0 + r32) * d
+               : n < F ? static_cast<T*>(p.dw_gate) + wat + static_cast<size_t>(n) * d
+                       : static_cast<T*>(p.dw_up) + wat + static_cast<size_t>(n - F) * d;
+      ActTraits<T>::store(out + c, v[i]);
+    }
+  }
+}
+
+template <typename T, GatedPart PART>
+__global__ __launch_bounds__(64 * kSmallWaves) void gated_small_kernel(GatedArgs p) {
+  __shared__ SmallSums red;
+  __shared__ EntryPlan plan;
+  make_entries<64 * kSmallWaves, 32, kMaxGroups>(p, plan);
+  const long long total = small_items<PART>(p, plan);
+  for (long long it = blockIdx.x; it < total; it += gridDim.x)
+    small_item<T, PART, false>(p, plan, it, red);
+}
+
+// All gradients in one launch.
+template <typename T, bool FROM_PRE>
+__global__ __launch_bounds__(64 * kSmallWaves) void gated_small_grads_kernel(GatedArgs p) {
+  __shared__ SmallSums red;
+  __shared__ EntryPlan plan;
+  make_entries<64 * kSmallWaves, 32, kMaxGroups>(p, plan);
+  const long long dx = p.dx ? small_items<GatedPart::kDx>(p, plan) : 0;
+  const long long total = dx + (p.dw_gate ? small_items<GatedPart::kDw>(p, plan) : 0);
+  for (long long it = blockIdx.x; it < total; it += gridDim.x) {
+    if (it < dx) small_item<T, GatedPart::kDx, FROM_PRE>(p, plan, it, red);
+    else small_item<T, GatedPart::kDw, FROM_PRE>(p, plan, it - dx, red);
   }
 }
 
@@ -259,9 +328,7 @@ __global__ __launch_bounds__(256) void gated_dau_kernel(GatedArgs p, int quads) 
     load4(dh + row * F + c, n, vec, g);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float s = sigmoid(a[e]);
-      da[e] = g[e] * u[e] * s * (1.0f + a[e] * (1.0f - s));
-      du[e] = g[e] * a[e] * s;
+      gate_grad<T>(a[e], u[e], g[e], da[e], du[e]);
     }
     T* o = dau + row * 2 * F + c;
     if (vec) {
@@ -280,17 +347,13 @@ __global__ __launch_bounds__(256) void gated_dau_kernel(GatedArgs p, int quads) 
 
 template <typename T, GatedPart PART>
 void run(const GatedArgs& a, hipStream_t st) {
-  const int cols = PART == GatedPart::kForward ? 2 * a.F : a.d;
+  // tiles of 64 while 128 would leave compute units without one
+  const long long cols = PART == GatedPart::kForward ? 2 * a.F : a.d;
   const long long rows = PART == GatedPart::kDw ? 2LL * a.F * a.E : a.M;
-  // tiles of 64 while 128 would leave compute units without one; blocks of 32 whose K
-  // eight waves share while tiles of 64 would.  Measured (us, tiles of 64 / blocks of
-  // 32): M=333 d=520 F=264 fp32 forward 24 / 9, dx 32 / 10.5, dW 19 / 10; M=300
-  // d=2000 F=500 bf16 forward 90 / 34.
-  const long long of64 = (rows + 63) / 64 * ((cols + 63) / 64);
-  const long long of128 = (rows + 127) / 128 * ((cols + 127) / 128);
-  if (of64 < 256) gated_small_kernel<T, PART><<<1024, 64 * kSmallWaves, 0, st>>>(a);
-  else if (of128 < 256) gated_tile_kernel<1, T, PART><<<1024, kT32Threads, 0, st>>>(a);
-  else gated_tile_kernel<2, T, PART><<<1024, kT32Threads, 0, st>>>(a);
+  if ((rows + 127) / 128 * ((cols + 127) / 128) < 256)
+    gated_tile_kernel<1, T, PART><<<1024, kT32Threads, 0, st>>>(a);
+  else
+    gated_tile_kernel<2, T, PART><<<1024, kT32Threads, 0, st>>>(a);
 }
 
 template <typename T>
@@ -300,11 +363,36 @@ void run(const GatedArgs& a, GatedPart part, hipStream_t st) {
   else run<T, GatedPart::kDw>(a, st);
 }
 
+constexpr int kSmallGrid = 1024;
+
+template <typename T>
+void run_small(const GatedArgs& a, GatedPart part, hipStream_t st) {
+  auto go = [&](auto kernel) { kernel<<<kSmallGrid, 64 * kSmallWaves, 0, st>>>(a); };
+  if (part == GatedPart::kForward) go(gated_small_kernel<T, GatedPart::kForward>);
+  else if (part == GatedPart::kDx) go(gated_small_kernel<T, GatedPart::kDx>);
+  else go(gated_small_kernel<T, GatedPart::kDw>);
+}
+
 }  // namespace
 
 hipError_t launch_gated_tile(const GatedArgs& a, GatedPart part, hipStream_t st) {
   if (a.bf16) run<bf16_t>(a, part, st);
   else run<float>(a, part, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_small(const GatedArgs& a, GatedPart part, hipStream_t st) {
+  if (a.bf16) run_small<bf16_t>(a, part, st);
+  else run_small<float>(a, part, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_small_grads(const GatedArgs& a, bool from_pre, hipStream_t st) {
+  auto go = [&](auto kernel) { kernel<<<kSmallGrid, 64 * kSmallWaves, 0, st>>>(a); };
+  if (a.bf16)
+    from_pre ? go(gated_small_grads_kernel<bf16_t, true>) : go(gated_small_grads_kernel<bf16_t, false>);
+  else
+    from_pre ? go(gated_small_grads_kernel<float, true>) : go(gated_small_grads_kernel<float, false>);
   return hipGetLastError();
 }
 

@@ -229,9 +229,24 @@ def test_no_rows():
 @pytest.mark.parametrize("M,N,offsets", [(256, 520, [3, 200]), (256, 333, [0, 256]), (9, 130, [1, 9]),
                                          (8, 130, [2, 7]), (100, 2048, [50, 50]), (130, 258, None)])
 def test_slices_of_k(M, N, offsets, dt):
-    """One group of part of the rows, a product cut along K, columns of any number."""
-    assert M < 100 or ops().gemm_fp8_workspace(M, N, 3500).numel() > 1
+    """One group of part of the rows, columns of any number."""
     check_product(M, N, 3500, offsets, dt=dt, seed=M + N)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,offsets", [(256, 2048, [3, 200]), (256, 1999, None), (700, 1030, [0, 699]),
+                                         (300, 2048, [50, 50])])
+def test_slices_of_k_in_memory(M, N, offsets, dt):
+    """A product whose tiles are cut along K, their sums in the workspace."""
+    assert ops().gemm_fp8_workspace(M, N, 3500).numel() > 1
+    check_product(M, N, 3500, offsets, dt=dt, seed=M + N)
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K,offsets", [(3, 5000, 3000, None), (8, 7168, 1920, [1, 8]),
+                                           (5, 900, 5000, [0, 2, 2, 5])])
+def test_few_rows_of_many_weights(M, N, K, offsets, dt):
+    check_product(M, N, K, offsets, dt=dt, seed=M + N)
 
 
 @pytest.mark.parametrize("M,N,K,offsets", [
