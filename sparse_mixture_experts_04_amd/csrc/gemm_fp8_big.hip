@@ -18,6 +18,7 @@
 // step, 32 row scales and the two weight scales of the tile into the stage's slot by
 // one 4-byte direct-to-LDS load, so that no load of theirs disturbs the count of
 // loads in flight.
+#include <algorithm>
 #include <cmath>
 
 #include "fp8.h"
@@ -536,12 +537,12 @@ __global__ __launch_bounds__(256) void gemm_fp8_reduce_kernel(Fp8Args p) {
 // have none.  Estimated (us): the walk, and for slices 6 and their sums written and
 // read at 4 TB/s.  Measured (us, one walk / slices): N=2048 K=7168 128 rows 46 / 21.5,
 // 256 rows 47 / 24, 512 rows 46 / 29, 1024 rows 47 / 38; N=K=7168 256 rows 47 / 36.
-int fp8_splits(int M, int N, int Kp, int E) {
-  if (E != 1) return 1;
-  const double items = std::ceil(M / 128.0) * std::ceil(N / 256.0), nk = Kp / kFp8Block;
+static int splits_of(int M, int N, int Kp, int E, double& time) {
+  const double entries = std::ceil(M / 128.0) + (E > 1 ? std::min(M, E) : 0);
+  const double items = entries * std::ceil(N / 256.0), nk = Kp / kFp8Block;
   int best = 1;
-  double time = nk * 0.75 * std::ceil(items / 256.0);
-  for (int s = 2; s <= 16 && s * 2 <= nk; ++s) {
+  time = nk * 0.75 * std::ceil(items / 256.0);
+  for (int s = 2; E == 1 && s <= 16 && s * 2 <= nk; ++s) {
     const double t = 6.0 + std::ceil(nk / s) * 0.75 * std::ceil(items * s / 256.0) +
                      8.0 * s * M * N / 4e6;
     if (t < 0.9 * time) {
@@ -550,6 +551,16 @@ int fp8_splits(int M, int N, int Kp, int E) {
     }
   }
   return best;
+}
+
+int fp8_splits(int M, int N, int Kp, int E) {
+  double time;
+  return splits_of(M, N, Kp, E, time);
+}
+
+double fp8_tiles_time(int M, int N, int Kp, int E) {
+  double time;
+  return (splits_of(M, N, Kp, E, time) > 1 ? 12.0 : 6.5) + time;
 }
 
 hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st) {

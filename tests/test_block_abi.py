@@ -160,9 +160,9 @@ def test_gemm_fp8_checks():
     assert g(ref(d), P, P, P, P, None, EIGHT, P, 0, None) == 5
     grouped = L.GemmFp8Desc(4, 8, 100, 2, L.BF16)
     assert g(ref(grouped), P, P, P, P, None, P, P, 0, None) == 1    # offsets missing
-    sliced = L.GemmFp8Desc(256, 2048, 7168, 1, L.BF16)
+    sliced = L.GemmFp8Desc(1024, 2048, 7168, 1, L.BF16)
     need = size_of(lib.moe_gemm_fp8_workspace_size, sliced)[1]
-    assert need >= 2 * 256 * 2048 * 4 and need % (256 * 2048 * 4) == 0
+    assert need >= 2 * 1024 * 2048 * 4 and need % (1024 * 2048 * 4) == 0
     assert g(ref(sliced), P, P, P, P, None, P, P, need - 1, None) == 4
     assert g(ref(sliced), P, P, P, P, None, P, None, need, None) == 4
     assert g(ref(sliced), P, P, P, P, None, P, EIGHT, need, None) == 5

@@ -234,12 +234,14 @@ def test_slices_of_k(M, N, offsets, dt):
 
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("M,N,offsets", [(256, 2048, [3, 200]), (256, 1999, None), (700, 1030, [0, 699]),
-                                         (300, 2048, [50, 50])])
-def test_slices_of_k_in_memory(M, N, offsets, dt):
-    """A product whose tiles are cut along K, their sums in the workspace."""
-    assert ops().gemm_fp8_workspace(M, N, 3500).numel() > 1
-    check_product(M, N, 3500, offsets, dt=dt, seed=M + N)
+@pytest.mark.parametrize("M,N,K,offsets", [
+    (256, 2048, 3500, [3, 200]), (256, 1999, 3500, None), (700, 1030, 3500, [0, 699]),
+    (1024, 2048, 7000, [3, 1000]), (1000, 1999, 7000, None), (1100, 2050, 7000, [50, 50])])
+def test_slices_of_k_in_memory(M, N, K, offsets, dt):
+    """A product whose tiles are cut along K, their sums in the workspace (the last
+    three; smaller ones are not cut)."""
+    assert M < 1000 or ops().gemm_fp8_workspace(M, N, K).numel() > 1
+    check_product(M, N, K, offsets, dt=dt, seed=M + N)
 
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
