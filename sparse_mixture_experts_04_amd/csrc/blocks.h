@@ -1,4 +1,4 @@
-// Internal declarations of the stream kernel (few rows a group).
+// Internal declarations of the products in blocks of 32 rows (blocks.hip).
 #pragma once
 
 #include "common.h"
@@ -6,9 +6,9 @@
 
 namespace moe {
 
-enum class StreamKind { kFp8, kGatedBf16, kGatedF32 };
+enum class BlockKind { kFp8, kGatedBf16, kGatedF32 };
 
-struct StreamArgs {
+struct BlockArgs {
   const void* a;          // activations [M, K]
   const void* w0;         // weights [E, N, K]; gated: Wg and Wu
   const void* w1;
@@ -22,7 +22,11 @@ struct StreamArgs {
   bool out_bf16;          // kFp8
 };
 
-// Rows of a and the weights start on 16 bytes and are a multiple of it long.
-hipError_t launch_stream(const StreamArgs& a, StreamKind kind, hipStream_t st);
+// Rows of a and of the weights start on 16 bytes and are a multiple of it long.
+hipError_t launch_blocks(const BlockArgs& a, BlockKind kind, hipStream_t st);
+
+// Estimated time of it (us): two workgroups a compute unit at a time, and for each block
+// a start, an end and a step for every 128 bytes of a row.
+double blocks_time(int M, int N, long long row_bytes, int E, bool gated);
 
 }  // namespace moe

@@ -32,15 +32,12 @@ struct Fp8Args {
   int splits;             // slices of K (fp8_splits)
   bool out_bf16;
 };
-// Whether a product goes through the stream of its weights (stream.hip).
-bool fp8_streams(int M);
-// Whether it goes through blocks of 32 x 32 whose K the waves share (gemm_fp8_small.hip).
-bool fp8_small(int M, int N, int Kp, int E);
+// Whether a product goes in blocks of 32 rows (blocks.hip).
+bool fp8_blocks(int M, int N, int Kp, int E);
 int fp8_splits(int M, int N, int Kp, int E);
 // Estimated time of the 128-row tiles (us).
 double fp8_tiles_time(int M, int N, int Kp, int E);
 hipError_t launch_gemm_fp8(const Fp8Args& a, hipStream_t st);
-hipError_t launch_gemm_fp8_small(const Fp8Args& a, hipStream_t st);
 hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st);
 
 }  // namespace moe

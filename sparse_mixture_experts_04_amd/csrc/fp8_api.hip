@@ -32,7 +32,7 @@ moe_status check_gemm(const moe_gemm_fp8_desc* d) {
 // Slices of K whose sums the workspace holds (1: none).
 int slices(const moe_gemm_fp8_desc* d) {
   const int kp = static_cast<int>(fp8_row(d->K));
-  return d->M == 0 || d->N == 0 || fp8_streams(d->M) || fp8_small(d->M, d->N, kp, d->E)
+  return d->M == 0 || d->N == 0 || fp8_blocks(d->M, d->N, kp, d->E)
              ? 1
              : fp8_splits(d->M, d->N, kp, d->E);
 }

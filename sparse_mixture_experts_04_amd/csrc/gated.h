@@ -48,6 +48,8 @@ hipError_t launch_gated_small_grads(const GatedArgs& a, bool from_pre, hipStream
 // bf16 rows of 16-byte pieces, in tiles of 128 or 256 rows (gated_big.hip).
 hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, hipStream_t st);
 int gated_splits(int M, int d, int F, int E, GatedPart part);
+// Estimated time of the 128-row tiles (us).
+double gated_tiles_time(int M, int d, int F, int E, GatedPart part);
 // Floats of GatedArgs::part that a product may need (0: none).
 size_t gated_part_floats(int M, int d, int F, int E, bool bf16, GatedPart part);
 // pre, dh -> dau.

@@ -2,49 +2,50 @@
 #include <algorithm>
 #include <cmath>
 
+#include "blocks.h"
 #include "gated.h"
-#include "stream.h"
 
 namespace moe {
 
 static bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Few rows a group: the stream of the weights instead of tiles.  Measured (us, stream
-// / tiles, the forward pass):
-//   d=2048 F=768    bf16  1 row 9 / 13, 16 rows 12 / 12, 64 rows 15 / 13.5
-//                   fp32  1 row 11 / 18, 32 rows 15.5 / 18, 64 rows 22 / 19
-//   d=7168 F=2048   bf16  8 rows 18 / 20, 32 rows 28 / 22    fp32  32 rows 48 / 69
-//   d=512 F=2048    fp32  16 rows 12 / 8
-//   d=2048 F=768, 256 groups   bf16  384 rows 217 / 226, 1000 rows 316 / 273
-//                              fp32  1000 rows 668 / 1086, 4000 rows 1047 / 1833
-static bool streams(int M, int d, int E, bool bf16, GatedPart part) {
+// Forward: blocks of 32 rows (blocks.hip) for rows of 16 bytes.  In fp32 they are
+// bound by the same instruction as tiles of 64 and 128 and start and end sooner; in
+// bf16 they are taken for few rows a group, and where their estimated time is below
+// that of the tiles.  Measured (us, bf16, blocks / tiles; fp32, blocks / tiles of 64):
+//   M=333 d=520 F=264       5.0 / 13.7     8.4 / 24
+//   M=64 d=2048 F=768       5.9 / 13.3     15.6 / 38
+//   M=256, 512, 1000        9.6 / 17.4, 14.4 / 19.5, 26.0 / 27.4     (1000 rows) 72 / 110
+//   M=2000 d=1024 F=512     21.8 / 18.3    53 / 62 (M=2048)
+//   M=300 d=7168 F=2048     62.7 / 36.5
+//   d=2048 F=768, 256 groups   384 rows 205 / 226, 1000 rows 285 / 291
+//                              1000 rows 525 / 637, 4000 rows 657 / 1109
+static bool in_blocks(int M, int d, int F, int E, bool bf16, GatedPart part) {
   if (part != GatedPart::kForward) return false;
-  if (bf16) return E == 1 ? M <= 16 : M / E < 3;
-  return d >= 1024 && (E == 1 ? M <= 32 : M / E < 24);
+  return !bf16 || (E == 1 ? M <= 16 : M / E < 3) ||
+         blocks_time(M, F, 2LL * d, E, true) < gated_tiles_time(M, d, F, E, part);
 }
 
-// Few results: blocks of 32 x 32 whose K the waves of a workgroup share, K in chunks of
-// 64 for each.  fp32: while tiles of 64 would leave compute units without one.
-// Measured (us, tiles of 64 / blocks): M=333 d=520 F=264 forward 24 / 8.4, dx 32 / 10.5,
-// dW 19 / 10.  bf16 in rows of 16 bytes has tiles on its own matrix instruction, so
-// that only chunks few and short win (us, its tiles / blocks):
-//   M=40 d=64 F=32       forward 8.4 / 4.1     gradients 14 / 5.1
-//   M=333 d=520 F=264            13.7 / 8.9              24.4 / 18.6
-//   700 rows, 7 groups, d=256 F=96   11.9 / 7.7          20.9 / 14.7
-//   2000 rows, 64 groups             11.8 / 12.6         20.2 / 29
-//   M=64 d=2048 F=768            13.4 / 21               21.9 / 44
-// One row of d=512 F=128 takes 8.8 in the stream, 7.3 in blocks.
+// Gradients of few results: blocks of 32 x 32 whose K the waves of a workgroup share, K
+// in chunks of 64 for each; as the forward pass of rows that do not start on 16 bytes.
+// On the fp32 matrix cores: while tiles of 64 would leave compute units without one.
+// Measured (us, tiles of 64 / blocks): fp32 M=333 d=520 F=264 dx 32 / 10.5, dW 19 / 10.
+// bf16 in rows of 16 bytes has tiles on its own matrix instruction, so that only chunks
+// few and short win (us, its tiles / blocks, dx and dW):
+//   M=40 d=64 F=32   14 / 5.1      700 rows, 7 groups, d=256 F=96    20.9 / 14.7
+//   M=333 d=520 F=264  24.4 / 18.6     2000 rows, 64 groups          20.2 / 29
+//   M=64 d=2048 F=768  21.9 / 44
 struct SmallWork {
   double blocks, chunks;
 };
 static SmallWork small_work(int M, int d, int F, int E, GatedPart part) {
   const double entries = std::ceil(M / 32.0) + (E > 1 ? std::min(M, E) : 0);
-  if (part == GatedPart::kForward) return {entries * std::ceil(F / 16.0), std::ceil(d / 64.0)};
   if (part == GatedPart::kDx) return {entries * std::ceil(d / 32.0), std::ceil(F / 32.0)};
   return {std::ceil(2.0 * F / 32) * E * std::ceil(d / 32.0), std::ceil(M / 64.0 / E)};
 }
-static bool is_small(int M, int d, int F, int E, bool rows16, GatedPart part) {
-  if (rows16) {
+static bool is_small(int M, int d, int F, int E, bool big, GatedPart part) {
+  if (big) {
+    if (part == GatedPart::kForward) return false;
     const SmallWork w = small_work(M, d, F, E, part);
     return w.chunks <= 10 && w.blocks <= 512 && w.blocks * w.chunks <= 2048;
   }
@@ -56,8 +57,8 @@ static bool is_small(int M, int d, int F, int E, bool rows16, GatedPart part) {
 static bool rows_of_8(int d, int F, bool bf16) { return bf16 && d % 8 == 0 && F % 8 == 0; }
 
 size_t gated_part_floats(int M, int d, int F, int E, bool bf16, GatedPart part) {
-  if (!rows_of_8(d, F, bf16) || M == 0 || is_small(M, d, F, E, true, part) ||
-      streams(M, d, E, bf16, part))
+  if (!rows_of_8(d, F, bf16) || M == 0 || in_blocks(M, d, F, E, bf16, part) ||
+      is_small(M, d, F, E, true, part))
     return 0;
   const int s = gated_splits(M, d, F, E, part);
   if (s == 1) return 0;
@@ -80,24 +81,22 @@ static bool big_tiles(const GatedArgs& a, GatedPart part) {
 
 hipError_t launch_gated(const GatedArgs& a, GatedPart part, hipStream_t st) {
   const bool big = big_tiles(a, part);
-  // (the stream's fp32 rows are long ones: it comes first)
-  const bool stream = streams(a.M, a.d, a.E, a.bf16, part) && wide_rows(a);
-  if (is_small(a.M, a.d, a.F, a.E, big, part) && !(stream && !big))
-    return launch_gated_small(a, part, st);
-  if (stream) {
-    StreamArgs s{};
-    s.a = a.x;
-    s.w0 = a.w_gate;
-    s.w1 = a.w_up;
-    s.offsets = a.offsets;
-    s.out = a.h;
-    s.pre = a.pre;
-    s.M = a.M;
-    s.N = a.F;
-    s.K = a.d;
-    s.E = a.E;
-    return launch_stream(s, a.bf16 ? StreamKind::kGatedBf16 : StreamKind::kGatedF32, st);
+  if (part == GatedPart::kForward && wide_rows(a) &&
+      (!big || in_blocks(a.M, a.d, a.F, a.E, a.bf16, part))) {
+    BlockArgs b{};
+    b.a = a.x;
+    b.w0 = a.w_gate;
+    b.w1 = a.w_up;
+    b.offsets = a.offsets;
+    b.out = a.h;
+    b.pre = a.pre;
+    b.M = a.M;
+    b.N = a.F;
+    b.K = a.d;
+    b.E = a.E;
+    return launch_blocks(b, a.bf16 ? BlockKind::kGatedBf16 : BlockKind::kGatedF32, st);
   }
+  if (is_small(a.M, a.d, a.F, a.E, big, part)) return launch_gated_small(a, part, st);
   if (big) {
     GatedArgs b = a;
     b.splits = gated_part_floats(a.M, a.d, a.F, a.E, true, part) > 0

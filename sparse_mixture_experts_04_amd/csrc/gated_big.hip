@@ -8,6 +8,7 @@
 // contiguous along their rows.
 // Rows of x, the matrices, dau and the results start on 16 bytes (d and F are
 // multiples of 8).
+#include <algorithm>
 #include <cmath>
 
 #include "gated.h"
@@ -327,15 +328,17 @@ hipError_t run(const GatedArgs& a, hipStream_t st) {
 // at 4 TB/s.  Measured (us, one walk / slices, d=7168 F=2048): 256 rows forward 68 /
 // 31, dx 39 / 27, dW 31 / 24; 1024 rows forward 72 / 62; 64 rows of d=2048 F=768
 // forward 21.5 / 13.6, dx 12.6 / 7.2.
-int gated_splits(int M, int d, int F, int E, GatedPart part) {
-  if (E != 1) return 1;
+static int splits_of(int M, int d, int F, int E, GatedPart part, double& time) {
   const bool fwd = part == GatedPart::kForward, dw = part == GatedPart::kDw;
   const double rows = dw ? 2.0 * F : M, cols = fwd ? 2.0 * F : d;
-  const double items = std::ceil(rows / 128.0) * std::ceil(cols / 256.0);
-  const double nk = fwd ? std::ceil(d / 64.0) : dw ? std::ceil(M / 64.0) : 2.0 * std::ceil(F / 64.0);
+  const double entries = std::ceil(rows / 128.0) * (dw ? E : 1) + (!dw && E > 1 ? std::min(M, E) : 0);
+  const double items = entries * std::ceil(cols / 256.0);
+  const double nk = fwd  ? std::ceil(d / 64.0)
+                    : dw ? std::ceil(M / 64.0 / E)
+                         : 2.0 * std::ceil(F / 64.0);
   int best = 1;
-  double time = nk * 0.6 * std::ceil(items / 256.0);
-  for (int s = 2; s <= 16 && s * 2 <= nk; ++s) {
+  time = nk * 0.6 * std::ceil(items / 256.0);
+  for (int s = 2; E == 1 && s <= 16 && s * 2 <= nk; ++s) {
     const double t = 6.0 + std::ceil(nk / s) * 0.6 * std::ceil(items * s / 256.0) +
                      8.0 * s * rows * cols / 4e6;
     if (t < 0.9 * time) {
@@ -344,6 +347,17 @@ int gated_splits(int M, int d, int F, int E, GatedPart part) {
     }
   }
   return best;
+}
+
+int gated_splits(int M, int d, int F, int E, GatedPart part) {
+  double time;
+  return splits_of(M, d, F, E, part, time);
+}
+
+double gated_tiles_time(int M, int d, int F, int E, GatedPart part) {
+  double time;
+  splits_of(M, d, F, E, part, time);
+  return 3.5 + time;
 }
 
 hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, hipStream_t st) {

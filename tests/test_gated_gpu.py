@@ -254,12 +254,16 @@ def test_row_counts_where_the_kernel_changes(M, dt):
     check(x, wg, wu, dh, None, both(x, wg, wu, dh, None))
 
 
-@pytest.mark.parametrize("M,offsets", [(200, [5, 190]), (200, [0, 200]), (200, [7, 7]), (70, [69, 70])])
-def test_slices_of_k_with_rows_outside(M, offsets):
-    """One group of part of the rows, where a product is cut along K."""
+@pytest.mark.parametrize("M,d,F,offsets", [
+    (200, 2000, 504, [5, 190]), (200, 2000, 504, [0, 200]), (200, 2000, 504, [7, 7]),
+    (70, 2000, 504, [69, 70]), (400, 6000, 1000, [5, 390]), (400, 6000, 1000, [9, 9]),
+    (330, 7000, 1000, None)])
+def test_slices_of_k_with_rows_outside(M, d, F, offsets):
+    """One group of part of the rows, where products are cut along K (the last three:
+    the forward pass too)."""
     from sparse_mixture_experts_04_amd import ops
-    assert ops.gated_ff_workspace(M, 2000, 504, 1, BF, "cuda").numel() > 1
-    x, wg, wu, dh = inputs(M, 2000, 504, 1, BF, seed=M)
+    assert d < 6000 or ops.gated_ff_workspace(M, d, F, 1, BF, "cuda").numel() > 1
+    x, wg, wu, dh = inputs(M, d, F, 1, BF, seed=M)
     check(x, wg, wu, dh, offsets, both(x, wg, wu, dh, offsets))
 
 
