@@ -488,9 +488,12 @@ def code_row(K):
 def _at(t, idx, dtype, shape, name):
     """Address of a tensor that must be on GPU `idx`, dense, of this dtype and
     shape."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == idx and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == idx
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass  # no tensor
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
     _ptr(t, dtype, shape, name)
@@ -510,12 +513,15 @@ def _on_gpu(x, name):
 # torch's current stream as a handle, without an object around it (8-bit and
 # few-token calls take some 10 us on the GPU, the object alone 2 us)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+# torch's current GPU without the check that torch is initialised (a tensor on a GPU is
+# there by then)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(idx, fn, *args):
     """fn(*args, stream) on the current stream of GPU idx, with that GPU the
     current device."""
-    if idx == torch.cuda.current_device():
+    if idx == _current_gpu():
         return fn(*args, _raw_stream(idx))
     with torch.cuda.device(idx):
         return fn(*args, _raw_stream(idx))
@@ -523,9 +529,11 @@ def _call(idx, fn, *args):
 
 def _ws(ws, idx):
     """Address and size of a workspace on GPU idx."""
-    if (isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8 and ws.get_device() == idx
-            and ws.is_contiguous()):
-        return ws.data_ptr(), ws.numel()
+    try:
+        if ws.dtype is torch.uint8 and ws.get_device() == idx and ws.is_contiguous():
+            return ws.data_ptr(), ws.numel()
+    except AttributeError:
+        pass  # no tensor
     _ptr(ws, torch.uint8, None, "ws")
     raise ValueError(f"ws must be a tensor on cuda:{idx}")
 
