@@ -229,17 +229,23 @@ __global__ __launch_bounds__(kThreads, 4) void blocks_kernel(BlockArgs p) {
 
 }  // namespace
 
+// Blocks there may be: an entry for each 32 rows of a group, one at least for each group
+// with rows.
+static double most_blocks(int M, int N, int E, bool gated) {
+  return (std::ceil(M / 32.0) + (E > 1 ? std::min(M, E) : 0)) * std::ceil(N / (gated ? 16.0 : 32.0));
+}
+
 double blocks_time(int M, int N, long long row_bytes, int E, bool gated) {
-  const double entries = std::ceil(M / 32.0) + (E > 1 ? std::min(M, E) : 0);
-  const double blocks = entries * std::ceil(N / (gated ? 16.0 : 32.0));
-  return 3.0 + std::max(0.5, blocks / 512) * (2.3 + 0.18 * std::ceil(row_bytes / 128.0));
+  return 3.0 + std::max(0.5, most_blocks(M, N, E, gated) / 512) *
+                   (2.3 + 0.18 * std::ceil(row_bytes / 128.0));
 }
 
 hipError_t launch_blocks(const BlockArgs& a, BlockKind kind, hipStream_t st) {
-  constexpr int kGrid = 1024;
-  if (kind == BlockKind::kFp8) blocks_kernel<BlockKind::kFp8><<<kGrid, kThreads, 0, st>>>(a);
-  else if (kind == BlockKind::kGatedBf16) blocks_kernel<BlockKind::kGatedBf16><<<kGrid, kThreads, 0, st>>>(a);
-  else blocks_kernel<BlockKind::kGatedF32><<<kGrid, kThreads, 0, st>>>(a);
+  const unsigned grid =
+      static_cast<unsigned>(std::min(1024.0, most_blocks(a.M, a.N, a.E, kind != BlockKind::kFp8)));
+  if (kind == BlockKind::kFp8) blocks_kernel<BlockKind::kFp8><<<grid, kThreads, 0, st>>>(a);
+  else if (kind == BlockKind::kGatedBf16) blocks_kernel<BlockKind::kGatedBf16><<<grid, kThreads, 0, st>>>(a);
+  else blocks_kernel<BlockKind::kGatedF32><<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -357,7 +357,7 @@ int gated_splits(int M, int d, int F, int E, GatedPart part) {
 double gated_tiles_time(int M, int d, int F, int E, GatedPart part) {
   double time;
   splits_of(M, d, F, E, part, time);
-  return 3.5 + time;
+  return 7.0 + time;
 }
 
 hipError_t launch_gated_big(const GatedArgs& a, GatedPart part, hipStream_t st) {

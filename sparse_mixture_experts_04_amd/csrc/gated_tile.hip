@@ -5,6 +5,9 @@
 // columns.  dx: rows of dau, whose 2F values of K meet the rows of Wg, then of Wu.
 // dW: columns of dau (rows of the result: F of dWg, then F of dWu) and of x, K the
 // rows of the group; a group without rows writes zeros.
+#include <algorithm>
+#include <cmath>
+
 #include "gated.h"
 #include "tile32.h"
 
@@ -363,11 +366,18 @@ void run(const GatedArgs& a, GatedPart part, hipStream_t st) {
   else run<T, GatedPart::kDw>(a, st);
 }
 
-constexpr int kSmallGrid = 1024;
+// Workgroups for a product's blocks of 32 x 32, of which there are that many at most.
+unsigned small_grid(const GatedArgs& a, GatedPart part) {
+  const double entries = std::ceil(a.M / 32.0) + (a.E > 1 ? std::min(a.M, a.E) : 0);
+  const double blocks = part == GatedPart::kForward ? entries * std::ceil(a.F / 16.0)
+                        : part == GatedPart::kDx    ? entries * std::ceil(a.d / 32.0)
+                                                    : std::ceil(a.F / 16.0) * a.E * std::ceil(a.d / 32.0);
+  return static_cast<unsigned>(std::min(1024.0, blocks));
+}
 
 template <typename T>
 void run_small(const GatedArgs& a, GatedPart part, hipStream_t st) {
-  auto go = [&](auto kernel) { kernel<<<kSmallGrid, 64 * kSmallWaves, 0, st>>>(a); };
+  auto go = [&](auto kernel) { kernel<<<small_grid(a, part), 64 * kSmallWaves, 0, st>>>(a); };
   if (part == GatedPart::kForward) go(gated_small_kernel<T, GatedPart::kForward>);
   else if (part == GatedPart::kDx) go(gated_small_kernel<T, GatedPart::kDx>);
   else go(gated_small_kernel<T, GatedPart::kDw>);
@@ -388,7 +398,9 @@ hipError_t launch_gated_small(const GatedArgs& a, GatedPart part, hipStream_t st
 }
 
 hipError_t launch_gated_small_grads(const GatedArgs& a, bool from_pre, hipStream_t st) {
-  auto go = [&](auto kernel) { kernel<<<kSmallGrid, 64 * kSmallWaves, 0, st>>>(a); };
+  const unsigned grid = std::min(1024u, (a.dx ? small_grid(a, GatedPart::kDx) : 0) +
+                                           (a.dw_gate ? small_grid(a, GatedPart::kDw) : 0));
+  auto go = [&](auto kernel) { kernel<<<grid, 64 * kSmallWaves, 0, st>>>(a); };
   if (a.bf16)
     from_pre ? go(gated_small_grads_kernel<bf16_t, true>) : go(gated_small_grads_kernel<bf16_t, false>);
   else
