@@ -550,9 +550,9 @@ moe_status moe_quantize_fp8_weights(int32_t E, int32_t N, int32_t K, moe_dtype d
 /* Grouped product: y[m, n] = sum_b a_scale[m, b] w_scale[e, n/128, b] sum_{k in b}
  * a[m, k] w[e, n, k] over the blocks b of 128 values of K, for the rows m of group
  * e (offsets as for moe_gated_ff; rows outside every group keep what y held).
- * Sums are fp32, y is rounded once to `out` (MOE_F32 or MOE_BF16); for a bf16 y of
- * more than 8 rows the products come from an instruction that keeps some 16 bits of
- * 8 at a time (1.4e-5 of y, 1/100 of y's rounding).  Codes are any
+ * Sums are fp32, y is rounded once to `out` (MOE_F32 or MOE_BF16); the products of a
+ * large bf16 y come from an instruction that keeps some 16 bits of 8 at a time (1.4e-5
+ * of y, 1/100 of y's rounding).  Codes are any
  * e4m3 values; a NaN code (0x7f, 0xff) makes its products NaN.
  *   a [M, Kp], a_scale [M, Kp/128], w [E, N, Kp], w_scale [E, ceil(N/128), Kp/128],
  *   y [M, N]; y shares no memory with the inputs.

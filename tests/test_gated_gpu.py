@@ -256,7 +256,7 @@ def test_row_counts_where_the_kernel_changes(M, dt):
 
 @pytest.mark.parametrize("M,d,F,offsets", [
     (200, 2000, 504, [5, 190]), (200, 2000, 504, [0, 200]), (200, 2000, 504, [7, 7]),
-    (70, 2000, 504, [69, 70]), (400, 6000, 1000, [5, 390]), (400, 6000, 1000, [9, 9]),
+    (70, 2000, 504, [69, 70]), (330, 7000, 1000, [5, 320]), (330, 7000, 1000, [9, 9]),
     (330, 7000, 1000, None)])
 def test_slices_of_k_with_rows_outside(M, d, F, offsets):
     """One group of part of the rows, where products are cut along K (the last three:
