@@ -31,7 +31,6 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 
-
 // Eight codes as bf16, which holds every e4m3 value.
 __device__ __forceinline__ bf16x8_t wide8(uint32_t lo, uint32_t hi) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));

@@ -373,3 +373,18 @@ def test_refusals_of_the_binding():
     torch.cuda.synchronize()
     for k in t:
         assert all(torch.equal(a, b) for a, b in zip(t[k], old[k]))
+
+
+def test_no_plan_inside_a_capture():
+    L = ops()
+    t = tensors([300], F32, F32, 32)
+    L.adamw_step(L.adamw_plan(**t), 1, **HYPER)
+    x = torch.zeros(4, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x += 1
+        with pytest.raises(RuntimeError):
+            L.adamw_plan(**t)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (x == 1).all()

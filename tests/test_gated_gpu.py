@@ -346,3 +346,29 @@ def test_refusals_of_the_binding():
                             ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert not h.any()
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,d,F,offsets", [(5, 264, 40, None), (1, 2048, 768, None), (40, 1000, 72, None),
+                                           (9, 520, 33, [0, 4, 4, 9]), (2500, 72, 40, None)])
+def test_products_computed_again(M, d, F, offsets, dt):
+    """Every kernel of the forward pass without a place for h."""
+    E = 1 if offsets is None else len(offsets) - 1
+    x, wg, wu, dh = inputs(M, d, F, E, dt, seed=M)
+    a, b = both(x, wg, wu, dh, offsets), both(x, wg, wu, dh, offsets, saved=False)
+    check(x, wg, wu, dh, offsets, b)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("rows", [1, 2, 31, 32, 33])
+def test_rows_that_a_group_ends_with(rows):
+    """NaN behind a group's last row and columns past the last whole block reach nobody."""
+    x, wg, wu, dh = inputs(80, 1000, 45, 1, F32, seed=rows)
+    x[7 + rows:] = float("nan")
+    x[:7] = float("inf")
+    for dt in (F32, BF):
+        y = [t.to(dt) for t in (x, wg, wu, dh)]
+        got = both(*y, [7, 7 + rows])
+        clean = torch.nan_to_num(y[0], 0.0, 0.0, 0.0)
+        check(clean, *y[1:], [7, 7 + rows], got)
