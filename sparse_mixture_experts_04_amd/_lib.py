@@ -855,9 +855,20 @@ ADAMW_BLOCK = 256
 class AdamwPlan:
     """The tensors of a step in a device table (see adamw_plan)."""
 
-    def __init__(self, device, desc, chunks, table, tensors):
+    def __init__(self, device, desc, chunks, table, tensors, stream):
         self.device, self.desc, self.chunks, self.table = device, desc, chunks, table
         self.tensors = tensors  # keeps them alive
+        self.stream = stream    # handle of the one the table was allocated on
+
+    def in_use(self):
+        """To be called behind a launch that reads the table.  On another stream than
+        the plan's, torch would give a dropped plan's table away while that launch
+        still reads it; it is told of the stream.  (Inside a capture nothing runs yet:
+        whoever owns the graph keeps the plan.)"""
+        if _raw_stream(self.device) != self.stream:
+            with torch.cuda.device(self.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    self.table.record_stream(torch.cuda.current_stream())
 
 
 def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v_scales=None,
@@ -868,7 +879,8 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v
     zeros to begin with).  ``copies``: bf16 tensors that take each fp32 parameter
     too.  ``m_values``, ``v_values``: fp32 tensors for adamw_state_values.  The plan
     holds the tensors; a gradient that moves needs a new plan.  Waits for the current
-    stream; not for use inside a capture (a step with the plan is)."""
+    stream; not for use inside a capture (a step with the plan is: keep the plan as long
+    as the graph is replayed)."""
     lists = {"params": params, "grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
              "copies": copies, "m_scales": m_scales, "v_scales": v_scales, "m_values": m_values,
              "v_values": v_values}
@@ -913,7 +925,7 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v
     _check("moe_adamw_prepare", _call(dev, lib.moe_adamw_prepare, ctypes.byref(desc), rows,
                                       ctypes.byref(chunks), table.data_ptr(), n.value))
     torch.cuda.current_stream(device).synchronize()  # steps may run on any stream
-    return AdamwPlan(dev, desc, chunks.value, table, lists)
+    return AdamwPlan(dev, desc, chunks.value, table, lists, _raw_stream(dev))
 
 
 def adamw_step(plan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
@@ -936,6 +948,7 @@ def adamw_step(plan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
             raise TypeError("grad_scale must be a torch.Tensor")
     _check("moe_adamw", _call(plan.device, lib.moe_adamw, ctypes.byref(plan.desc),
                               ctypes.byref(a), plan.chunks, plan.table.data_ptr()))
+    plan.in_use()
 
 
 def adamw_state_values(plan):
@@ -946,3 +959,4 @@ def adamw_state_values(plan):
     _check("moe_adamw_state_values", _call(plan.device, lib.moe_adamw_state_values,
                                            ctypes.byref(plan.desc), plan.chunks,
                                            plan.table.data_ptr()))
+    plan.in_use()
