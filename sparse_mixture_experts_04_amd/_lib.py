@@ -44,12 +44,24 @@ class MoEError(RuntimeError):
         self.status = status
 
 
+def _fit32(fn, *sizes):
+    """Refuses sizes that the library's 32-bit arguments cannot hold (ctypes would pass
+    their low bits)."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise MoEError(fn, 5, f"{n} does not fit in 32 bits")
+
+
 class Desc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("F", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("S", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("act", ctypes.c_int), ("weight", ctypes.c_int),
                 ("gate_norm", ctypes.c_int32), ("gate_scale", ctypes.c_float),
                 ("capacity_factor", ctypes.c_float)]
+
+    def __init__(self, T=0, d=0, F=0, E=0, S=0, k=0, *more, **named):
+        _fit32("Desc", T, d, F, E, S, k)
+        super().__init__(T, d, F, E, S, k, *more, **named)
 
 
 class Weights(ctypes.Structure):
@@ -58,9 +70,17 @@ class Weights(ctypes.Structure):
                  "sc_gate", "sc_up", "sc_down", "w_router_planes")]
 
 
+_fields = ctypes.Structure.__init__
+
+
 class GemmInt8Desc(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("out", ctypes.c_int)]
+
+    def __init__(self, M=0, N=0, K=0, E=0, out=0):
+        if (M | N | K | E) >> 31:  # (one test where all is well: a call makes one of these)
+            _fit32(type(self).__name__, M, N, K, E)
+        _fields(self, M, N, K, E, out)
 
 
 class WeightsInt8(ctypes.Structure):
@@ -72,6 +92,11 @@ class WeightsInt8(ctypes.Structure):
 class GatedFfDesc(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int32), ("d", ctypes.c_int32), ("F", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("act", ctypes.c_int)]
+
+    def __init__(self, M=0, d=0, F=0, E=0, act=0):
+        if (M | d | F | E) >> 31:
+            _fit32("GatedFfDesc", M, d, F, E)
+        _fields(self, M, d, F, E, act)
 
 
 class GemmFp8Desc(GemmInt8Desc):
@@ -282,6 +307,7 @@ def quantize_mxfp4(w):
     """moe_quantize_mxfp4 of a bf16 stack w [E, N, K]: returns (codes
     uint8 [E, K/128, N, 64], scales uint8 [E, K/128, N, 4]) on w's device."""
     E, N, K = w.shape
+    _fit32("quantize_mxfp4", E, N, K)
     if K % 128:
         raise ValueError(f"quantize_mxfp4: K = {K} is not a multiple of 128")
     codes = torch.empty((E, K // 128, N, 64), dtype=torch.uint8, device=w.device)
@@ -548,6 +574,7 @@ def quantize_int8(x, codes=None, scales=None):
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least one value")
     K = shape[-1]
+    _fit32("quantize_int8", K)
     lead = shape[:-1]
     out = (*lead, code_row(K))
     if codes is None:
@@ -715,7 +742,7 @@ def gated_ff_workspace(M, d, F, E, dtype, device, backward=False, saved=True):
     gated_ff_backward (``saved``: which will be given ``pre``)."""
     n = ctypes.c_size_t(0)
     _check("moe_gated_ff_workspace_size", lib.moe_gated_ff_workspace_size(
-        ctypes.byref(GatedFfDesc(M, d, F, E, act_code(dtype))), int(backward), int(saved),
+        ctypes.byref(GatedFfDesc(M, d, F, E, act_code(dtype))), bool(backward), bool(saved),
         ctypes.byref(n)))
     return torch.empty(max(n.value, 1), dtype=torch.uint8, device=device)
 
@@ -783,6 +810,7 @@ def quantize_fp8(x, codes=None, scales=None):
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x needs a last dimension of at least one value")
     K, lead = shape[-1], shape[:-1]
+    _fit32("quantize_fp8", K)
     out, sc = (*lead, _blocks(K) * FP8_BLOCK), (*lead, _blocks(K))
     if codes is None:
         codes = torch.empty(out, dtype=FP8, device=x.device)
@@ -802,6 +830,7 @@ def quantize_fp8_weights(w, codes=None, scales=None):
     if w.dim() != 3 or w.shape[2] < 1:
         raise ValueError("quantize_fp8_weights takes w [E, N, K]")
     E, N, K = w.shape
+    _fit32("quantize_fp8_weights", E, N, K)
     out, sc = (E, N, _blocks(K) * FP8_BLOCK), (E, _blocks(N), _blocks(K))
     if codes is None:
         codes = torch.empty(out, dtype=FP8, device=w.device)
@@ -942,6 +971,8 @@ def adamw_step(plan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
             if v.numel() != 1:
                 raise ValueError(f"{name} must hold one value")
             setattr(a, name + "_dev", _at(v, plan.device, dt, v.shape, name))
+        elif name == "step" and v >> 63 > 0:
+            raise ValueError(f"step must fit in 64 bits, got {v}")
         elif name != "grad_scale":
             setattr(a, name, v)
         elif v is not None:

@@ -61,3 +61,63 @@ def test_a_captured_step_leaves_the_plan_to_the_graphs_owner(host):
     host.update(stream=9, capturing=True)
     L.adamw_step(p, 1, lr=1e-3)
     assert p.table.streams == [] and len(host["calls"]) == 1
+
+
+WIDE = (1 << 32) + 128  # its low 32 bits are a size that calls take
+
+
+@pytest.mark.parametrize("make", [
+    lambda n: L.GatedFfDesc(1, n, 8, 1, L.BF16), lambda n: L.GatedFfDesc(n, 8, 8, 1, L.BF16),
+    lambda n: L.GatedFfDesc(1, 8, F=n, E=1), lambda n: L.GatedFfDesc(1, 8, 8, n),
+    lambda n: L.GemmFp8Desc(1, n, 128, 1, L.BF16), lambda n: L.GemmFp8Desc(M=1, N=8, K=n, E=1, out=L.F32),
+    lambda n: L.GemmInt8Desc(n, 8, 128, 1, L.BF16), lambda n: L.GemmInt8Desc(1, 8, 128, n, L.BF16),
+    lambda n: L.make_desc(n, 512, 128, torch.bfloat16), lambda n: L.make_desc(4, n, 128, torch.bfloat16),
+    lambda n: L.Desc(T=4, d=512, F=n), lambda n: L.make_desc(4, 512, 128, torch.bfloat16, k=n),
+    lambda n: L.gated_ff_workspace(n, 8, 8, 1, torch.bfloat16, "cpu"),
+    lambda n: L.gated_ff_workspace(1, 8, n, 1, torch.bfloat16, "cpu"),
+    lambda n: L.gemm_fp8_workspace(1, 8, n, device="cpu"),
+    lambda n: L.gemm_int8_workspace(1, n, 128, device="cpu"),
+])
+@pytest.mark.parametrize("n", [WIDE, 1 << 31, -WIDE, (1 << 63) + 8])
+def test_sizes_of_more_than_32_bits_are_refused(make, n):
+    """They are not cut to their low 32 bits."""
+    with pytest.raises(L.MoEError) as e:
+        make(n)
+    assert e.value.status == 5
+
+
+@pytest.mark.parametrize("call,shape", [
+    (lambda x: L.quantize_fp8(x), (0, WIDE)), (lambda x: L.quantize_int8(x), (0, WIDE)),
+    (lambda x: L.quantize_fp8_weights(x), (0, 8, WIDE)), (lambda x: L.quantize_fp8_weights(x), (0, WIDE, 8)),
+    (lambda x: L.quantize_fp8_weights(x), (WIDE, 0, 8)), (lambda x: L.quantize_mxfp4(x), (0, 8, WIDE)),
+])
+def test_rows_of_more_than_32_bits_are_refused(monkeypatch, call, shape):
+    """Of tensors too: the library would see a row of 128 values (no values here, so
+    that nothing is launched)."""
+    monkeypatch.setattr(L, "_on_gpu", lambda x, name: 0)
+    monkeypatch.setattr(L, "_at", lambda *a: 0x1000)
+    monkeypatch.setattr(L, "_ptr", lambda *a: 0x1000)
+    monkeypatch.setattr(L, "_stream", lambda d: None)
+    monkeypatch.setattr(L, "_call", lambda idx, fn, *args: fn(*args, None))
+    with pytest.raises(L.MoEError) as e:
+        call(torch.empty(shape, dtype=torch.bfloat16, device="meta"))
+    assert e.value.status == 5
+
+
+def test_sizes_of_32_bits_keep_their_meaning():
+    d = L.GatedFfDesc(1, 2, 3, 4, L.BF16)
+    assert (d.M, d.d, d.F, d.E, d.act) == (1, 2, 3, 4, L.BF16)
+    d = L.GemmFp8Desc(-1, 5, out=L.BF16, K=(1 << 31) - 1)
+    assert (d.M, d.N, d.K, d.E, d.out) == (-1, 5, (1 << 31) - 1, 0, L.BF16)
+    d = L.make_desc(8, 512, 128, torch.bfloat16, E=64, S=1, k=4, gate_norm="logsumexp", gate_scale=2.5,
+                    capacity_factor=1.25)
+    assert (d.T, d.d, d.F, d.E, d.S, d.k) == (8, 512, 128, 64, 1, 4)
+    assert (d.act, d.weight, d.gate_norm, d.gate_scale, d.capacity_factor) == (
+        L.BF16, L.BF16, L.GATE_LOGSUMEXP, 2.5, 1.25)
+
+
+def test_steps_of_more_than_64_bits_are_refused(host):
+    for step in (1 << 63, (1 << 64) + 5):
+        with pytest.raises(ValueError):
+            L.adamw_step(plan(), step, lr=1e-3)
+    assert not host["calls"]
