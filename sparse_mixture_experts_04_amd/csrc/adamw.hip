@@ -217,6 +217,7 @@ __device__ __forceinline__ void walk_chunks(const AdamwTable& t, Work& work) {
 struct Rates {
   double b1, b2, a1, a2;
   float decay, lr, rate, inv_c1, inv_c2, eps, factor;
+  float inv_root_c2;  // of 1 - b2^t's root: v' / (1 - b2^t) itself may pass fp32 where v' does not
 };
 
 template <typename P, typename G, bool BITS8>
@@ -264,7 +265,7 @@ struct StepWork {
         const float gi = g[i] * r.factor;
         m[i] = b1 * m[i] + a1 * gi;
         v[i] = b2 * v[i] + a2 * gi * gi;
-        p[i] = p[i] * r.decay - r.lr * (m[i] * r.inv_c1) / (sqrtf(v[i] * r.inv_c2) + r.eps);
+        p[i] = p[i] * r.decay - r.lr * (m[i] * r.inv_c1) / (sqrtf(v[i]) * r.inv_root_c2 + r.eps);
       }
       hm[k].join(m);
       hv[k].join(v);
@@ -311,15 +312,16 @@ struct StepWork {
 #pragma unroll
       for (int i = 0; i < 4; ++i) upd[i] = m[i] * r.rate * __builtin_amdgcn_rcpf(den[i]);
       // near a border, a scale or a denominator that the short forms do not reach
-      const bool tiny = (ms < kTinyScale && ms > 0.0f) || (vs < kTinyScale && vs > 0.0f);
-      if (off > kNearBorder || tiny || least < 0x1p-50f) {
+      const bool far = (ms < kTinyScale && ms > 0.0f) || (vs < kTinyScale && vs > 0.0f) ||
+                       !(vs * r.inv_c2 < INFINITY);
+      if (off > kNearBorder || far || least < 0x1p-50f) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = ms > 0.0f ? exact_code<2>(fabs(md[i]), ms, tm[i], 127) : 0;
           fm[i] = kMagic + static_cast<float>(md[i] < 0.0 ? -c : c);
           const int q = vs > 0.0f ? exact_code<4>(vd[i], vs, tv[i], 255) : 0;
           fv[i] = kMagic + static_cast<float>(vd[i] > 0.0 && q < 1 ? 1 : q);
-          upd[i] = r.lr * (m[i] * r.inv_c1) / (sqrtf(v[i] * r.inv_c2) + r.eps);
+          upd[i] = r.lr * (m[i] * r.inv_c1) / (sqrtf(v[i]) * r.inv_root_c2 + r.eps);
         }
       }
 #pragma unroll
@@ -363,6 +365,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwTable t, AdamwStep
     shared.rate = static_cast<float>(lr / c1);
     shared.inv_c1 = static_cast<float>(1.0 / c1);
     shared.inv_c2 = static_cast<float>(1.0 / c2);
+    shared.inv_root_c2 = static_cast<float>(1.0 / sqrt(c2));
     shared.eps = static_cast<float>(s.eps);
     shared.factor = s.grad_scale ? *s.grad_scale : 1.0f;
   }

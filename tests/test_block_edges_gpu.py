@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from block_util import rand
+from block_util import adamw64, rand, within
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -45,3 +45,31 @@ def test_a_dropped_plan_outlives_its_step_on_another_stream():
     assert not torch.equal(t["params"][0], old["params"])
     for k in t:
         assert torch.equal(t[k][0], want[k][0]), k
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.999])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_first_steps_of_gradients_whose_squares_pass_fp32(bits, beta2):
+    """v' = (1 - beta2) g^2 is a number of fp32 and v' / (1 - beta2^step) is not: the
+    step goes by the exact quotient all the same, not by infinity."""
+    n, eight = 3000, bits == 8
+    z = rand((n,), F32, 4)
+    g = torch.sign(z) * (1.0 + z.abs().clamp(max=4.0)) * 2.0e19 / (1.0 if beta2 > 0.99 else 1.9)
+    assert ((1 - beta2) * g.double() ** 2).max() < 3.4e38 and (g.double() ** 2).max() > 3.4e38
+    t = {"params": [rand((n,), F32, 5)], "grads": [g]}
+    if eight:
+        t["exp_avg"], t["exp_avg_sq"] = ([torch.zeros(n, dtype=d, device="cuda")]
+                                         for d in (torch.int8, torch.uint8))
+        t["m_scales"], t["v_scales"] = ([torch.zeros((n + 255) // 256, device="cuda")] for _ in range(2))
+    else:
+        t["exp_avg"], t["exp_avg_sq"] = ([torch.zeros(n, device="cuda")] for _ in range(2))
+    plan = ops().adamw_plan(**t)
+    for step in (1, 2):
+        r = adamw64(t["params"][0], g, t["exp_avg"][0], t["exp_avg_sq"][0], step, 0.01, 0.9, beta2, 1e-8,
+                    0.1, 1.0, *((t["m_scales"][0], t["v_scales"][0]) if eight else ()))
+        if not r["v"].max() < 3.4e38:
+            break  # (a second step's v' may pass it)
+        ops().adamw_step(plan, step, lr=0.01, beta2=beta2, weight_decay=0.1)
+        within(t["params"][0], r["p"], r["ep"], f"p, step {step}")
+        if not eight:
+            within(t["exp_avg_sq"][0], r["v"], r["ev"], "v")
