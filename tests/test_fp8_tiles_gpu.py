@@ -119,3 +119,151 @@ def test_what_the_instruction_keeps(M, N):
         y = product(a[:rows].contiguous(), one(rows, 1), w, sw, dt).float().cpu()
         for at in (0, 16, 32):
             assert (y[:, at:at + 7] == torch.tensor(small)).all()
+
+
+@tiles
+def test_nan_stays_in_its_row_and_columns(M, N, K, dt):
+    """NaN scales of one row's block and of one weight block."""
+    a, sa, w, sw = operands(M, N, K)
+    clean = product(a, sa, w, sw, dt)
+    nb, kb = sw.shape[1:]
+    row, block = M - 3, nb - 2
+    sa, sw = sa.clone(), sw.clone()
+    sa[row, kb - 1] = float("nan")
+    sw[0, block, kb // 2] = float("nan")
+    y = product(a, sa, w, sw, dt)
+    cols = torch.zeros(N, dtype=torch.bool, device="cuda")
+    cols[128 * block:128 * block + 128] = True
+    assert torch.isnan(y[row]).all() and torch.isnan(y[:, cols]).all()
+    rows = torch.arange(M, device="cuda") != row
+    assert torch.equal(y[rows][:, ~cols], clean[rows][:, ~cols])
+
+
+@tiles
+def test_a_nan_code_stays_in_its_row_and_column(M, N, K, dt):
+    a, sa, w, sw = operands(M, N, K, seed=3)
+    clean = product(a, sa, w, sw, dt)
+    a, w = a.clone(), w.clone()
+    a.view(torch.uint8)[130, K - 1] = 0x7f
+    w.view(torch.uint8)[0, N - 1, 5] = 0xff
+    y = product(a, sa, w, sw, dt)
+    assert torch.isnan(y[130]).all() and torch.isnan(y[:, N - 1]).all()
+    rows = torch.arange(M, device="cuda") != 130
+    assert torch.equal(y[rows][:, :N - 1], clean[rows][:, :N - 1])
+
+
+@tiles
+def test_every_code_value(M, N, K, dt):
+    """All 254 finite codes against a column of ones: exact in either type."""
+    codes = torch.tensor([c for c in range(256) if c & 0x7f != 0x7f], dtype=torch.uint8, device="cuda")
+    codes = codes.repeat((M + 253) // 254)[:M]
+    kp = (K + 127) // 128 * 128
+    a = torch.zeros((M, kp), dtype=torch.uint8, device="cuda")
+    at = torch.arange(M, device="cuda") * 37 % K
+    a[torch.arange(M, device="cuda"), at] = codes
+    one = lambda *s: torch.ones(s, device="cuda")
+    y = product(a.view(FP8), one(M, kp // 128), one(1, N, kp).to(FP8),
+                one(1, (N + 127) // 128, kp // 128), dt)
+    assert torch.equal(y, codes.view(FP8).to(dt)[:, None].expand(M, N))
+
+
+@pytest.mark.parametrize("M,N,K,dt", [(2050, 1300, 640, BF), (2050, 1300, 640, F32), (4200, 3104, 640, BF),
+                                      (1024, 2048, 7040, BF), (1024, 2048, 7040, F32)], ids=TILE_IDS)
+def test_scales_that_differ_widely(M, N, K, dt):
+    """Blocks of K whose scales lie 2^60 apart in products, a row and a weight block of
+    scale 0."""
+    a, sa, w, sw = operands(M, N, K, seed=5)
+    kb = sa.shape[1]
+    up = torch.tensor([0.0, 30, -30, 10, -20], device="cuda")[torch.arange(kb, device="cuda") % 5]
+    down = torch.tensor([5.0, -25, 20, 0, 10], device="cuda")[torch.arange(kb, device="cuda") % 5]
+    sa = (sa * torch.exp2(up)[None]).contiguous()
+    sw = (sw * torch.exp2(down)[None, None]).contiguous()
+    sa[7] = 0
+    sw[0, 1, 2] = 0
+    y = product(a, sa, w, sw, dt)
+    want, bound, _ = fp8_product64(a, sa, w, sw, None, dt)
+    lost = 0.0 if dt == F32 else (1 + 2.0 ** -8) * instruction_loss(a, sa, w, sw)
+    within(y, want, bound + lost)
+    assert not y[7].any()
+
+
+@tiles
+def test_a_row_does_not_depend_on_the_others_of_its_tile(M, N, K, dt):
+    """Same bits beside rows and weight rows of NaN, in tiles whose last rows and columns
+    are not whole."""
+    a, sa, w, sw = operands(M, N, K, seed=7)
+    y = product(a, sa, w, sw, dt)
+    a2, w2 = a.clone(), w.clone()
+    a2.view(torch.uint8)[100:M - 1] = 0x7f
+    w2.view(torch.uint8)[0, 200:N - 1] = 0x7f
+    y2 = product(a2, sa, w2, sw, dt)
+    rows = torch.tensor([*range(100), M - 1], device="cuda")
+    cols = torch.tensor([*range(200), N - 1], device="cuda")
+    assert torch.equal(y[rows][:, cols], y2[rows][:, cols])
+    assert torch.isnan(y2[100:M - 1]).all() and torch.isnan(y2[:, 200:N - 1]).all()
+
+
+@pytest.mark.parametrize("M,N,K,dt,offsets", [
+    (3000, 1100, 256, BF, [5, 700, 700, 1401, 2990]), (3000, 1100, 256, F32, [5, 700, 700, 1401, 2990]),
+    (6000, 2200, 256, BF, [0, 1, 1, 2048, 2305, 5990])], ids=["128-bf16", "128-fp32", "256-bf16"])
+def test_groups_of_nan_rows(M, N, K, dt, offsets):
+    """A group of NaN rows, and NaN rows outside every group, beside the others."""
+    E = len(offsets) - 1
+    a, sa, w, sw = operands(M, N, K, E, seed=9)
+    clean = product(a, sa, w, sw, dt, offsets)
+    a2, sa2 = a.clone(), sa.clone()
+    bad = slice(offsets[2], offsets[3])
+    sa2[bad] = float("nan")
+    sa2[:offsets[0]] = float("nan")
+    a2.view(torch.uint8)[offsets[-1]:] = 0x7f
+    y = product(a2, sa2, w, sw, dt, offsets)
+    assert torch.isnan(y[bad]).all()
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    assert torch.equal(y[keep], clean[keep])
+    assert (y[:offsets[0]] == 7.0).all() and (y[offsets[-1]:] == 7.0).all()
+
+
+def test_slices_captured_with_work_between():
+    """A product with sums in its workspace, captured with the quantiser before it;
+    replayed on new rows with eager products between."""
+    L = ops()
+    M, N, K = 1024, 2048, 7000
+    assert sliced(M, N, K)
+    w, sw = L.quantize_fp8_weights(rand((1, N, K), F32, 2, K ** -0.5))
+    x = rand((M, K), BF, 1)
+    y, want = (torch.empty((M, N), dtype=BF, device="cuda") for _ in range(2))
+    ws = L.gemm_fp8_workspace(M, N, K)
+    c, s = L.quantize_fp8(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.quantize_fp8(x, c, s)
+        L.gemm_fp8(c, s, w, sw, y, ws=ws)
+    for i in range(3):
+        x.copy_(rand((M, K), BF, 20 + i))
+        ws.fill_(0xff)
+        y.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        L.gemm_fp8(*L.quantize_fp8(x), w, sw, want)
+        assert torch.equal(y, want), i
+
+
+def test_two_sliced_products_at_once():
+    """Two streams, a workspace each."""
+    L = ops()
+    M, N, K = 1024, 2048, 7000
+    assert sliced(M, N, K)
+    sets = [operands(M, N, K, seed=s) for s in (1, 5)]
+    want = [product(*s, BF) for s in sets]
+    got = [torch.zeros_like(t) for t in want]
+    wss = [L.gemm_fp8_workspace(M, N, K) for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, y, ws, st in zip(sets, got, wss, streams):
+            with torch.cuda.stream(st):
+                L.gemm_fp8(*s, y, ws=ws)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
