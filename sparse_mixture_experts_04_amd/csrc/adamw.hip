@@ -15,9 +15,10 @@
 // 1.6% at its top, and the smallest code stands for 6e-5 of the largest m and 2.4e-10
 // of the largest v.  A v that is not 0 never becomes 0, for p divides by its root.
 // m' and v' are taken in 64 bits: a code hangs on which side of a border they lie,
-// and on a cancelling sum 32 bits would not say.  The root is taken in 32 bits, and
-// where it lies within 1/2048 of a border, the border itself decides, in 64 bits
-// and without a root: |m'| against s ((k + 1/2) / 127)^2.
+// and on a cancelling sum 32 bits would not say.  The root is taken in 32 bits, within
+// 7e-5 of the exact one.  Where one of a lane's codes lies within 1/8192 (1.2e-4) of a
+// border, the lane looks at its codes again, and at each within 1/4096 of one the border
+// itself decides, in 64 bits and without a root: |m'| against s ((k + 1/2) / 127)^2.
 #include <cmath>
 #include <type_traits>
 

@@ -1,4 +1,6 @@
 """Edges of the gated block, the e4m3 products and the AdamW step."""
+import ctypes
+
 import pytest
 import torch
 
@@ -73,3 +75,46 @@ def test_first_steps_of_gradients_whose_squares_pass_fp32(bits, beta2):
         within(t["params"][0], r["p"], r["ep"], f"p, step {step}")
         if not eight:
             within(t["exp_avg_sq"][0], r["v"], r["ev"], "v")
+
+
+def test_values_of_the_tensors_that_have_a_place_for_them():
+    """A table of which some tensors have m_values and v_values (the C ABI takes it): those
+    are written, whole and no further; the others' states stay as they are."""
+    L = ops()
+    sizes, has = [300, 2048, 5, 4097, 77, 1], [True, False, True, False, False, True]
+    g = torch.Generator().manual_seed(3)
+    code = lambda n, lo, hi, dt: torch.randint(lo, hi, (n,), generator=g).to(dt).cuda()
+    m = [code(n, -127, 128, torch.int8) for n in sizes]
+    v = [code(n, 0, 256, torch.uint8) for n in sizes]
+    scales = [[(torch.rand((n + 255) // 256, generator=g) + 0.5).cuda() for n in sizes] for _ in range(2)]
+    p, grad = ([torch.zeros(n, device="cuda") for n in sizes] for _ in range(2))
+    values = [[torch.full((n + 8,), 9.0, device="cuda") for n in sizes] for _ in range(2)]
+    rows = (L.AdamwTensor * len(sizes))()
+    for i, r in enumerate(rows):
+        r.p, r.g, r.m, r.v = (t[i].data_ptr() for t in (p, grad, m, v))
+        r.m_scale, r.v_scale, r.n = scales[0][i].data_ptr(), scales[1][i].data_ptr(), sizes[i]
+        if has[i]:
+            r.m_values, r.v_values = (t[i].data_ptr() for t in values)
+    desc = L.AdamwDesc(len(sizes), L.F32, L.F32, 8)
+    size, chunks = ctypes.c_size_t(0), ctypes.c_int64(0)
+    assert L.lib.moe_adamw_table_size(ctypes.byref(desc), ctypes.byref(size)) == 0
+    table = torch.empty(size.value, dtype=torch.uint8, device="cuda")
+    before = [[x.clone() for x in t] for t in (m, v, scales[0], scales[1], p)]
+    stream = torch.cuda.current_stream().cuda_stream
+    assert L.lib.moe_adamw_prepare(ctypes.byref(desc), rows, ctypes.byref(chunks), table.data_ptr(),
+                                   size.value, stream) == 0
+    assert L.lib.moe_adamw_state_values(ctypes.byref(desc), chunks.value, table.data_ptr(), stream) == 0
+    torch.cuda.synchronize()
+    for i, n in enumerate(sizes):
+        for got, c, s, top, power in ((values[0][i], m[i], scales[0][i], 127.0, 2),
+                                      (values[1][i], v[i], scales[1][i], 255.0, 4)):
+            if not has[i]:
+                assert (got == 9.0).all(), i
+                continue
+            c = c.cpu().double()
+            want = torch.sign(c) * (c.abs() / top) ** power * s.cpu().double().repeat_interleave(256)[:n]
+            # 64 bits inside, rounded once
+            within(got[:n], want, 1.01 * 2.0 ** -24 * want.abs() + 1e-45, i)
+            assert (got[n:] == 9.0).all(), i
+    for t, old in zip((m, v, scales[0], scales[1], p), before):
+        assert all(torch.equal(a, b) for a, b in zip(t, old))
