@@ -763,7 +763,9 @@ def gated_ff(x, w_gate, w_up, h, offsets=None, pre=None, ws=None):
     """moe_gated_ff: h [M, F] = silu(x W_gate^T) * (x W_up^T) for x [M, d] and
     matrices [E, F, d], all fp32 or all bf16.  ``offsets`` int32 [E+1] gives each
     group's rows; without it E must be 1.  ``pre`` fp32 [M, 2F] takes the two
-    products for gated_ff_backward."""
+    products for gated_ff_backward.  Like every call here it writes its outputs without
+    torch's autograd: no graph is made of it and no version counter raised (inside a
+    torch.autograd.Function it stands beside gated_ff_backward)."""
     dev, desc, args = _gated_args("gated_ff", x, w_gate, w_up)
     M, F, E = desc.M, desc.F, desc.E
     if ws is None:
@@ -964,7 +966,8 @@ def adamw_step(plan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
     may be an int64 tensor of one value on the GPU and ``lr`` an fp32 one, read when
     the kernel runs (a captured graph then follows them); ``grad_scale``, an fp32
     tensor of one value, multiplies every gradient, and where it is NaN or infinite
-    the step changes nothing."""
+    the step changes nothing.  Parameters change without torch's version counters: a
+    backward pass that needs the old ones goes first."""
     a = AdamwStep(0.0, beta1, beta2, eps, weight_decay, 0)
     for name, v, dt in (("lr", lr, torch.float32), ("step", step, torch.int64),
                         ("grad_scale", grad_scale, torch.float32)):

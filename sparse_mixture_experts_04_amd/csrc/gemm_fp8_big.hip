@@ -567,6 +567,21 @@ double fp8_tiles_time(int M, int N, int Kp, int E) {
   return (splits_of(M, N, Kp, E, time) > 1 ? 12.0 : 6.5) + time;
 }
 
+// Whether a bf16 y takes the 256-row tiles: groups that fill one to 5/8, and as many
+// values of y as 192 tiles have, for with fewer the 128-row tiles keep more compute
+// units busy.  Measured (us, 256 / 128 rows):
+//   16384 x 7168 by 2048   184 / 227      8192 x 2048 by 1024    32 / 23
+//   8192 x 7168 by 2048    104 / 117      4096 x 7168 by 2048    95 / 62
+//   8192 x 2048 by 2048    39 / 41.5      3500 x 4096 by 3500    66 / 70
+//   2048 x 2048 by 7168    36.4 / 38      3000 x 4096 by 3000    55 / 61
+//   24576 x 768 by 2048, 128 groups  98 / 104    24576 x 2048 by 768, 256 groups  120 / 110
+//   24576 x 2048 by 768, 128 groups  78 / 79     the same, 64 groups  63 / 56
+// (3500, 3000 rows and 64 groups are 6, 10 and 13% off the better kernel: there the
+// rounds of tiles decide, which the rule does not count)
+static bool large_tiles(const Fp8Args& a) {
+  return a.M / a.E >= 160 && static_cast<long long>(a.M) * a.N >= 192LL * 256 * 256;
+}
+
 hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st) {
   const int grid = (device_cus_big() + kXcds - 1) / kXcds * kXcds;
   auto go = [&](auto kernel) { kernel<<<grid, MidF8::THREADS, 0, st>>>(a); };
@@ -581,7 +596,7 @@ hipError_t launch_gemm_fp8_big(const Fp8Args& a, hipStream_t st) {
     else gemm_fp8_reduce_kernel<false><<<g, 256, 0, st>>>(a);
   } else if (!a.out_bf16) {
     go(gemm_fp8_big_kernel<MidF8, false, false>);
-  } else if (a.M / a.E >= 160 && static_cast<long long>(a.M) * a.N >= 6291456LL * 2) {
+  } else if (large_tiles(a)) {
     go(gemm_fp8_big_kernel<BigF8, true, true>);
   } else {
     go(gemm_fp8_big_kernel<MidF8, true, true>);
