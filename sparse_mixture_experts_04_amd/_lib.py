@@ -924,7 +924,10 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, copies=None, m_scales=None, v
     if count == 0:
         raise ValueError("adamw_plan: no params")
     dev = _on_gpu(lists["params"][0], "params[0]")
-    if torch.cuda.is_current_stream_capturing():
+    capturing = torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(dev):  # (the stream that the table would be written on)
+        capturing = capturing or torch.cuda.is_current_stream_capturing()
+    if capturing:
         raise RuntimeError("adamw_plan: make the plan before the capture that uses it")
     pt, gt = lists["params"][0].dtype, getattr(lists["grads"][0], "dtype", None)
     bits8 = getattr(lists["exp_avg"][0], "dtype", None) is torch.int8

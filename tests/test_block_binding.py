@@ -121,3 +121,36 @@ def test_steps_of_more_than_64_bits_are_refused(host):
         with pytest.raises(ValueError):
             L.adamw_step(plan(), step, lr=1e-3)
     assert not host["calls"]
+
+
+@pytest.mark.parametrize("current,captured,refused", [(0, 1, True), (0, 0, True), (0, None, False),
+                                                      (1, 1, True), (1, None, False)])
+def test_no_plan_where_either_gpus_stream_is_captured(monkeypatch, host, current, captured, refused):
+    """Of the current GPU or of the tensors' own (cuda:1 here): the table's kernels would
+    go into the capture, and the wait behind them would end it."""
+    at = [current]
+
+    @contextlib.contextmanager
+    def device(idx):
+        before, at[0] = at[0], idx
+        yield
+        at[0] = before
+
+    class Stream:
+        def synchronize(self):
+            host["calls"].append("wait")
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at[0] == captured)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(L, "_on_gpu", lambda x, name: 1)
+    monkeypatch.setattr(L, "_at", lambda *a: 0x1000)
+    x = torch.zeros(4)
+    if refused:
+        with pytest.raises(RuntimeError, match="before the capture"):
+            L.adamw_plan([x], [x], [x], [x])
+        assert host["calls"] == []
+    else:
+        assert L.adamw_plan([x], [x], [x], [x]).device == 1
+        assert host["calls"][-1] == "wait"
+    assert at[0] == current
