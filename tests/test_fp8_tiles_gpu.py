@@ -3,7 +3,7 @@ and cut along K) and the 256-row ones, where values or sums are out of the ordin
 import pytest
 import torch
 
-from block_util import fp8_product64, rand, within
+from block_util import fp8_product64, rand, spans, within
 
 pytestmark = pytest.mark.gpu
 BF, F32, FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
@@ -267,3 +267,20 @@ def test_two_sliced_products_at_once():
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,N,K,offsets", [
+    (1477, 587, 42, [0, 192, 381, 621, 914, 974, 1048, 1257, 1289, 1477]), (1500, 2100, 8, None),
+    (1500, 2100, 1, None), (5000, 3000, 42, [0, 1000, 1000, 2600, 4990])])
+def test_short_rows(M, N, K, offsets):
+    """K of a few products, each a large part of its sum: the instruction's loss shows
+    beside the rounding of a bf16 y."""
+    E = 1 if offsets is None else len(offsets) - 1
+    a, sa, w, sw = operands(M, N, K, E, seed=K)
+    want, bound, covered = fp8_product64(a, sa, w, sw, offsets, BF)
+    for e, (lo, hi) in enumerate(spans(offsets, M, E)):
+        if hi > lo:
+            bound[lo:hi] += (1 + 2.0 ** -8) * instruction_loss(a[lo:hi], sa[lo:hi], w[e:e + 1], sw[e:e + 1])
+    within(product(a, sa, w, sw, BF, offsets)[covered.cuda()], want[covered], bound[covered], "bf16 y")
+    want, bound, covered = fp8_product64(a, sa, w, sw, offsets, F32)
+    within(product(a, sa, w, sw, F32, offsets)[covered.cuda()], want[covered], bound[covered], "fp32 y")
